@@ -13,6 +13,12 @@ missing or fails to load, every call raises.
     nvfp4_paged_ctx_attn(q_fp8, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens,
                          *, q_scale=1.0, out_scale=1.0, out=None)
     gqa_debug_dequant_pages(fp4, sf, block_table, kv_lens, max_kv)
+    gqa_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, *, qo_indptr=None, rope=None,
+                     interleaved=False, k_scale=1.0, v_scale=1.0, q_out=None)
+    nvfp4_paged_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, *, rope=None,
+                       interleaved=False, q_scale=1.0, q_out=None)
+    gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=None, q_scale=1.0,
+                   k_scale=1.0, v_scale=1.0, window=0, softcap=0.0, workspace=None)
 """
 from __future__ import annotations
 
@@ -25,7 +31,7 @@ import torch
 __all__ = [
     "GqaError", "lib", "gqa_decode", "nvfp4_paged_ctx_attn", "gqa_debug_dequant_pages",
     "gqa_check_device_errors", "gqa_release_workspace", "gqa_decode_plan", "gqa_ctx_plan", "gqa_decode_paged", "gqa_debug_wait_expiry", "gqa_decode_noalloc", "gqa_debug_starve_producers", "gqa_set_schedule", "gqa_set_ctx_grid", "LIB_PATH",
-    "build",
+    "build", "gqa_paged_append", "nvfp4_paged_append", "gqa_paged_attn", "gqa_paged_attn_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,7 +48,8 @@ class GqaTensor(ctypes.Structure):
                 ("ndim", ctypes.c_int32), ("shape", ctypes.c_int64 * 6), ("strides", ctypes.c_int64 * 6)]
 
 
-_DTYPES = {torch.float16: 1, torch.float8_e4m3fn: 2, torch.uint8: 3, torch.int32: 4, torch.float32: 5}
+_DTYPES = {torch.float16: 1, torch.float8_e4m3fn: 2, torch.uint8: 3, torch.int32: 4, torch.float32: 5,
+           torch.bfloat16: 6}
 
 
 def _desc(t: torch.Tensor, name: str) -> GqaTensor:
@@ -125,6 +132,14 @@ def lib() -> ctypes.CDLL:
             L.gqa_set_schedule.restype = c.c_int
             L.gqa_set_ctx_grid.argtypes = [c.c_int]
             L.gqa_set_ctx_grid.restype = c.c_int
+            L.gqa_paged_append_t.argtypes = [tp] * 10 + [c.c_int, f32, f32, vp]
+            L.gqa_paged_append_t.restype = c.c_int
+            L.nvfp4_paged_append_t.argtypes = [tp] * 12 + [c.c_int, f32, vp]
+            L.nvfp4_paged_append_t.restype = c.c_int
+            L.gqa_paged_attn_t.argtypes = [tp] * 7 + [f32, f32, f32, c.c_int, f32, vp, i64, vp]
+            L.gqa_paged_attn_t.restype = c.c_int
+            L.gqa_paged_attn_workspace.argtypes = [i64, i64, i64]
+            L.gqa_paged_attn_workspace.restype = i64
             L.gqa_release_workspace.argtypes = []
             L.gqa_release_workspace.restype = c.c_int
             _lib = L
@@ -225,6 +240,74 @@ def nvfp4_paged_ctx_attn(q_fp8, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr
                                    (kv_lens, "kv_lens"), (out, "out_fp8"))]
     r = list(map(_ref, ds))
     _check(lib().nvfp4_paged_ctx_attn_t(r[0], float(q_scale), *r[1:9], float(out_scale), _stream_for(q_fp8)))
+    return out
+
+
+def _opt(t, name: str):
+    """Reference to a descriptor, or NULL for None."""
+    return None if t is None else _ref(_desc(t, name))
+
+
+def gqa_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, *, qo_indptr=None, rope=None,
+                     interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0, q_out=None):
+    """Rotate new q and k rows to their positions and append k and v to a
+    paged cache (see include/gqa.h).
+
+    q [T,Hq,D] (or None), k, v [T,Hkv,D] f16 or bf16; k_pages, v_pages
+    [num_pages,Hkv,page_size,D] of the same type or E4M3, in any order in
+    memory; block_table [B,max_pages_per_seq], kv_lens [B] (the new tokens
+    included) and qo_indptr [B+1] int32 (None: one token per sequence); rope
+    [positions,rot] f32, cosines then sines (None: no rotation).  Returns the
+    rotated queries (q_out, which may be q itself; None without q).
+    """
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    _check(lib().gqa_paged_append_t(
+        _opt(q, "q"), _opt(k, "k"), _opt(v, "v"), _opt(k_pages, "k_pages"), _opt(v_pages, "v_pages"),
+        _opt(block_table, "block_table"), _opt(kv_lens, "kv_lens"), _opt(qo_indptr, "qo_indptr"), _opt(rope, "rope"),
+        _opt(q_out, "q_out"), 1 if interleaved else 0, float(k_scale), float(v_scale), _stream_for(k)))
+    return q_out
+
+
+def nvfp4_paged_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, *, rope=None,
+                       interleaved: bool = False, q_scale: float = 1.0, q_out=None):
+    """gqa_paged_append into the NVFP4 pages that nvfp4_paged_ctx_attn reads
+    (see include/gqa.h): k and v quantised to E2M1 codes with one E4M3 scale
+    per 16 elements.  Returns the rotated queries / q_scale as uint8 E4M3
+    codes (or writes `q_out`; None without q)."""
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.uint8, device=q.device)
+    _check(lib().nvfp4_paged_append_t(
+        _opt(q, "q"), _opt(k, "k"), _opt(v, "v"), _opt(k_fp4, "k_fp4"), _opt(k_sf, "k_sf"), _opt(v_fp4, "v_fp4"),
+        _opt(v_sf, "v_sf"), _opt(block_table, "block_table"), _opt(qo_indptr, "qo_indptr"), _opt(kv_lens, "kv_lens"),
+        _opt(rope, "rope"), _opt(q_out, "q_out"), 1 if interleaved else 0, float(q_scale), _stream_for(k)))
+    return q_out
+
+
+def gqa_paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace of a gqa_paged_attn call, whatever its batch and lengths."""
+    return int(lib().gqa_paged_attn_workspace(int(q_heads), int(kv_heads), int(head_dim)))
+
+
+def gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=None, q_scale: float = 1.0,
+                   k_scale: float = 1.0, v_scale: float = 1.0, window: int = 0, softcap: float = 0.0, workspace=None):
+    """Attention of one new token per sequence over a paged cache (see
+    include/gqa.h): q [B,Hq,D] f16 or bf16, k_pages / v_pages
+    [num_pages,Hkv,page_size,D] of q's type or E4M3, in any order in memory,
+    block_table [B,max_pages_per_seq] and seq_lens [B] int32.  Writes `lse`
+    [B,Hq] f32 if given.  The workspace is allocated for the call unless one
+    of at least gqa_paged_attn_workspace(Hq, Hkv, D) bytes (uint8) is given;
+    calls that can run at the same time need one each."""
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if workspace is None and q.is_cuda and q.dim() == 3 and k_pages.dim() == 4:
+        workspace = torch.empty(gqa_paged_attn_workspace(q.shape[1], k_pages.shape[1], q.shape[2]), dtype=torch.uint8,
+                                device=q.device)
+    ws, n = (_p(workspace), workspace.numel()) if workspace is not None else (None, 1 << 62)
+    _check(lib().gqa_paged_attn_t(
+        _opt(q, "q"), _opt(k_pages, "k_pages"), _opt(v_pages, "v_pages"), _opt(block_table, "block_table"),
+        _opt(seq_lens, "seq_lens"), _opt(out, "out"), _opt(lse, "lse"), float(q_scale), float(k_scale), float(v_scale),
+        int(window), float(softcap), ws, n, _stream_for(q)))
     return out
 
 

@@ -23,7 +23,8 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgqa.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
-SOURCES = ["api.cpp", "decode.cu", "ctx_nvfp4.cu", "ctx_study.cu"]
+SOURCES = ["api.cpp", "decode.cu", "ctx_nvfp4.cu", "ctx_study.cu", "append.cu", "paged_attn.cpp", "paged_attn_f16.cu",
+           "paged_attn_bf16.cu", "paged_attn_e4m3.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I", CSRC, "-I", INCLUDE]

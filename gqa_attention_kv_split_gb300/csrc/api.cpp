@@ -190,6 +190,7 @@ const char* dtype_name(int32_t d) {
     case GQA_U8: return "u8";
     case GQA_I32: return "i32";
     case GQA_F32: return "f32";
+    case GQA_BF16: return "bf16";
     default: return "unknown";
   }
 }
@@ -265,7 +266,7 @@ extern "C" {
 
 const char* gqa_last_error(void) { return t_last_error.c_str(); }
 
-int gqa_version(void) { return 302; }  // 0.3.2: decode-shaped context kernel, gqa_ctx_plan(decode_shaped)
+int gqa_version(void) { return 400; }  // 0.4.0: gqa_paged_append_t, nvfp4_paged_append_t, gqa_paged_attn_t
 
 namespace {
 gqa_status decode_impl(const void* q, const void* kv, const int32_t* seq_lens, void* out, int64_t batch,
@@ -656,11 +657,13 @@ gqa_status gqa_check_device_errors(int device, uint32_t* word) {
   *word = 0;
   ScopedDevice sd(device);
   if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", device);
-  uint32_t a = 0, b = 0, c = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0, f = 0;
   GQA_CUDA_TRY(gqa::decode_read_errors(&a), "read decode error word");
   GQA_CUDA_TRY(gqa::ctx_read_errors(&b), "read ctx error word");
   GQA_CUDA_TRY(gqa::ctx_study_read_errors(&c), "read ctx study error word");
-  *word = a | b | c;
+  GQA_CUDA_TRY(gqa::append_read_errors(&d), "read append error word");
+  GQA_CUDA_TRY(gqa::paged_attn_read_errors(&f), "read paged attention error word");
+  *word = a | b | c | d | f;
   if (*word & 1u) return fail(GQA_ERR_TIMEOUT, "a kernel's bounded wait expired (error word 0x%x)", *word);
   if (*word)
     return fail(GQA_ERR_INVALID_ARG,
@@ -723,6 +726,323 @@ gqa_status nvfp4_paged_ctx_attn_t(const gqa_tensor* q_fp8, float q_scale, const 
                   static_cast<const int32_t*>(block_table->data), static_cast<const int32_t*>(qo_indptr->data),
                   static_cast<const int32_t*>(kv_lens->data), out_fp8->data, out_scale, ls[0], qs[0], ps[0], bs[1],
                   stream, q_fp8->device);
+}
+
+// ---- paged cache of any layout: append, one-token attention -------------------
+
+namespace {
+
+int64_t dtype_bytes(int32_t d) {
+  return d == GQA_F16 || d == GQA_BF16 ? 2 : d == GQA_E4M3 || d == GQA_U8 ? 1 : 4;
+}
+
+// Structural check of a tensor that may be strided: as check_desc, but the last
+// dimension alone has to be dense and the other strides are multiples of 16 bytes;
+// one that is written must not overlap itself.  An empty tensor may have no data.
+gqa_status check_strided(const gqa_tensor* t, const char* name, std::initializer_list<int32_t> dtypes,
+                         std::initializer_list<int64_t> shape, bool written, int64_t* got = nullptr) {
+  if (!t) return fail(GQA_ERR_INVALID_ARG, "%s: null descriptor", name);
+  gqa_tensor dense = *t;  // the checks that do not depend on the strides
+  int64_t n = 1;
+  if (t->ndim >= 0 && t->ndim <= 6)
+    for (int d = t->ndim - 1; d >= 0; --d) {
+      dense.strides[d] = n;
+      if (t->shape[d] >= 0 && t->shape[d] <= (int64_t(1) << 40) && n <= (int64_t(1) << 40)) n *= t->shape[d];
+    }
+  if (!dense.data && n == 0) dense.data = &dense;
+  GQA_TRY(check_desc(&dense, name, dtypes, shape, got));
+  const int64_t esz = dtype_bytes(t->dtype);
+  const int nd = t->ndim;
+  if (t->shape[nd - 1] > 1 && t->strides[nd - 1] != 1)
+    return fail(GQA_ERR_INVALID_ARG, "%s: the last dimension is not dense (stride %lld)", name, (long long)t->strides[nd - 1]);
+  for (int d = 0; d < nd - 1; ++d) {
+    if (t->shape[d] <= 1) continue;
+    if (t->strides[d] < 0 || t->strides[d] * esz % 16 != 0 || t->strides[d] > (int64_t(1) << 38))
+      return fail(GQA_ERR_INVALID_ARG, "%s: stride %lld in dimension %d is not a multiple of 16 bytes in [0, 2^38]", name,
+                  (long long)t->strides[d], d);
+  }
+  if (!written) return GQA_OK;
+  // Dimensions from the smallest stride up: each steps over all that the smaller ones cover.
+  int64_t covered = t->shape[nd - 1];
+  bool used[6] = {};
+  for (int k = 0; k < nd - 1; ++k) {
+    int at = -1;
+    for (int d = 0; d < nd - 1; ++d)
+      if (!used[d] && t->shape[d] > 1 && (at < 0 || t->strides[d] < t->strides[at])) at = d;
+    if (at < 0) break;
+    used[at] = true;
+    if (t->strides[at] < covered)
+      return fail(GQA_ERR_INVALID_ARG, "%s overlaps itself (stride %lld in dimension %d)", name, (long long)t->strides[at], at);
+    covered += t->strides[at] * (t->shape[at] - 1);
+  }
+  return GQA_OK;
+}
+
+// Stride of a dimension; 0 where its extent is 1 (nothing is ever added for it).
+int64_t stride_of(const gqa_tensor* t, int d) { return t->shape[d] > 1 ? t->strides[d] : 0; }
+
+gqa_status check_scale(float s, const char* name) {
+  if (!std::isfinite(s) || !(s > 0.f) || !std::isfinite(1.f / s))
+    return fail(GQA_ERR_INVALID_ARG, "%s must be finite and > 0", name);
+  return GQA_OK;
+}
+
+using Named = std::pair<const gqa_tensor*, const char*>;
+
+// What the two appends share: q, k, v, q_out, the metadata and the rope table; fills
+// in everything but the pages.  Null q, q_out, indptr and rope are left out.
+gqa_status append_common(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, const gqa_tensor* block_table,
+                         const gqa_tensor* kv_lens, const gqa_tensor* indptr, const gqa_tensor* rope, const gqa_tensor* q_out,
+                         std::initializer_list<int32_t> out_dtypes, int64_t hq, int64_t hkv, int64_t dim, int rot_step,
+                         int interleaved, gqa::AppendArgs* a, std::vector<Named>* ts) {
+  int64_t ks[3], qs[3], ls[1], bs[2], rs[2];
+  GQA_TRY(check_strided(k, "k", {GQA_F16, GQA_BF16}, {-1, hkv, dim}, false, ks));
+  GQA_TRY(check_strided(v, "v", {k->dtype}, {ks[0], ks[1], ks[2]}, false));
+  if (ks[2] != 64 && ks[2] != 128 && ks[2] != 256)
+    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "head dim %lld is not 64, 128 or 256", (long long)ks[2]);
+  if (ks[1] < 1 || ks[1] > 1024) return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld KV heads: 1 to 1024 are taken", (long long)ks[1]);
+  if (ks[0] > 2147483647LL) return fail(GQA_ERR_INVALID_ARG, "total %lld out of range", (long long)ks[0]);
+  if ((q == nullptr) != (q_out == nullptr)) return fail(GQA_ERR_INVALID_ARG, "q and q_out go together: one of them is NULL");
+  *ts = {{k, "k"}, {v, "v"}, {block_table, "block_table"}, {kv_lens, "kv_lens"}};
+  if (q) {
+    GQA_TRY(check_strided(q, "q", {k->dtype}, {ks[0], hq, ks[2]}, false, qs));
+    if (qs[1] < 1 || qs[1] > 1024) return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld query heads: 1 to 1024 are taken", (long long)qs[1]);
+    GQA_TRY(check_strided(q_out, "q_out", out_dtypes, {ks[0], qs[1], ks[2]}, true));
+    if (q_out->data == q->data && q_out->dtype == q->dtype)
+      for (int d = 0; d < 2; ++d)
+        if (stride_of(q, d) != stride_of(q_out, d))
+          return fail(GQA_ERR_INVALID_ARG, "q_out may be q itself, with q's strides");
+    ts->push_back({q, "q"});
+    ts->push_back({q_out, "q_out"});
+  }
+  GQA_TRY(check_desc(kv_lens, "kv_lens", {GQA_I32}, {-1}, ls));
+  if (ls[0] < 1 || ls[0] > (1 << 20)) return fail(GQA_ERR_UNSUPPORTED, "batch %lld outside [1, 2^20]", (long long)ls[0]);
+  GQA_TRY(check_desc(block_table, "block_table", {GQA_I32}, {ls[0], -1}, bs));
+  if (indptr) {
+    GQA_TRY(check_desc(indptr, "qo_indptr", {GQA_I32}, {ls[0] + 1}));
+    ts->push_back({indptr, "qo_indptr"});
+  } else if (ks[0] != ls[0]) {
+    return fail(GQA_ERR_INVALID_ARG, "without qo_indptr there is one token per sequence: %lld tokens, %lld sequences",
+                (long long)ks[0], (long long)ls[0]);
+  }
+  *a = gqa::AppendArgs{};
+  if (rope) {
+    GQA_TRY(check_desc(rope, "rope", {GQA_F32}, {-1, -1}, rs));
+    if (rs[1] < rot_step || rs[1] > ks[2] || rs[1] % rot_step != 0)
+      return fail(GQA_ERR_UNSUPPORTED_SHAPE, "rope has %lld columns; a multiple of %d up to the head dim is wanted",
+                  (long long)rs[1], rot_step);
+    a->rope = static_cast<const float*>(rope->data);
+    a->rope_len = rs[0];
+    a->rot = (int)rs[1];
+    ts->push_back({rope, "rope"});
+  }
+  a->interleaved = interleaved ? 1 : 0;
+  a->k = k->data;
+  a->v = v->data;
+  a->block_table = static_cast<const int32_t*>(block_table->data);
+  a->kv_lens = static_cast<const int32_t*>(kv_lens->data);
+  a->indptr = indptr ? static_cast<const int32_t*>(indptr->data) : nullptr;
+  a->k_tok = stride_of(k, 0);
+  a->k_head = stride_of(k, 1);
+  a->v_tok = stride_of(v, 0);
+  a->v_head = stride_of(v, 1);
+  if (q) {
+    a->q = q->data;
+    a->q_out = q_out->data;
+    a->q_tok = stride_of(q, 0);
+    a->q_head = stride_of(q, 1);
+    a->qo_tok = stride_of(q_out, 0);
+    a->qo_head = stride_of(q_out, 1);
+    a->hq = (int)qs[1];
+  }
+  a->hkv = (int)ks[1];
+  a->d = (int)ks[2];
+  a->total = ks[0];
+  a->batch = ls[0];
+  a->max_pages_per_seq = bs[1];
+  a->bf16 = k->dtype == GQA_BF16;
+  a->inv_k = a->inv_v = a->inv_q = 1.f;
+  return GQA_OK;
+}
+
+// All tensors on one device, where their descriptors say, 16-byte aligned (int32 ones
+// 4-byte); host memory is refused.
+gqa_status locate_tensors(const std::vector<Named>& ts, const char* op, Where* where) {
+  std::vector<Arg> args;
+  for (const Named& t : ts) {
+    if (t.first->device != ts[0].first->device)
+      return fail(GQA_ERR_DEVICE_MISMATCH, "%s is on device %d but %s is on device %d", t.second, t.first->device, ts[0].second,
+                  ts[0].first->device);
+    args.push_back({t.first->data, t.second, t.first->dtype == GQA_I32 ? size_t(4) : size_t(16)});
+  }
+  if (ts[0].first->device < 0) return fail(GQA_ERR_UNSUPPORTED, "%s takes device tensors only", op);
+  GQA_TRY(locate(args, where, ts[0].first->device));
+  return GQA_OK;
+}
+
+gqa_status run_append(const gqa::AppendArgs& a, const std::vector<Named>& ts, const char* op, gqa_stream_t stream) {
+  if (a.total == 0) return GQA_OK;
+  if (a.num_pages < 1 || a.num_pages > 2147483647LL) return fail(GQA_ERR_INVALID_ARG, "num_pages %lld out of range", (long long)a.num_pages);
+  if (a.max_pages_per_seq < 1) return fail(GQA_ERR_INVALID_ARG, "block_table has no column");
+  if (a.rope && a.rope_len < 1) return fail(GQA_ERR_INVALID_ARG, "rope has no row");
+  Where where;
+  GQA_TRY(locate_tensors(ts, op, &where));
+  ScopedDevice sd(where.device);
+  if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", where.device);
+  GQA_CUDA_TRY(gqa::launch_append(a, reinterpret_cast<cudaStream_t>(stream)), "append launch");
+  return GQA_OK;
+}
+
+}  // namespace
+
+gqa_status gqa_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, gqa_tensor* k_pages,
+                              gqa_tensor* v_pages, const gqa_tensor* block_table, const gqa_tensor* kv_lens,
+                              const gqa_tensor* qo_indptr, const gqa_tensor* rope, gqa_tensor* q_out, int interleaved,
+                              float k_scale, float v_scale, gqa_stream_t stream) {
+  gqa::AppendArgs a;
+  std::vector<Named> ts;
+  if (!k) return fail(GQA_ERR_INVALID_ARG, "k: null descriptor");
+  GQA_TRY(append_common(q, k, v, block_table, kv_lens, qo_indptr, rope, q_out, {k->dtype}, -1, -1, -1, 16, interleaved, &a, &ts));
+  int64_t ps[4];
+  GQA_TRY(check_strided(k_pages, "k_pages", {k->dtype, GQA_E4M3, GQA_U8}, {-1, a.hkv, -1, a.d}, true, ps));
+  const bool e4m3 = k_pages->dtype != k->dtype;
+  GQA_TRY(e4m3 ? check_strided(v_pages, "v_pages", {GQA_E4M3, GQA_U8}, {ps[0], a.hkv, ps[2], a.d}, true)
+               : check_strided(v_pages, "v_pages", {k->dtype}, {ps[0], a.hkv, ps[2], a.d}, true));
+  if (a.total > 0 && (ps[2] < 1 || ps[2] > (1 << 20)))
+    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "page size %lld outside [1, 2^20]", (long long)ps[2]);
+  GQA_TRY(check_scale(k_scale, "k_scale"));
+  GQA_TRY(check_scale(v_scale, "v_scale"));
+  if (!e4m3 && (k_scale != 1.f || v_scale != 1.f))
+    return fail(GQA_ERR_INVALID_ARG, "k_scale and v_scale belong to E4M3 pages: 1 is wanted");
+  a.mode = e4m3 ? gqa::kAppendE4m3 : gqa::kAppendSame;
+  a.inv_k = 1.f / k_scale;
+  a.inv_v = 1.f / v_scale;
+  a.k_pages = k_pages->data;
+  a.v_pages = v_pages->data;
+  a.kp_page = stride_of(k_pages, 0);
+  a.kp_head = stride_of(k_pages, 1);
+  a.kp_slot = stride_of(k_pages, 2);
+  a.vp_page = stride_of(v_pages, 0);
+  a.vp_head = stride_of(v_pages, 1);
+  a.vp_slot = stride_of(v_pages, 2);
+  a.num_pages = ps[0];
+  a.page_size = (int)ps[2];
+  ts.push_back({k_pages, "k_pages"});
+  ts.push_back({v_pages, "v_pages"});
+  return run_append(a, ts, "gqa_paged_append", stream);
+}
+
+gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, gqa_tensor* k_fp4,
+                                gqa_tensor* k_sf, gqa_tensor* v_fp4, gqa_tensor* v_sf, const gqa_tensor* block_table,
+                                const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens, const gqa_tensor* rope,
+                                gqa_tensor* q_out, int interleaved, float q_scale, gqa_stream_t stream) {
+  gqa::AppendArgs a;
+  std::vector<Named> ts;
+  if (!k) return fail(GQA_ERR_INVALID_ARG, "k: null descriptor");
+  GQA_TRY(append_common(q, k, v, block_table, kv_lens, qo_indptr, rope, q_out, {GQA_E4M3, GQA_U8}, 32, 8, 128, 32, interleaved, &a,
+                        &ts));
+  int64_t ps[4];
+  GQA_TRY(check_desc(k_fp4, "k_fp4", {GQA_U8}, {-1, 8, 64, 64}, ps));
+  GQA_TRY(check_desc(k_sf, "k_sf", {GQA_E4M3, GQA_U8}, {ps[0], 8, 64, 8}));
+  GQA_TRY(check_desc(v_fp4, "v_fp4", {GQA_U8}, {ps[0], 8, 64, 64}));
+  GQA_TRY(check_desc(v_sf, "v_sf", {GQA_E4M3, GQA_U8}, {ps[0], 8, 64, 8}));
+  GQA_TRY(check_scale(q_scale, "q_scale"));
+  a.mode = gqa::kAppendNvfp4;
+  a.inv_q = 1.f / q_scale;
+  a.k_pages = k_fp4->data;
+  a.v_pages = v_fp4->data;
+  a.k_sf = static_cast<uint8_t*>(k_sf->data);
+  a.v_sf = static_cast<uint8_t*>(v_sf->data);
+  a.num_pages = ps[0];
+  a.page_size = 64;
+  for (const Named& t : {Named{k_fp4, "k_fp4"}, Named{k_sf, "k_sf"}, Named{v_fp4, "v_fp4"}, Named{v_sf, "v_sf"}}) ts.push_back(t);
+  return run_append(a, ts, "nvfp4_paged_append", stream);
+}
+
+int64_t gqa_paged_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t d) {
+  if (kv_heads < 1 || q_heads < 1 || q_heads > 1024 || q_heads % kv_heads != 0 || (d != 64 && d != 128 && d != 256)) return 0;
+  return (int64_t)gqa::paged_attn_workspace_bytes((int)q_heads, (int)kv_heads, (int)d);
+}
+
+gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, const gqa_tensor* v_pages,
+                            const gqa_tensor* block_table, const gqa_tensor* seq_lens, gqa_tensor* out, gqa_tensor* lse,
+                            float q_scale, float k_scale, float v_scale, int window, float softcap, void* workspace_,
+                            int64_t workspace_bytes, gqa_stream_t stream) {
+  int64_t qs[3], ps[4], bs[2];
+  GQA_TRY(check_strided(q, "q", {GQA_F16, GQA_BF16}, {-1, -1, -1}, false, qs));
+  GQA_TRY(check_strided(k_pages, "k_pages", {q->dtype, GQA_E4M3, GQA_U8}, {-1, -1, -1, qs[2]}, true, ps));
+  const bool e4m3 = k_pages->dtype != q->dtype;
+  GQA_TRY(e4m3 ? check_strided(v_pages, "v_pages", {GQA_E4M3, GQA_U8}, {ps[0], ps[1], ps[2], qs[2]}, true)
+               : check_strided(v_pages, "v_pages", {q->dtype}, {ps[0], ps[1], ps[2], qs[2]}, true));
+  GQA_TRY(check_desc(seq_lens, "seq_lens", {GQA_I32}, {qs[0]}));
+  GQA_TRY(check_desc(block_table, "block_table", {GQA_I32}, {qs[0], -1}, bs));
+  GQA_TRY(check_desc(out, "out", {q->dtype}, {qs[0], qs[1], qs[2]}));
+  if (lse) GQA_TRY(check_desc(lse, "lse", {GQA_F32}, {qs[0], qs[1]}));
+  if (qs[0] < 1 || qs[0] > 65535) return fail(GQA_ERR_UNSUPPORTED, "batch %lld outside [1, 65535]", (long long)qs[0]);
+  if (qs[2] != 64 && qs[2] != 128 && qs[2] != 256)
+    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "head dim %lld is not 64, 128 or 256", (long long)qs[2]);
+  if (ps[1] < 1 || qs[1] < 1 || qs[1] > 1024 || qs[1] % ps[1] != 0)
+    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld query heads over %lld KV heads: 1 to 1024, a multiple, are taken",
+                (long long)qs[1], (long long)ps[1]);
+  if (ps[2] != 16 && ps[2] != 32 && ps[2] != 64 && ps[2] != 128 && ps[2] != 256)
+    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "page size %lld is not 16, 32, 64, 128 or 256", (long long)ps[2]);
+  if (ps[0] < 1 || ps[0] > 2147483647LL) return fail(GQA_ERR_INVALID_ARG, "num_pages %lld out of range", (long long)ps[0]);
+  if (bs[1] < 1 || bs[1] > (int64_t(1) << 30) / ps[2])
+    return fail(GQA_ERR_INVALID_ARG, "max_pages_per_seq %lld out of range", (long long)bs[1]);
+  if (!std::isfinite(q_scale)) return fail(GQA_ERR_INVALID_ARG, "q_scale is not finite");
+  GQA_TRY(check_scale(k_scale, "k_scale"));
+  GQA_TRY(check_scale(v_scale, "v_scale"));
+  if (window < 0) return fail(GQA_ERR_INVALID_ARG, "window %d is negative", window);
+  if (!std::isfinite(softcap) || softcap < 0.f) return fail(GQA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  const int64_t need = gqa_paged_attn_workspace(qs[1], ps[1], qs[2]);
+  if (workspace_bytes < need)
+    return fail(GQA_ERR_INVALID_ARG, "workspace of %lld bytes; %lld are needed", (long long)workspace_bytes, (long long)need);
+  gqa_tensor ws = *q;  // the workspace's place is checked with the tensors'
+  ws.data = workspace_;
+  std::vector<Named> ts = {{q, "q"}, {k_pages, "k_pages"}, {v_pages, "v_pages"}, {block_table, "block_table"},
+                           {seq_lens, "seq_lens"}, {out, "out"}, {&ws, "workspace"}};
+  gqa_tensor l;
+  if (lse) {
+    l = *lse;
+    l.dtype = GQA_I32;  // (4-byte alignment)
+    ts.push_back({&l, "lse"});
+  }
+  Where where;
+  GQA_TRY(locate_tensors(ts, "gqa_paged_attn", &where));
+  gqa::PagedAttnArgs a{};
+  a.q = q->data;
+  a.out = out->data;
+  a.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+  a.k_pages = k_pages->data;
+  a.v_pages = v_pages->data;
+  a.block_table = static_cast<const int32_t*>(block_table->data);
+  a.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  a.q_seq = stride_of(q, 0);
+  a.q_head = stride_of(q, 1);
+  a.kp_page = k_pages->strides[0];
+  a.kp_head = k_pages->strides[1];
+  a.kp_slot = k_pages->strides[2];
+  a.vp_page = v_pages->strides[0];
+  a.vp_head = v_pages->strides[1];
+  a.vp_slot = v_pages->strides[2];
+  a.batch = qs[0];
+  a.num_pages = ps[0];
+  a.max_pages_per_seq = bs[1];
+  a.hq = (int)qs[1];
+  a.hkv = (int)ps[1];
+  a.d = (int)qs[2];
+  a.page_size = (int)ps[2];
+  a.q_bf16 = q->dtype == GQA_BF16;
+  a.cache = e4m3 ? gqa::kCacheE4m3 : a.q_bf16 ? gqa::kCacheBf16 : gqa::kCacheF16;
+  a.scale = (float)((double)q_scale * k_scale / std::sqrt((double)qs[2]));
+  a.v_scale = v_scale;
+  a.softcap = softcap;
+  a.window = window;
+  a.starve = gqa::starve_producers();
+  ScopedDevice sd(where.device);
+  if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", where.device);
+  GQA_CUDA_TRY(gqa::launch_paged_attn(a, workspace_, reinterpret_cast<cudaStream_t>(stream)), "paged attention launch");
+  return GQA_OK;
 }
 
 gqa_status gqa_release_workspace(void) {

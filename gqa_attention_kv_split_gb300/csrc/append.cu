@@ -1,0 +1,383 @@
+// append.cu -- rotary embedding of new query and key rows and the append of
+// the keys and values to a paged cache: 16-bit pages, E4M3 pages, and NVFP4
+// pages (E2M1 codes with one E4M3 scale per 16 elements, the pages that
+// nvfp4_paged_ctx_attn reads).
+//
+// Mathematics.  Token t of sequence b sits at position
+//   pos = kv_lens[b] - (indptr[b+1] - t),
+// and a rotated pair (x, y) of a q or k row becomes (x c - y s, y c + x s) with
+// c = rope[pos, i], s = rope[pos, rot/2 + i] -- pairs (i, i + rot/2), or
+// (2i, 2i + 1) interleaved.  Products and sums are formed in f32, each rounded
+// once (no contraction), and the result is rounded once to its stored type.
+// NVFP4: sf = E4M3(amax / 6) of a 16-element block, codes = E2M1(x / sf), true
+// f32 divisions, so a plain f32 evaluation gives the same bits.
+//
+// What bounds it: HBM for prompts (each input read once, each output written
+// once, 3 flops per rotated element), latency for single tokens -- a chain of
+// dependent loads (lengths, then the table entry and the angles).  Hence:
+//  * one thread owns one pair of 16-byte vectors of a row (the two halves of a
+//    rotation when it is a half-split one), so a rotation needs no exchange;
+//  * the row data, which depend on no metadata, are loaded before the token's
+//    sequence, position and page are looked up;
+//  * a warp looks up one token (a 32-way search of indptr: two probes for up
+//    to 1024 sequences), and a block's warps look up its tokens side by side.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gqa {
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kMaxTok = kAppendThreads / 32;  // tokens per block: one looked up by each warp
+
+__device__ uint32_t g_append_err;
+
+// Where a block's token goes: its position, and its page and slot; pos < 0: not written.
+struct TokenPlace {
+  int64_t page;
+  int64_t pos;
+  int slot;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float f[8], __half) {
+  const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __half22float2(h[i]);
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float f[8], __nv_bfloat16) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float f[8], __half) {
+  uint4 u;
+  __half2* h = reinterpret_cast<__half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+  return u;
+}
+__device__ __forceinline__ uint4 pack8(const float f[8], __nv_bfloat16) {
+  uint4 u;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  return u;
+}
+
+// Two f32 -> two E4M3 bytes (lo in the low byte), RNE, saturating; NaN stays NaN.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint2 pack8_e4m3(const float f[8], float inv_scale) {
+  uint2 u;
+  u.x = f32x2_to_e4m3x2(__fmul_rn(f[0], inv_scale), __fmul_rn(f[1], inv_scale)) |
+        (f32x2_to_e4m3x2(__fmul_rn(f[2], inv_scale), __fmul_rn(f[3], inv_scale)) << 16);
+  u.y = f32x2_to_e4m3x2(__fmul_rn(f[4], inv_scale), __fmul_rn(f[5], inv_scale)) |
+        (f32x2_to_e4m3x2(__fmul_rn(f[6], inv_scale), __fmul_rn(f[7], inv_scale)) << 16);
+  return u;
+}
+
+// Two f32 -> one byte of E2M1 codes (lo in the low nibble), RNE, saturating.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float amax8(const float f[8]) {
+  float m = fabsf(f[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+  return m;
+}
+// E4M3 scale byte of a block's largest magnitude, and the scale's value.
+__device__ __forceinline__ uint32_t block_scale(float amax, float* value) {
+  const uint32_t byte = f32x2_to_e4m3x2(__fdiv_rn(amax, 6.f), 0.f);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)byte));
+  *value = __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+  return byte & 0xffu;
+}
+// Eight elements -> 4 bytes of codes; all codes 0 where the scale is 0 or NaN.
+__device__ __forceinline__ uint32_t codes8(const float f[8], float scale) {
+  if (!(scale > 0.f)) return 0u;
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r |= f32x2_to_e2m1x2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)) << (8 * i);
+  return r;
+}
+
+// The sequence of token t: the last b with indptr[b] <= t (the whole warp).
+// Each step probes 32 evenly spaced entries; every probe lies in [lo, hi).
+__device__ __forceinline__ int64_t find_sequence(const int32_t* indptr, int64_t batch, int64_t t, int lane) {
+  int64_t lo = 0, hi = batch;  // the answer is in [lo, hi) if indptr[0] <= t
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 31) / 32;
+    const int64_t at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && indptr[at] <= t);
+    const int k = le ? 31 - __clz(le) : 0;
+    lo += k * step;
+    hi = hi < lo + step ? hi : lo + step;
+  }
+  return lo;
+}
+
+// Position, page and slot of token t (the whole warp; the result in lane 0).
+__device__ __forceinline__ TokenPlace place_token(const AppendArgs& a, int64_t t, int lane) {
+  TokenPlace p{0, -1, 0};
+  int64_t b = t, behind = 1;  // tokens from t to the end of its sequence's new ones
+  if (a.indptr) {
+    b = find_sequence(a.indptr, a.batch, t, lane);
+    const int64_t lo = a.indptr[b], hi = a.indptr[b + 1];
+    if (t < lo || t >= hi) {
+      // Behind the last sequence is a padded batch; anywhere else the offsets are wrong.
+      if (t < a.indptr[a.batch] && lane == 0) atomicOr(&g_append_err, kErrBadIndptr);
+      return p;
+    }
+    behind = hi - t;
+  }
+  const int64_t pos = (int64_t)a.kv_lens[b] - behind;
+  if (pos < 0) return p;  // an inactive sequence
+  const int64_t lp = pos / a.page_size;
+  int64_t page = -1;
+  if (lp < a.max_pages_per_seq) page = a.block_table[b * a.max_pages_per_seq + lp];
+  if (page < 0 || page >= a.num_pages || (a.rope && pos >= a.rope_len)) {
+    if (lane == 0) atomicOr(&g_append_err, kErrBadIndex);
+    return p;
+  }
+  p.page = page;
+  p.pos = pos;
+  p.slot = (int)(pos - lp * a.page_size);
+  return p;
+}
+
+// kMode: kAppendSame (pages of the inputs' type), kAppendE4m3, kAppendNvfp4.
+template <typename T, int D, int kMode>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  constexpr int kLanes = D / 16;  // threads per row, each with two 16-byte vectors
+  __shared__ TokenPlace place[kMaxTok];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tok_per_block;
+  const int n_tok = (int)(a.total < t0 + a.tok_per_block ? a.total - t0 : a.tok_per_block);
+  const int rows = (a.q ? a.hq : 0) + 2 * a.hkv;  // of one token: q heads, k heads, v heads
+  const int hq = a.q ? a.hq : 0;
+  const uint32_t n_items = (uint32_t)n_tok * rows * kLanes;
+  const int turned = a.rope ? a.rot / 16 : 0;  // lanes of a row that rotate
+
+  struct Item {
+    uint4 lo, hi;
+  };
+  // Item i: (token, row, lane of the row) and its two vectors' numbers within the row.
+  auto where = [&](uint32_t i, int& tok, int& row, int& j) {
+    j = (int)(i % kLanes);
+    const uint32_t r = i / kLanes;
+    tok = (int)(r / (uint32_t)rows);
+    row = (int)(r - (uint32_t)tok * rows);
+  };
+  auto vectors = [&](int row, int j, int& v0, int& v1) {
+    const bool split = row < hq + a.hkv && j < turned && !a.interleaved;
+    v0 = split ? j : 2 * j;
+    v1 = split ? j + turned : 2 * j + 1;
+  };
+  auto load = [&](uint32_t i) {
+    Item it{};
+    if (i < n_items) {
+      int tok, row, j, v0, v1;
+      where(i, tok, row, j);
+      vectors(row, j, v0, v1);
+      const T* src;
+      if (row < hq)
+        src = static_cast<const T*>(a.q) + (t0 + tok) * a.q_tok + row * a.q_head;
+      else if (row < hq + a.hkv)
+        src = static_cast<const T*>(a.k) + (t0 + tok) * a.k_tok + (row - hq) * a.k_head;
+      else
+        src = static_cast<const T*>(a.v) + (t0 + tok) * a.v_tok + (row - hq - a.hkv) * a.v_head;
+      it.lo = *reinterpret_cast<const uint4*>(src + 8 * v0);
+      it.hi = *reinterpret_cast<const uint4*>(src + 8 * v1);
+    }
+    return it;
+  };
+
+  Item cur = load(threadIdx.x);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.indptr && a.indptr[a.batch] > a.total)
+    atomicOr(&g_append_err, kErrBadIndptr);
+  if (warp < n_tok) {
+    const TokenPlace p = place_token(a, t0 + warp, lane);
+    if (lane == 0) place[warp] = p;
+  }
+  __syncthreads();
+
+  const uint32_t n_round = (n_items + kAppendThreads - 1) / kAppendThreads;
+  for (uint32_t n = 0; n < n_round; ++n) {
+    const uint32_t i = n * kAppendThreads + threadIdx.x;
+    const Item it = cur;
+    cur = load(i + kAppendThreads);
+    int tok = 0, row = 0, j = 0, v0, v1;
+    const bool have = i < n_items;
+    if (have) where(i, tok, row, j);
+    vectors(row, j, v0, v1);
+    const TokenPlace p = place[tok];
+    const bool live = have && p.pos >= 0;
+    float x[8], y[8];
+    unpack8(it.lo, x, T());
+    unpack8(it.hi, y, T());
+    if (live && row < hq + a.hkv && j < turned) {
+      const float* cs = a.rope + p.pos * a.rot + 8 * j;
+      float c[8], s[8];
+      *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs);
+      *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(cs + 4);
+      *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(cs + a.rot / 2);
+      *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(cs + a.rot / 2 + 4);
+      if (a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float u = x[2 * e], w = x[2 * e + 1];
+          x[2 * e] = __fsub_rn(__fmul_rn(u, c[e]), __fmul_rn(w, s[e]));
+          x[2 * e + 1] = __fadd_rn(__fmul_rn(w, c[e]), __fmul_rn(u, s[e]));
+          const float u2 = y[2 * e], w2 = y[2 * e + 1];
+          y[2 * e] = __fsub_rn(__fmul_rn(u2, c[4 + e]), __fmul_rn(w2, s[4 + e]));
+          y[2 * e + 1] = __fadd_rn(__fmul_rn(w2, c[4 + e]), __fmul_rn(u2, s[4 + e]));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = x[e], w = y[e];
+          x[e] = __fsub_rn(__fmul_rn(u, c[e]), __fmul_rn(w, s[e]));
+          y[e] = __fadd_rn(__fmul_rn(w, c[e]), __fmul_rn(u, s[e]));
+        }
+      }
+    }
+    // The largest magnitudes of an NVFP4 block: a rotated half-split row has its
+    // blocks in two neighbouring lanes (rot is a multiple of 32, so lanes 2i and
+    // 2i+1 hold the halves of one block, twice); otherwise a lane has a whole one.
+    float ax = 0.f, ay = 0.f;
+    const bool split = v1 != v0 + 1;
+    if (kMode == kAppendNvfp4) {
+      ax = amax8(x);
+      ay = amax8(y);
+      const float ox = __shfl_xor_sync(0xffffffffu, ax, 1), oy = __shfl_xor_sync(0xffffffffu, ay, 1);
+      if (split) {
+        ax = max_nan(ax, ox);
+        ay = max_nan(ay, oy);
+      } else {
+        ax = max_nan(ax, ay);
+      }
+    }
+    if (!live) continue;
+    if (row < hq) {
+      if (kMode == kAppendNvfp4) {
+        uint8_t* dst = static_cast<uint8_t*>(a.q_out) + (t0 + tok) * a.qo_tok + row * a.qo_head;
+        *reinterpret_cast<uint2*>(dst + 8 * v0) = pack8_e4m3(x, a.inv_q);
+        *reinterpret_cast<uint2*>(dst + 8 * v1) = pack8_e4m3(y, a.inv_q);
+      } else {
+        T* dst = static_cast<T*>(a.q_out) + (t0 + tok) * a.qo_tok + row * a.qo_head;
+        *reinterpret_cast<uint4*>(dst + 8 * v0) = pack8(x, T());
+        *reinterpret_cast<uint4*>(dst + 8 * v1) = pack8(y, T());
+      }
+      continue;
+    }
+    const bool is_v = row >= hq + a.hkv;
+    const int h = row - hq - (is_v ? a.hkv : 0);
+    if (kMode == kAppendNvfp4) {
+      const int64_t r = (p.page * kHkv + h) * kPage + p.slot;
+      uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + r * (D / 2);
+      uint8_t* sf = (is_v ? a.v_sf : a.k_sf) + r * (D / 16);
+      float sx, sy;
+      if (split) {
+        const uint32_t bx = block_scale(ax, &sx), by = block_scale(ay, &sy);
+        *reinterpret_cast<uint32_t*>(codes + 4 * v0) = codes8(x, sx);
+        *reinterpret_cast<uint32_t*>(codes + 4 * v1) = codes8(y, sy);
+        if ((j & 1) == 0) {
+          sf[v0 / 2] = (uint8_t)bx;
+          sf[v1 / 2] = (uint8_t)by;
+        }
+      } else {
+        sf[j] = (uint8_t)block_scale(ax, &sx);
+        *reinterpret_cast<uint2*>(codes + 8 * j) = make_uint2(codes8(x, sx), codes8(y, sx));
+      }
+    } else {
+      const int64_t off = is_v ? p.page * a.vp_page + h * a.vp_head + p.slot * a.vp_slot
+                               : p.page * a.kp_page + h * a.kp_head + p.slot * a.kp_slot;
+      void* base = is_v ? a.v_pages : a.k_pages;
+      if (kMode == kAppendE4m3) {
+        const float inv = is_v ? a.inv_v : a.inv_k;
+        uint8_t* dst = static_cast<uint8_t*>(base) + off;
+        *reinterpret_cast<uint2*>(dst + 8 * v0) = pack8_e4m3(x, inv);
+        *reinterpret_cast<uint2*>(dst + 8 * v1) = pack8_e4m3(y, inv);
+      } else {
+        T* dst = static_cast<T*>(base) + off;
+        *reinterpret_cast<uint4*>(dst + 8 * v0) = pack8(x, T());
+        *reinterpret_cast<uint4*>(dst + 8 * v1) = pack8(y, T());
+      }
+    }
+  }
+}
+
+template <typename T, int kMode>
+cudaError_t launch_d(const AppendArgs& a, unsigned grid, cudaStream_t stream) {
+  if (kMode == kAppendNvfp4) {
+    append_kernel<T, kD, kMode><<<grid, kAppendThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  switch (a.d) {
+    case 64: append_kernel<T, 64, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
+    case 128: append_kernel<T, 128, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
+    default: append_kernel<T, 256, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_mode(const AppendArgs& a, unsigned grid, cudaStream_t stream) {
+  switch (a.mode) {
+    case kAppendSame: return launch_d<T, kAppendSame>(a, grid, stream);
+    case kAppendE4m3: return launch_d<T, kAppendE4m3>(a, grid, stream);
+    default: return launch_d<T, kAppendNvfp4>(a, grid, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append(AppendArgs a, cudaStream_t stream) {
+  // Tokens per block: enough blocks for every SM first, then up to one token
+  // per warp, which shares a block's start among more rows.
+  int64_t per = a.total / (152 * 4);
+  if (per < 1) per = 1;
+  if (per > kMaxTok) per = kMaxTok;
+  a.tok_per_block = (int)per;
+  const int64_t grid = (a.total + per - 1) / per;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return a.bf16 ? launch_mode<__nv_bfloat16>(a, (unsigned)grid, stream) : launch_mode<__half>(a, (unsigned)grid, stream);
+}
+
+cudaError_t append_read_errors(uint32_t* word) {
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return e;
+  uint32_t zero = 0;
+  if ((e = cudaMemcpyFromSymbol(word, g_append_err, sizeof(uint32_t))) != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_append_err, &zero, sizeof(uint32_t));
+}
+
+}  // namespace gqa

@@ -1,0 +1,772 @@
+// paged_attn.cuh -- attention of one new token per sequence over a paged K/V
+// cache (f16, bf16 or E4M3 pages), grouped queries, split over the cache's
+// length and joined, for sm_103a.
+//
+// Mathematics.  For sequence b, query head h and KV head g = h / G,
+//   s_t = cap( (q . K_t) * scale ),  cap(x) = softcap * tanh(x / softcap) if softcap > 0,
+//   out = v_scale * sum_t exp(s_t - m) V_t / sum_t exp(s_t - m),  lse = ln sum_t exp(s_t)
+// over max(0, len - window) <= t < len.  A range of tokens is summed as
+// (m, l, o) with the running maximum m, l = sum exp(s - m) and o = sum exp(s -
+// m) V in f32; ranges join by rescaling to the larger m.
+//
+// What bounds it: HBM -- every K/V byte is read once for 4 G / w flops (w bytes
+// per element).  FMA units keep up only to G of about 6 at 16 bits, so both
+// products run on the tensor cores, transposed: S^T = K Q^T and O^T = V^T P^T,
+// with 16 keys (then 16 output elements) on the M side and 8 heads on the N
+// side.  The cache is the A operand straight from shared memory, a group of up
+// to 8 heads costs the same as one, and the accumulators of the output are D / 4
+// registers for each 8 heads.  The warp-level mma is enough: at HBM speed
+// it is busy for a few per cent (a tcgen05 tile has 128 rows for the 4 to 16
+// that there are, and its P would have to travel through TMEM).
+//
+//  * Grid: one block per SM, each with an equal share of all 16-byte-row tiles of
+//    all (sequence, KV head, block of heads) units, in order, whatever the
+//    lengths -- the shares are computed on the device from seq_lens.  A unit that
+//    lies inside one block is written by it; the pieces of one that does not go
+//    to the workspace (at most two per block) and a second kernel joins them.
+//  * A producer warp moves tiles of 64 (32) tokens with tensor-map TMA copies
+//    into a ring of about 190 KB: any page size and cache order is a box of the
+//    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
+//  * Eight consumer warps (four at head dim 256), each with its own 16 keys of a tile and its own
+//    (m, l, o); groups of warps take alternate tiles, so that one tile's softmax
+//    overlaps the next one's products.  They meet at the end of a unit only.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "paged_attn_host.h"
+
+namespace gqa {
+namespace pa {
+
+namespace {
+
+__device__ uint32_t g_paged_attn_err;  // of this translation unit's kernels
+
+}  // namespace
+
+
+template <int kCache, int D>
+struct Shape {
+  static constexpr int kEsz = kCache == kCacheE4m3 ? 1 : 2;
+  static constexpr int kRow = D * kEsz;                     // bytes of a token's row
+  static constexpr int kChunk = kRow < 128 ? kRow : 128;    // bytes of a swizzled row in shared memory
+  static constexpr int kChunks = kRow / kChunk;
+  static constexpr int kTile = tile_of(kRow);                // tokens per stage
+  // Consumer warps: eight, or four where the accumulators need more than the 168
+  // registers a thread that nine warps leave.
+  static constexpr int kWarps = D > 128 ? 4 : 8;
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kGroupWarps = kTile / 16;            // warps that share a tile
+  static constexpr int kGroups = kWarps / kGroupWarps;      // tiles in work at a time
+  static constexpr int kHalf = kTile * kRow;                // bytes of K (and of V) of a stage
+  static constexpr int kRoom = D > 128 ? 128 * 1024 : 192 * 1024;  // the join's buffers take the rest
+  // A whole number of groups' turns, so that a stage always belongs to one group (a
+  // wait on its barrier can then never be a phase behind).
+  static constexpr int kStages = kRoom / (2 * kHalf) / kGroups * kGroups;
+  static_assert(kStages >= kGroups, "ring too small");
+};
+
+template <int kWarps, int D, int NT>
+struct Smem {
+  static constexpr int kRows = 8 * NT;
+  alignas(16) uint8_t q[2][kRows][D * 2 + 16];
+  alignas(16) float o[kWarps][4][D + 4];  // four heads at a time; the odd row length spreads the banks
+  float m[kWarps][kRows];
+  float l[kWarps][kRows];
+  alignas(8) uint64_t full[32];
+  uint64_t empty[32];
+  uint64_t q_full[2];
+  uint64_t q_empty[2];
+  int64_t scan[kWarps + 1];
+  int64_t total;  // tiles of the whole call
+  int64_t b0, rem;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t r[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t r[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ void mma(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  if (kBf16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* map, int slot, int head, int page, uint32_t bar,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(map), "r"(0), "r"(slot), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// First token and number of tiles of a sequence.
+template <int kTile>
+struct Span {
+  int len, first, tile0, tiles;
+  __device__ __forceinline__ Span(const Params& p, int64_t b) {
+    const int64_t cap = p.max_pages * p.page_size;
+    const int64_t n = p.seq_lens[b];
+    len = (int)(n < 0 ? 0 : (n > cap ? cap : n));
+    first = p.window > 0 && len > p.window ? len - p.window : 0;
+    tile0 = first / kTile;
+    tiles = (len + kTile - 1) / kTile - tile0;  // (a capacity is at most 2^30 tokens)
+  }
+};
+
+// Walks the units of a block's share [pos, end) of the call's tiles.
+template <int kTile>
+struct Walk {
+  int64_t pos, end, b;
+  int unit;   // within the sequence: kv head * head blocks + head block
+  int t_beg;  // first tile of the piece within the unit, and one past its last
+  int t_end;
+  Span<kTile> span;
+  int units;
+  __device__ __forceinline__ Walk(const Params& p, int64_t pos_, int64_t end_, int64_t b_, int64_t rem)
+      : pos(pos_), end(end_), b(b_), span(p, b_), units(p.hkv * p.head_blocks) {
+    unit = (int)(rem / span.tiles);
+    t_beg = (int)(rem - (int64_t)unit * span.tiles);
+    clip();
+  }
+  __device__ __forceinline__ void clip() {
+    const int64_t left = end - pos;
+    t_end = left < span.tiles - t_beg ? t_beg + (int)left : span.tiles;
+  }
+  // To the next piece; false at the end of the share.
+  __device__ __forceinline__ bool next(const Params& p) {
+    pos += t_end - t_beg;
+    if (pos >= end) return false;
+    t_beg = 0;
+    if (++unit == units) {
+      unit = 0;
+      do {
+        span = Span<kTile>(p, ++b);
+      } while (span.tiles == 0);
+    }
+    clip();
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t_beg == 0 && t_end == span.tiles; }
+};
+
+namespace {
+
+template <int kCache, int D, int NT>
+__global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
+    paged_attn_kernel(const Params p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+  uint32_t* const err = &g_paged_attn_err;
+  using S = Shape<kCache, D>;
+  constexpr bool kBf16 = kCache == kCacheBf16;
+  constexpr bool kFp8 = kCache == kCacheE4m3;
+  constexpr int kTile = S::kTile, kWarps = S::kWarps, kThreads = S::kThreads;
+  constexpr int kRows = 8 * NT;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = smem_raw;
+  Smem<S::kWarps, D, NT>& sm = *reinterpret_cast<Smem<S::kWarps, D, NT>*>(smem_raw + S::kStages * 2 * S::kHalf);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = p.hkv * p.head_blocks;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(smem_u32(&sm.full[i]), 1);
+      mbar_init(smem_u32(&sm.empty[i]), S::kGroupWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.q_full[i]), 1);
+      mbar_init(smem_u32(&sm.q_empty[i]), kWarps);
+    }
+    fence_mbar_init();
+  }
+  // Query rows that a unit does not have stay zero or hold an older row: each head is a
+  // column of its own in both products.
+  for (int i = threadIdx.x; i < (int)sizeof(sm.q) / 16; i += kThreads)
+    reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+
+  // ---- this block's share: tiles [T * block / n, T * (block + 1) / n) ---------
+  // Each thread sums the tiles of a contiguous range of sequences; a scan over the
+  // threads gives the ranges' starts, and the range that holds the share's first tile
+  // is walked by its thread.
+  const int64_t per = (p.batch + kThreads - 1) / kThreads;
+  const int64_t s0 = threadIdx.x * per < p.batch ? threadIdx.x * per : p.batch;
+  const int64_t s1 = s0 + per < p.batch ? s0 + per : p.batch;
+  int64_t mine = 0;
+  for (int64_t b = s0; b < s1; ++b) {
+    const Span<kTile> sp(p, b);
+    mine += sp.tiles;
+    if (sp.tiles == 0 && b % kGrid == blockIdx.x) {  // no token: a zero row
+      for (int h = 0; h < p.hq; ++h) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + ((int64_t)b * p.hq + h) * D * 2);
+        for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse) p.lse[(int64_t)b * p.hq + h] = -INFINITY;
+      }
+    }
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.scan[w];
+    total += sm.scan[w];
+  }
+  before += incl - mine;
+  before *= units;
+  total *= units;
+  const int64_t n_blocks = total < kGrid ? total : kGrid;  // blocks with a share: none is empty
+  const int64_t beg = blockIdx.x < n_blocks ? total * blockIdx.x / n_blocks : 0;
+  const int64_t end = blockIdx.x < n_blocks ? total * (blockIdx.x + 1) / n_blocks : 0;
+  if (beg < end && beg >= before && beg < before + mine * units) {
+    int64_t rem = beg - before;
+    int64_t b = s0;
+    for (;; ++b) {
+      const int64_t n = (int64_t)Span<kTile>(p, b).tiles * units;
+      if (rem < n) break;
+      rem -= n;
+    }
+    sm.b0 = b;
+    sm.rem = rem;
+  }
+  __syncthreads();
+  if (beg >= end) {
+    if (threadIdx.x == 0) p.record[blockIdx.x].unit = -1;
+    return;
+  }
+  Walk<kTile> walk(p, beg, end, sm.b0, sm.rem);
+
+  if (warp == kWarps) {
+    // ---------------- producer ------------------------------------------------
+    if (p.starve) return;
+    const uint64_t pol = p.head_blocks == 1 ? policy_evict_first() : policy_evict_last();
+    const int box = p.box;
+    const int boxes = kTile / box;  // copies per tile of K (and of V)
+    const uint32_t box_bytes = (uint32_t)box * S::kRow;
+    int64_t n = 0;  // tiles issued
+    int seg = 0;    // pieces begun
+    bool ok = true;
+    do {
+      const int kvh = walk.unit / p.head_blocks;
+      const int h0 = kvh * p.group + (walk.unit - kvh * p.head_blocks) * kRows;
+      const int heads = min(kRows, (kvh + 1) * p.group - h0);
+      const int qb = seg & 1;
+      if (seg >= 2 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_empty[qb]), ((seg >> 1) - 1) & 1, err))) ok = false;
+      if (!ok) break;
+      const uint32_t qf = smem_u32(&sm.q_full[qb]);
+      if (lane == 0) mbar_arrive_expect_tx(qf, (uint32_t)heads * D * 2);
+      __syncwarp();
+      if (lane < heads)
+        bulk_g2s_hint(smem_u32(sm.q[qb][lane]), static_cast<const uint8_t*>(p.q) + (walk.b * p.q_seq + (h0 + lane) * p.q_head) * 2,
+                      D * 2, qf, policy_evict_last());
+      ++seg;
+      // Page numbers, 32 copies' worth at a time and one such group ahead (lane l has those of copy l).
+      const int32_t* row = p.block_table + walk.b * p.max_pages;
+      const int c0 = (walk.span.tile0 + walk.t_beg) * boxes;       // first copy, counted from the sequence's first token
+      const int c_end = (walk.span.len + box - 1) / box;           // copies behind the last token are not made
+      const int c_first = walk.span.first / box;                   // nor those before the window
+      auto page_of = [&](int c) {
+        if (c < c_first || c >= c_end) return 0;
+        int g = row[(int64_t)c * box / p.page_size];
+        if (g < 0 || g >= p.num_pages) {
+          atomicOr(err, kErrBadIndex);
+          g = 0;
+        }
+        return g;
+      };
+      int cur = page_of(c0 + lane), nxt = page_of(c0 + 32 + lane);
+      int at = 0;  // copies of this piece so far
+      for (int t = walk.t_beg; t < walk.t_end; ++t, ++n) {
+        const int st = (int)(n % S::kStages);
+        if (n >= S::kStages && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.empty[st]), (int)(n / S::kStages - 1) & 1, err))) {
+          ok = false;
+          break;
+        }
+        const int c = c0 + at + lane;
+        const int pg = __shfl_sync(0xffffffffu, cur, (at + lane) & 31);
+        const bool live = lane < boxes && c >= c_first && c < c_end;
+        const uint32_t bar = smem_u32(&sm.full[st]);
+        const uint32_t bytes = 2u * box_bytes * __popc(__ballot_sync(0xffffffffu, live));
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        if (live) {
+          const uint32_t dst = smem_u32(ring) + st * 2 * S::kHalf + lane * box_bytes;
+          const int slot = (int)((int64_t)c * box % p.page_size);
+          tma_5d(dst, &k_map, slot, kvh, pg, bar, pol);
+          tma_5d(dst + S::kHalf, &v_map, slot, kvh, pg, bar, pol);
+        }
+        at += boxes;
+        if ((at & 31) == 0) {
+          cur = nxt;
+          nxt = page_of(c0 + at + 32 + lane);
+        }
+      }
+    } while (ok && walk.next(p));
+    // No copy may land after the block has gone.
+    if (lane == 0) {
+      for (int64_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
+        mbar_wait(smem_u32(&sm.full[i % S::kStages]), (int)(i / S::kStages) & 1, err);
+      for (int i = seg > 2 ? seg - 2 : 0; i < seg; ++i) mbar_wait(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1, err);
+    }
+    return;
+  }
+
+  // ---------------- consumers --------------------------------------------------
+  const int grp = warp / S::kGroupWarps;
+  const int row0 = (warp % S::kGroupWarps) * 16;  // this warp's keys of a tile
+  const int g = lane >> 2, c2 = (lane & 3) * 2;
+  const uint32_t ring_u = smem_u32(ring);
+  // 16-key block of a copy: the copy's base and this warp's first row in it
+  const int box = p.box;
+  const uint32_t blk = (uint32_t)(row0 / box) * box * S::kRow + (uint32_t)(row0 % box) * S::kChunk;
+  const uint32_t chunk_step = (uint32_t)box * S::kChunk;
+  // ldmatrix row of this lane: K rows 0-15 (A operand), V rows 0-15 (transposed A operand)
+  const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8;
+  const int v_row = kFp8 ? k_row : (lane & 7) + (lane >> 4) * 8;
+  const int k_sel = lane >> 4, v_sel = kFp8 ? lane >> 4 : (lane >> 3) & 1;  // which 16 bytes of a 32-byte step
+  auto swz = [](int row, int c16) { return S::kChunk == 128 ? (c16 ^ (row & 7)) : (c16 ^ ((row >> 1) & 3)); };
+  // 16-byte column c16 of the whole row -> offset within the block
+  auto col = [&](int row, int c16) {
+    constexpr int kPer = S::kChunk / 16;
+    return (uint32_t)(c16 / kPer) * chunk_step + (uint32_t)row * S::kChunk + (uint32_t)swz(row, c16 % kPer) * 16;
+  };
+  // P keeps f16's full precision down to 2^-28 of the largest weight.
+  constexpr float kShift = kBf16 ? 0.f : 14.f;
+
+  int64_t n = 0;
+  int seg = 0;
+  bool dead = false;  // a wait has expired: nothing more is waited for or computed
+  do {
+    const int kvh = walk.unit / p.head_blocks;
+    const int h0 = kvh * p.group + (walk.unit - kvh * p.head_blocks) * kRows;
+    const int heads = min(kRows, (kvh + 1) * p.group - h0);
+    const int qb = seg & 1;
+    if (!dead && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_full[qb]), (seg >> 1) & 1, err))) dead = true;
+    // Q as the B operand of S^T = K Q^T: column g = head, rows = head-dim elements (for
+    // E4M3 pages in the order in which a widened 32-bit word of K gives them).
+    uint32_t qf[NT][D / 16][2];
+    float sc[NT][2];  // scale of the scores of heads c2, c2 + 1
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint8_t* qr = sm.q[qb][8 * t + g];
+      if (!kFp8) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          qf[t][k][0] = *reinterpret_cast<const uint32_t*>(qr + (16 * k + c2) * 2);
+          qf[t][k][1] = *reinterpret_cast<const uint32_t*>(qr + (16 * k + c2 + 8) * 2);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint2 w = *reinterpret_cast<const uint2*>(qr + (16 * k + 2 * c2) * 2);
+          qf[t][k][0] = w.x;
+          qf[t][k][1] = w.y;
+        }
+      }
+      sc[t][0] = sc[t][1] = 1.f;
+      if (kFp8 && p.q_bf16) {
+        // bf16 rows enter the f16 product scaled by a power of two that brings their
+        // largest element into [1, 2): exact but for elements below 2^-14 of it, whose
+        // rounding is at most 2^-25 of the largest.
+        uint32_t mx = 0;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx = max(mx, qf[t][k][i] & 0x7fffu);
+            mx = max(mx, (qf[t][k][i] >> 16) & 0x7fffu);
+          }
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = min(max((int)(mx >> 7), 1), 253);  // biased exponent
+        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+        const float up = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[t][k][i] = pack_f16(bf16_lo(qf[t][k][i]) * down, bf16_hi(qf[t][k][i]) * down);
+        sc[t][0] = __shfl_sync(0xffffffffu, up, c2 * 4);
+        sc[t][1] = __shfl_sync(0xffffffffu, up, c2 * 4 + 4);
+      }
+      const float f = p.cap_out != 0.f ? p.cap_in : p.scale_log2;
+      sc[t][0] *= f;
+      sc[t][1] *= f;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[qb]));
+    ++seg;
+
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
+
+    for (int tile = walk.t_beg; tile < walk.t_end; ++tile, ++n) {
+      if ((int)(n % S::kGroups) != grp || dead) continue;
+      const int st = (int)(n % S::kStages);
+      const int key0 = (walk.span.tile0 + tile) * kTile + row0;  // this warp's first key
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), (int)(n / S::kStages) & 1, err))) {
+        dead = true;
+        continue;
+      }
+      const uint32_t kb = ring_u + st * 2 * S::kHalf + blk, vb = kb + S::kHalf;
+      if (key0 < walk.span.len && key0 + 16 > walk.span.first) {
+        const bool edge = key0 + 16 > walk.span.len || key0 < walk.span.first;
+        // ---- S^T = K Q^T, in two sums (even and odd steps)
+        float s[NT][2][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][i][e] = 0.f;
+        if (!kFp8) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t a[4];
+            ldsm4(a, kb + col(k_row, 2 * k + k_sel));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma<kBf16>(s[t][k & 1], a, qf[t][k][0], qf[t][k][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t w[4];
+            ldsm4(w, kb + col(k_row, 2 * k + k_sel));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a[4] = {e4m3_to_f16x2(w[2 * i] & 0xffffu), e4m3_to_f16x2(w[2 * i + 1] & 0xffffu),
+                                     e4m3_to_f16x2(w[2 * i] >> 16), e4m3_to_f16x2(w[2 * i + 1] >> 16)};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma<false>(s[t][i], a, qf[t][2 * k + i][0], qf[t][2 * k + i][1]);
+            }
+          }
+        }
+        if (edge) {
+          // V rows outside the sequence may hold anything; 0 * NaN is NaN, so they are zeroed.
+          for (int i = lane; i < 16 * (S::kRow / 16); i += 32) {
+            const int r = i % 16, c16 = i / 16;
+            if (key0 + r >= walk.span.len || key0 + r < walk.span.first)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + col(r, c16)), "r"(0) : "memory");
+          }
+          __syncwarp();
+        }
+        // ---- softmax weights: rows (keys) g, g + 8; columns (heads) c2, c2 + 1
+        uint32_t pb[NT][2], pl[NT][2];
+        float alpha[NT][2];
+        bool grow = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = (s[t][0][e] + s[t][1][e]) * sc[t][e & 1];
+            if (p.cap_out != 0.f) v[e] = p.cap_out * (1.f - __fdividef(2.f, fast_exp2(v[e]) + 1.f));
+          }
+          if (edge) {
+            const int ka = key0 + g, kc = ka + 8;
+            if (ka >= walk.span.len || ka < walk.span.first) v[0] = v[1] = -INFINITY;
+            if (kc >= walk.span.len || kc < walk.span.first) v[2] = v[3] = -INFINITY;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x = fmaxf(v[i], v[i + 2]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float mn = fmaxf(m[t][i], x);
+            const float sub = mn == -INFINITY ? 0.f : mn;
+            grow |= mn != m[t][i];
+            alpha[t][i] = fast_exp2(m[t][i] - sub);
+            m[t][i] = mn;
+            v[i] = fast_exp2(v[i] - sub + kShift);
+            v[i + 2] = fast_exp2(v[i + 2] - sub + kShift);
+            l[t][i] = fmaf(l[t][i], alpha[t][i], v[i] + v[i + 2]);
+          }
+          // P^T as the B operand of O^T = V^T P^T: rows = keys, columns = heads.  A bf16
+          // weight is split into two bf16 terms (16 bits of it are kept); an f16 weight is
+          // rounded once, to 11 bits.
+          if (kBf16) {
+            const uint32_t x0 = pack_bf16(v[0], v[1]), x1 = pack_bf16(v[2], v[3]);
+            pb[t][0] = movm_t(x0);
+            pb[t][1] = movm_t(x1);
+            pl[t][0] = movm_t(pack_bf16(v[0] - bf16_lo(x0), v[1] - bf16_hi(x0)));
+            pl[t][1] = movm_t(pack_bf16(v[2] - bf16_lo(x1), v[3] - bf16_hi(x1)));
+          } else {
+            pb[t][0] = movm_t(pack_f16(v[0], v[1]));
+            pb[t][1] = movm_t(pack_f16(v[2], v[3]));
+          }
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][i][e] *= alpha[t][e & 1];
+        }
+        // ---- O^T += V^T P^T
+        if (!kFp8) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t a[4];
+            ldsm4_t(a, vb + col(v_row, 2 * i + v_sel));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma<kBf16>(o[t][i], a, pb[t][0], pb[t][1]);
+              if (kBf16) mma<kBf16>(o[t][i], a, pl[t][0], pl[t][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t w[4];
+            ldsm4_t(w, vb + col(v_row, 2 * k + v_sel));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              // two keys of two neighbouring elements -> the two keys of each element
+              const uint32_t lo = __byte_perm(w[2 * i], 0u, 0x3120), hi = __byte_perm(w[2 * i + 1], 0u, 0x3120);
+              const uint32_t a[4] = {e4m3_to_f16x2(lo & 0xffffu), e4m3_to_f16x2(lo >> 16), e4m3_to_f16x2(hi & 0xffffu),
+                                     e4m3_to_f16x2(hi >> 16)};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma<false>(o[t][2 * k + i], a, pb[t][0], pb[t][1]);
+            }
+          }
+        }
+        if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
+    }
+
+    // ---- join the warps --------------------------------------------------
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
+        if (g == 0) {
+          sm.m[warp][8 * t + c2 + i] = m[t][i];
+          sm.l[warp][8 * t + c2 + i] = l[t][i];
+        }
+      }
+    const bool whole = walk.whole();
+    const int slot = walk.pos == beg ? 0 : 1;
+    const int64_t piece = ((int64_t)blockIdx.x * 2 + slot) * kRows;
+    named_bar_sync(1, kWarps * 32);
+#pragma unroll
+    for (int q4 = 0; q4 < 2 * NT; ++q4) {
+      if (4 * q4 >= heads) break;  // the same for every warp
+      constexpr int kHeads = 4;
+      const int t = q4 / 2;
+      if ((c2 >> 2) == (q4 & 1)) {
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mm = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][8 * t + c2 + i]);
+          f[i] = m[t][i] == -INFINITY ? 0.f : fast_exp2(m[t][i] - mm);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // element of the head dim in row g (+ 8) of this 16-row block
+            const int d = kFp8 ? 16 * i + 2 * g + (e >> 1) : 16 * i + g + 8 * (e >> 1);
+            sm.o[warp][(c2 & 3) + (e & 1)][d] = o[t][i][e] * f[e & 1];
+          }
+      }
+      named_bar_sync(1, kWarps * 32);
+      const int hn = min(kHeads, heads - kHeads * q4);
+      for (int i = threadIdx.x; i < hn * (D / 2); i += kWarps * 32) {
+        const int h = i / (D / 2), d = (i % (D / 2)) * 2;
+        const int r = kHeads * q4 + h;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
+        float ll = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (sm.m[w][r] != -INFINITY) ll = fmaf(sm.l[w][r], fast_exp2(sm.m[w][r] - mm), ll);
+          const float2 u = *reinterpret_cast<const float2*>(&sm.o[w][h][d]);
+          x += u.x;
+          y += u.y;
+        }
+        if (dead) continue;
+        if (whole) {
+          const int64_t at = walk.b * p.hq + h0 + r;
+          const float inv = p.v_scale / ll;
+          const uint32_t pk = p.q_bf16 ? pack_bf16(x * inv, y * inv) : pack_f16(x * inv, y * inv);
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (at * D + d) * 2) = pk;
+          if (d == 0 && p.lse) p.lse[at] = (mm - kShift) * 0.6931471805599453f + logf(ll);
+        } else {
+          *reinterpret_cast<float2*>(p.part_o + (piece + r) * D + d) = make_float2(x, y);
+          if (d == 0) p.part_ml[piece + r] = make_float2(mm - kShift, ll);
+        }
+      }
+      named_bar_sync(1, kWarps * 32);  // the buffers are free again
+    }
+    // A unit that begins here and ends beyond this share: its last tile's block.
+    if (threadIdx.x == 0 && walk.pos + (walk.t_end - walk.t_beg) >= end) {
+      Record r{-1, 0, 0, 0};
+      if (!whole && walk.t_beg == 0) {
+        const int64_t last_tile = walk.pos + walk.span.tiles - 1;
+        r.unit = (int32_t)(walk.b * units + walk.unit);
+        r.last = (int32_t)(((last_tile + 1) * n_blocks + total - 1) / total - 1);
+        r.slot = slot;
+      }
+      p.record[blockIdx.x] = r;
+    }
+  } while (walk.next(p));
+}
+
+// Joins the pieces of each unit that lies in several blocks' shares: one block per
+// (share in which a unit begins, row).
+template <int D>
+__global__ void __launch_bounds__(D / 2) paged_attn_join_kernel(const Params p, int rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Record rec = p.record[blockIdx.x];
+  if (rec.unit < 0) return;
+  const int r = blockIdx.y;
+  const int units = p.hkv * p.head_blocks;
+  const int64_t b = rec.unit / units;
+  const int u = rec.unit - (int)b * units;
+  const int kvh = u / p.head_blocks;
+  const int h0 = kvh * p.group + (u - kvh * p.head_blocks) * rows;
+  if (h0 + r >= (kvh + 1) * p.group) return;
+  const int d = threadIdx.x * 2;
+  const int first = (int)blockIdx.x;
+  float mm = -INFINITY;
+  for (int i = first; i <= rec.last; ++i)
+    mm = fmaxf(mm, p.part_ml[((int64_t)i * 2 + (i == first ? rec.slot : 0)) * rows + r].x);
+  float l = 0.f, x = 0.f, y = 0.f;
+  for (int i = first; i <= rec.last; ++i) {
+    const int64_t at = ((int64_t)i * 2 + (i == first ? rec.slot : 0)) * rows + r;
+    const float2 ml = p.part_ml[at];
+    const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mm);
+    const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + d);
+    l = fmaf(ml.y, f, l);
+    x = fmaf(v.x, f, x);
+    y = fmaf(v.y, f, y);
+  }
+  const int64_t at = b * p.hq + h0 + r;
+  const float inv = p.v_scale / l;
+  const uint32_t pk = p.q_bf16 ? pack_bf16(x * inv, y * inv) : pack_f16(x * inv, y * inv);
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (at * D + d) * 2) = pk;
+  if (d == 0 && p.lse) p.lse[at] = mm * 0.6931471805599453f + logf(l);
+}
+
+template <int kCache, int D, int NT>
+cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                            cudaStream_t stream) {
+  using S = Shape<kCache, D>;
+  constexpr size_t smem = S::kStages * 2 * S::kHalf + sizeof(Smem<S::kWarps, D, NT>);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static_assert(S::kStages <= 32, "barrier arrays");
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(paged_attn_kernel<kCache, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  paged_attn_kernel<kCache, D, NT><<<kGrid, S::kThreads, smem, stream>>>(p, k_map, v_map);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kGrid, 8 * NT);
+  cfg.blockDim = dim3(D / 2);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D>, p, 8 * NT);
+}
+
+template <int kCache>
+cudaError_t launch_cache(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                         cudaStream_t stream) {
+  const bool two = p.group > 8;
+  switch (d) {
+    case 64:
+      return two ? launch_instance<kCache, 64, 2>(p, k_map, v_map, stream)
+                 : launch_instance<kCache, 64, 1>(p, k_map, v_map, stream);
+    case 128:
+      return two ? launch_instance<kCache, 128, 2>(p, k_map, v_map, stream)
+                 : launch_instance<kCache, 128, 1>(p, k_map, v_map, stream);
+    default:
+      return two ? launch_instance<kCache, 256, 2>(p, k_map, v_map, stream)
+                 : launch_instance<kCache, 256, 1>(p, k_map, v_map, stream);
+  }
+}
+
+cudaError_t read_errors_here(uint32_t* word) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_paged_attn_err, sizeof(uint32_t));
+  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_paged_attn_err, &zero, sizeof(uint32_t));
+}
+
+}  // namespace
+
+}  // namespace pa
+}  // namespace gqa

@@ -1,0 +1,55 @@
+// paged_attn_host.h -- what the host side and the kernels of the one-token
+// paged attention share.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+
+namespace gqa {
+namespace pa {
+
+constexpr int kGrid = 152;  // blocks: one per SM
+
+// Tokens per ring stage, from the bytes of a token's row: 16 to 32 KB of K and V a stage.
+constexpr int tile_of(int row_bytes) { return row_bytes > 256 ? 32 : 64; }
+
+// One record per block: the unit that begins in the block's share and ends
+// beyond it, and the last block that holds a piece of it.
+struct Record {
+  int32_t unit;  // (sequence * hkv + kv head) * head blocks + head block; -1: none
+  int32_t last;
+  int32_t slot;  // which of the block's two pieces
+  int32_t pad;
+};
+
+struct Params {
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  float* part_o;     // [kGrid][2][kRows][D]
+  float2* part_ml;   // [kGrid][2][kRows]
+  Record* record;    // [kGrid]
+  int64_t q_seq, q_head, batch, num_pages, max_pages;
+  int hq, hkv, group, head_blocks, page_size, box;  // box: tokens of one copy
+  int q_bf16;
+  float scale_log2;  // scores to the exp2 domain
+  float cap_in, cap_out;  // softcap: s2 = cap_out * tanh, tanh's argument doubled in the exp2 domain = cap_in * score; cap_out 0: none
+  float v_scale;
+  int window, starve;
+};
+
+// The instances of one cache type, each in a translation unit of its own.
+cudaError_t launch_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_bf16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_e4m3(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t read_errors_f16(uint32_t* word);
+cudaError_t read_errors_bf16(uint32_t* word);
+cudaError_t read_errors_e4m3(uint32_t* word);
+
+}  // namespace pa
+}  // namespace gqa

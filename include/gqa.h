@@ -79,7 +79,8 @@ typedef enum gqa_dtype {
   GQA_E4M3 = 2,  /* OCP FP8 E4M3 ("fn") bytes */
   GQA_U8 = 3,    /* bytes: packed E2M1 pairs, or E4M3 codes given as raw bytes */
   GQA_I32 = 4,
-  GQA_F32 = 5
+  GQA_F32 = 5,
+  GQA_BF16 = 6   /* bfloat16 */
 } gqa_dtype;
 
 typedef struct gqa_tensor {
@@ -331,6 +332,129 @@ gqa_status gqa_set_ctx_grid(int mode);
 gqa_status gqa_debug_dequant_pages(const void* fp4, const void* sf, const int32_t* block_table,
                                    const int32_t* kv_lens, void* out_e4m3, int64_t batch, int64_t num_pages,
                                    int64_t max_pages_per_seq, int64_t max_kv, gqa_stream_t stream);
+
+/*
+ * gqa_paged_append_t -- rotary position embedding of new query and key rows,
+ * and the append of the new keys and values to a paged K/V cache.  (An
+ * addition of this library, like the two entry points after it: they fill and
+ * read caches of other head counts, head dims, page sizes, element types and
+ * memory orders than the entry points above take.)
+ *
+ * The new tokens of a batch lie one sequence after the other.  Token t of
+ * sequence b (qo_indptr[b] <= t < qo_indptr[b+1]) has the position
+ *   pos = kv_lens[b] - (qo_indptr[b+1] - t)
+ * (kv_lens counts the new tokens: the lengths that the attention of the same
+ * step is given) and goes to page block_table[b, pos / page_size], slot
+ * pos % page_size.  The first `rot` elements of each q and k head are rotated
+ * with the cosines c = rope[pos, 0 .. rot/2) and sines s = rope[pos, rot/2 ..
+ * rot):  (x, y) -> (x c - y s, y c + x s) over the pairs (i, i + rot/2), or
+ * (2i, 2i + 1) if `interleaved`.  Everything is computed in f32 and rounded
+ * once.  E4M3 pages store round-to-nearest-even, saturating values of
+ * k * (1 / k_scale) and v * (1 / v_scale), the reciprocals in f32.
+ *
+ *   q            [total, q_heads, d]  f16 or bf16, or NULL (then q_out is NULL
+ *                too: keys and values only)
+ *   k, v         [total, kv_heads, d]  the same type
+ *   k_pages, v_pages  [num_pages, kv_heads, page_size, d]  the same type, or
+ *                E4M3 (GQA_E4M3 or GQA_U8), written
+ *   block_table  [batch, max_pages_per_seq]  int32
+ *   kv_lens      [batch]  int32
+ *   qo_indptr    [batch + 1]  int32, or NULL: one token per sequence (total =
+ *                batch)
+ *   rope         [positions, rot]  f32, or NULL: nothing is rotated
+ *   q_out        [total, q_heads, d]  q's type, written; may be q itself
+ *   d            64, 128 or 256; 1 .. 1024 heads; any page_size; rot a multiple
+ *                of 16, at most d
+ *   k_scale, v_scale  finite, > 0; 1 for pages of the inputs' type
+ *
+ * Strides.  q, k, v, q_out and the pages may have any strides that are
+ * multiples of 16 bytes as long as the last dimension is dense (slices of a
+ * fused projection; token-major pages given as a permuted view); what is
+ * written must not overlap itself.  Every other tensor is dense.
+ *
+ * Rows left alone.  Tokens at and behind qo_indptr[batch] (a padded batch) and
+ * tokens of negative position (a sequence with kv_lens[b] = 0) are skipped:
+ * nothing of them is written, in q_out neither.  A token whose position lies
+ * outside the block table or the rope table, or whose page lies outside [0,
+ * num_pages), is skipped too and bit 1 of the error word
+ * (gqa_check_device_errors) is set; offsets that are not non-decreasing from 0
+ * to at most `total` set bit 2, and nothing out of range is read or written.
+ * Two tokens that share a slot leave either's row.  No workspace; nothing is
+ * synchronised.  Host tensors are refused (GQA_ERR_UNSUPPORTED): a cache that
+ * lives on the host has nothing to be appended to on the device.
+ */
+gqa_status gqa_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, gqa_tensor* k_pages,
+                              gqa_tensor* v_pages, const gqa_tensor* block_table, const gqa_tensor* kv_lens,
+                              const gqa_tensor* qo_indptr, const gqa_tensor* rope, gqa_tensor* q_out, int interleaved,
+                              float k_scale, float v_scale, gqa_stream_t stream);
+
+/*
+ * nvfp4_paged_append_t -- gqa_paged_append_t into the NVFP4 pages that
+ * nvfp4_paged_ctx_attn reads; the rotated queries leave as the E4M3 values it
+ * takes:
+ *   sf    = E4M3_rne_sat(amax / 6) of each 16 elements of a k or v head,
+ *   codes = E2M1_rne_sat(x / sf), all 0 where sf is 0 or NaN,
+ *   q_out = E4M3_rne_sat(q * (1 / q_scale)), the reciprocal in f32.
+ * The divisions are true f32 divisions.  A block that holds a NaN gets a NaN
+ * scale; an infinity gets the largest scale and code.  q_scale is then the
+ * attention's q_scale.
+ *
+ *   q      [total, 32, 128], k, v [total, 8, 128]  f16 or bf16, strided as above
+ *   k_fp4, v_fp4  [num_pages, 8, 64, 64]  uint8, k_sf, v_sf [num_pages, 8, 64,
+ *          8]  E4M3 (or uint8), dense, written
+ *   q_out  [total, 32, 128]  E4M3 (or uint8), written; strides multiples of 16
+ *          bytes
+ *   rot    a multiple of 32
+ * The other arguments, and what is skipped, as above (qo_indptr may be NULL).
+ */
+gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, gqa_tensor* k_fp4,
+                                gqa_tensor* k_sf, gqa_tensor* v_fp4, gqa_tensor* v_sf, const gqa_tensor* block_table,
+                                const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens, const gqa_tensor* rope,
+                                gqa_tensor* q_out, int interleaved, float q_scale, gqa_stream_t stream);
+
+/*
+ * gqa_paged_attn_t -- attention of one new token per sequence over a paged K/V
+ * cache, split over the cache's length and joined:
+ *
+ *   s_t = (q[b,h,:] . K_t) * q_scale * k_scale / sqrt(d),   K_t of KV head
+ *         h / (q_heads / kv_heads), token t of sequence b
+ *   s_t = softcap * tanh(s_t / softcap)  if softcap > 0
+ *   out[b,h,:] = v_scale * sum_t softmax_t(s) V_t,  lse[b,h] = ln sum_t exp(s_t)
+ *   over max(0, len_b - window) <= t < len_b (window = 0: from 0),
+ *   len_b = clamp(seq_lens[b], 0, page_size * max_pages_per_seq)
+ *
+ *   q            [batch, q_heads, d]  f16 or bf16; strides multiples of 16 bytes,
+ *                last dimension dense
+ *   k_pages, v_pages  [num_pages, kv_heads, page_size, d]  q's type, or E4M3
+ *                (GQA_E4M3 or GQA_U8); strides as gqa_paged_append_t's
+ *   block_table  [batch, max_pages_per_seq]  int32; only the entries of pages
+ *                that hold a visible token are read
+ *   seq_lens     [batch]  int32, read on the device
+ *   out          [batch, q_heads, d]  q's type, dense, written
+ *   lse          [batch, q_heads]  f32, dense, written; or NULL
+ *   workspace    device memory of at least gqa_paged_attn_workspace(q_heads,
+ *                kv_heads, d) bytes, 16-byte aligned; its contents mean nothing
+ *                before or after a call.  The caller owns it: calls that can run
+ *                at the same time (on two streams, in two graphs) need one each
+ *   batch 1 .. 65535; d 64, 128 or 256; 1 .. 1024 query heads, a multiple of the
+ *   kv_heads; page_size 16, 32, 64, 128 or 256; page_size * max_pages_per_seq at
+ *   most 2^30
+ *
+ * A sequence of length 0 produces a zero row and lse = -infinity.  Slots outside
+ * the visible tokens may hold anything, NaN too.  A page outside [0, num_pages)
+ * is not read: page 0 is used instead and bit 1 of the error word is set.  The
+ * split is chosen on the device from the lengths, so a captured call stays
+ * balanced when they change.  Two kernels; host tensors are refused
+ * (GQA_ERR_UNSUPPORTED).
+ */
+gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, const gqa_tensor* v_pages,
+                            const gqa_tensor* block_table, const gqa_tensor* seq_lens, gqa_tensor* out, gqa_tensor* lse,
+                            float q_scale, float k_scale, float v_scale, int window, float softcap, void* workspace,
+                            int64_t workspace_bytes, gqa_stream_t stream);
+
+/* Bytes of workspace that gqa_paged_attn_t needs for a head layout, whatever the
+ * batch and the lengths (0 for one that it does not take). */
+int64_t gqa_paged_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t d);
 
 /*
  * gqa_check_device_errors -- synchronise `device` and return (then clear)
