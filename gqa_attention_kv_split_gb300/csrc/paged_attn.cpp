@@ -41,7 +41,9 @@ cudaError_t make_map(const void* pages, const PagedAttnArgs& a, int64_t s_page, 
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(pages), dims, strides, boxes, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE,
                               chunk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              // (rows of one head apart: what lies behind 128 bytes may be another head's)
+                              s_slot == a.d ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -77,8 +79,11 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   p.hq = a.hq;
   p.hkv = a.hkv;
   p.head_blocks = (p.group + rows - 1) / rows;
-  p.page_size = a.page_size;
-  p.box = a.page_size < tile ? a.page_size : tile;
+  const int box = a.page_size < tile ? a.page_size : tile;
+  for (p.page_shift = 0; (1 << p.page_shift) < a.page_size; ++p.page_shift) {
+  }
+  for (p.box_shift = 0; (1 << p.box_shift) < box; ++p.box_shift) {
+  }
   p.q_bf16 = a.q_bf16;
   const double log2e = 1.4426950408889634;
   p.scale_log2 = (float)(a.scale * log2e);
@@ -89,8 +94,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   p.starve = a.starve;
   CUtensorMap k_map, v_map;
   cudaError_t e;
-  if ((e = make_map(a.k_pages, a, a.kp_page, a.kp_head, a.kp_slot, p.box, &k_map)) != cudaSuccess) return e;
-  if ((e = make_map(a.v_pages, a, a.vp_page, a.vp_head, a.vp_slot, p.box, &v_map)) != cudaSuccess) return e;
+  if ((e = make_map(a.k_pages, a, a.kp_page, a.kp_head, a.kp_slot, box, &k_map)) != cudaSuccess) return e;
+  if ((e = make_map(a.v_pages, a, a.vp_page, a.vp_head, a.vp_slot, box, &v_map)) != cudaSuccess) return e;
   switch (a.cache) {
     case kCacheF16: return pa::launch_f16(p, a.d, k_map, v_map, stream);
     case kCacheBf16: return pa::launch_bf16(p, a.d, k_map, v_map, stream);

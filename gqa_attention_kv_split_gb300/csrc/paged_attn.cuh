@@ -27,9 +27,9 @@
 //  * A producer warp moves tiles of 64 (32) tokens with tensor-map TMA copies
 //    into a ring of about 190 KB: any page size and cache order is a box of the
 //    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
-//  * Eight consumer warps (four at head dim 256), each with its own 16 keys of a tile and its own
-//    (m, l, o); groups of warps take alternate tiles, so that one tile's softmax
-//    overlaps the next one's products.  They meet at the end of a unit only.
+//  * Eight consumer warps (four at head dim 256), each with its own 32 keys of a tile and its own
+//    (m, l, o); groups of warps take tiles in turn, so that one tile's softmax
+//    overlaps another one's products.  They meet at the end of a unit only.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -51,7 +51,7 @@ __device__ uint32_t g_paged_attn_err;  // of this translation unit's kernels
 }  // namespace
 
 
-template <int kCache, int D>
+template <int kCache, int D, int NT>
 struct Shape {
   static constexpr int kEsz = kCache == kCacheE4m3 ? 1 : 2;
   static constexpr int kRow = D * kEsz;                     // bytes of a token's row
@@ -62,7 +62,12 @@ struct Shape {
   // registers a thread that nine warps leave.
   static constexpr int kWarps = D > 128 ? 4 : 8;
   static constexpr int kThreads = (kWarps + 1) * 32;
-  static constexpr int kGroupWarps = kTile / 16;            // warps that share a tile
+  // 16-key blocks that a warp takes of a tile: two give it two independent sums of
+  // products and one reduction for 32 keys (1.28x over one block on 48 sequences of up
+  // to 16001 tokens in E4M3 pages of 64); with 16 heads and long rows the registers that the second one
+  // needs would spill (64 x 8192 tokens in bf16, 16 heads a KV head: 234 us with two, 210 with one).
+  static constexpr int kBlocks = NT == 2 && D > 64 ? 1 : 2;
+  static constexpr int kGroupWarps = kTile / (16 * kBlocks);  // warps that share a tile
   static constexpr int kGroups = kWarps / kGroupWarps;      // tiles in work at a time
   static constexpr int kHalf = kTile * kRow;                // bytes of K (and of V) of a stage
   static constexpr int kRoom = D > 128 ? 128 * 1024 : 192 * 1024;  // the join's buffers take the rest
@@ -146,7 +151,7 @@ template <int kTile>
 struct Span {
   int len, first, tile0, tiles;
   __device__ __forceinline__ Span(const Params& p, int64_t b) {
-    const int64_t cap = p.max_pages * p.page_size;
+    const int64_t cap = p.max_pages << p.page_shift;
     const int64_t n = p.seq_lens[b];
     len = (int)(n < 0 ? 0 : (n > cap ? cap : n));
     first = p.window > 0 && len > p.window ? len - p.window : 0;
@@ -194,14 +199,15 @@ struct Walk {
 namespace {
 
 template <int kCache, int D, int NT>
-__global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     paged_attn_kernel(const Params p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   uint32_t* const err = &g_paged_attn_err;
-  using S = Shape<kCache, D>;
+  using S = Shape<kCache, D, NT>;
   constexpr bool kBf16 = kCache == kCacheBf16;
   constexpr bool kFp8 = kCache == kCacheE4m3;
   constexpr int kTile = S::kTile, kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr int kRows = 8 * NT;
+  constexpr int kTileShift = kTile == 32 ? 5 : kTile == 64 ? 6 : 7;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = smem_raw;
   Smem<S::kWarps, D, NT>& sm = *reinterpret_cast<Smem<S::kWarps, D, NT>*>(smem_raw + S::kStages * 2 * S::kHalf);
@@ -285,11 +291,14 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
     // ---------------- producer ------------------------------------------------
     if (p.starve) return;
     const uint64_t pol = p.head_blocks == 1 ? policy_evict_first() : policy_evict_last();
-    const int box = p.box;
-    const int boxes = kTile / box;  // copies per tile of K (and of V)
-    const uint32_t box_bytes = (uint32_t)box * S::kRow;
-    int64_t n = 0;  // tiles issued
-    int seg = 0;    // pieces begun
+    // (a box and a page are powers of two: the loop below has no division)
+    const int box_shift = p.box_shift, page_shift = p.page_shift;
+    const int boxes = kTile >> box_shift;  // copies per tile of K (and of V)
+    const uint32_t box_bytes = (uint32_t)S::kRow << box_shift;
+    const uint32_t lane_dst = smem_u32(ring) + lane * box_bytes;
+    int st = 0, ph = 1;  // stage, and the parity of the phase that frees it (the first one is free)
+    int issued = 0;      // stages issued, up to all of them
+    int seg = 0;         // pieces begun
     bool ok = true;
     do {
       const int kvh = walk.unit / p.head_blocks;
@@ -307,27 +316,25 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
       ++seg;
       // Page numbers, 32 copies' worth at a time and one such group ahead (lane l has those of copy l).
       const int32_t* row = p.block_table + walk.b * p.max_pages;
-      const int c0 = (walk.span.tile0 + walk.t_beg) * boxes;       // first copy, counted from the sequence's first token
-      const int c_end = (walk.span.len + box - 1) / box;           // copies behind the last token are not made
-      const int c_first = walk.span.first / box;                   // nor those before the window
-      auto page_of = [&](int c) {
-        if (c < c_first || c >= c_end) return 0;
-        int g = row[(int64_t)c * box / p.page_size];
+      int c = ((walk.span.tile0 + walk.t_beg) << (kTileShift - box_shift)) + lane;  // this lane's copy, counted from the sequence's first token
+      const int c_end = ((walk.span.len - 1) >> box_shift) + 1;                     // copies behind the last token are not made
+      const int c_first = walk.span.first >> box_shift;                             // nor those before the window
+      auto page_of = [&](int copy) {
+        if (copy < c_first || copy >= c_end) return 0;
+        int g = row[copy >> (page_shift - box_shift)];
         if (g < 0 || g >= p.num_pages) {
           atomicOr(err, kErrBadIndex);
           g = 0;
         }
         return g;
       };
-      int cur = page_of(c0 + lane), nxt = page_of(c0 + 32 + lane);
-      int at = 0;  // copies of this piece so far
-      for (int t = walk.t_beg; t < walk.t_end; ++t, ++n) {
-        const int st = (int)(n % S::kStages);
-        if (n >= S::kStages && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.empty[st]), (int)(n / S::kStages - 1) & 1, err))) {
+      int cur = page_of(c), nxt = page_of(c + 32);
+      int at = 0;  // copies of this piece so far, within a group of 32
+      for (int t = walk.t_beg; t < walk.t_end; ++t) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.empty[st]), ph, err))) {
           ok = false;
           break;
         }
-        const int c = c0 + at + lane;
         const int pg = __shfl_sync(0xffffffffu, cur, (at + lane) & 31);
         const bool live = lane < boxes && c >= c_first && c < c_end;
         const uint32_t bar = smem_u32(&sm.full[st]);
@@ -335,22 +342,29 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();
         if (live) {
-          const uint32_t dst = smem_u32(ring) + st * 2 * S::kHalf + lane * box_bytes;
-          const int slot = (int)((int64_t)c * box % p.page_size);
+          const uint32_t dst = lane_dst + st * 2 * S::kHalf;
+          const int slot = (c << box_shift) & ((1 << page_shift) - 1);
           tma_5d(dst, &k_map, slot, kvh, pg, bar, pol);
           tma_5d(dst + S::kHalf, &v_map, slot, kvh, pg, bar, pol);
         }
+        c += boxes;
         at += boxes;
-        if ((at & 31) == 0) {
+        if (at == 32) {
+          at = 0;
           cur = nxt;
-          nxt = page_of(c0 + at + 32 + lane);
+          nxt = page_of(c + 32);
+        }
+        issued = min(issued + 1, S::kStages);
+        if (++st == S::kStages) {
+          st = 0;
+          ph ^= 1;
         }
       }
     } while (ok && walk.next(p));
     // No copy may land after the block has gone.
     if (lane == 0) {
-      for (int64_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
-        mbar_wait(smem_u32(&sm.full[i % S::kStages]), (int)(i / S::kStages) & 1, err);
+      // (stages before st were last filled in the present round, the others in the one before)
+      for (int i = 0; i < issued; ++i) mbar_wait(smem_u32(&sm.full[i]), i < st ? ph ^ 1 : ph, err);
       for (int i = seg > 2 ? seg - 2 : 0; i < seg; ++i) mbar_wait(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1, err);
     }
     return;
@@ -358,12 +372,18 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
 
   // ---------------- consumers --------------------------------------------------
   const int grp = warp / S::kGroupWarps;
-  const int row0 = (warp % S::kGroupWarps) * 16;  // this warp's keys of a tile
+  constexpr int kBlocks = S::kBlocks, kKeys = 16 * kBlocks;
+  const int row0 = (warp % S::kGroupWarps) * kKeys;  // this warp's keys of a tile
   const int g = lane >> 2, c2 = (lane & 3) * 2;
   const uint32_t ring_u = smem_u32(ring);
-  // 16-key block of a copy: the copy's base and this warp's first row in it
-  const int box = p.box;
-  const uint32_t blk = (uint32_t)(row0 / box) * box * S::kRow + (uint32_t)(row0 % box) * S::kChunk;
+  // This warp's 16-key blocks: the base of the block's copy and its first row in it
+  const int box = 1 << p.box_shift;
+  uint32_t blk[kBlocks];
+#pragma unroll
+  for (int j = 0; j < kBlocks; ++j) {
+    const int r = row0 + 16 * j;
+    blk[j] = (uint32_t)(r / box) * box * S::kRow + (uint32_t)(r % box) * S::kChunk;
+  }
   const uint32_t chunk_step = (uint32_t)box * S::kChunk;
   // ldmatrix row of this lane: K rows 0-15 (A operand), V rows 0-15 (transposed A operand)
   const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -378,7 +398,8 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   // P keeps f16's full precision down to 2^-28 of the largest weight.
   constexpr float kShift = kBf16 ? 0.f : 14.f;
 
-  int64_t n = 0;
+  int st = grp, ph = 0;  // this group's next stage and the parity that fills it
+  int skip = grp;        // tiles to this group's next one
   int seg = 0;
   bool dead = false;  // a wait has expired: nothing more is waited for or computed
   do {
@@ -454,76 +475,87 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
       l[t][0] = l[t][1] = 0.f;
     }
 
-    for (int tile = walk.t_beg; tile < walk.t_end; ++tile, ++n) {
-      if ((int)(n % S::kGroups) != grp || dead) continue;
-      const int st = (int)(n % S::kStages);
+    int tile = walk.t_beg + skip;
+    for (; tile < walk.t_end; tile += S::kGroups) {
+      if (dead) continue;
       const int key0 = (walk.span.tile0 + tile) * kTile + row0;  // this warp's first key
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), (int)(n / S::kStages) & 1, err))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), ph, err))) {
         dead = true;
         continue;
       }
-      const uint32_t kb = ring_u + st * 2 * S::kHalf + blk, vb = kb + S::kHalf;
-      if (key0 < walk.span.len && key0 + 16 > walk.span.first) {
-        const bool edge = key0 + 16 > walk.span.len || key0 < walk.span.first;
-        // ---- S^T = K Q^T, in two sums (even and odd steps)
-        float s[NT][2][4];
+      const uint32_t kb = ring_u + st * 2 * S::kHalf, vb = kb + S::kHalf;
+      if (key0 < walk.span.len && key0 + kKeys > walk.span.first) {
+        const bool edge = key0 + kKeys > walk.span.len || key0 < walk.span.first;
+        // ---- S^T = K Q^T
+        float s[kBlocks][NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[t][i][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[j][t][e] = 0.f;
         if (!kFp8) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            uint32_t a[4];
-            ldsm4(a, kb + col(k_row, 2 * k + k_sel));
+          for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma<kBf16>(s[t][k & 1], a, qf[t][k][0], qf[t][k][1]);
-          }
+            for (int j = 0; j < kBlocks; ++j) {
+              uint32_t a[4];
+              ldsm4(a, kb + blk[j] + col(k_row, 2 * k + k_sel));
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma<kBf16>(s[j][t], a, qf[t][k][0], qf[t][k][1]);
+            }
         } else {
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t w[4];
-            ldsm4(w, kb + col(k_row, 2 * k + k_sel));
+          for (int k = 0; k < D / 32; ++k)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t a[4] = {e4m3_to_f16x2(w[2 * i] & 0xffffu), e4m3_to_f16x2(w[2 * i + 1] & 0xffffu),
-                                     e4m3_to_f16x2(w[2 * i] >> 16), e4m3_to_f16x2(w[2 * i + 1] >> 16)};
+            for (int j = 0; j < kBlocks; ++j) {
+              uint32_t w[4];
+              ldsm4(w, kb + blk[j] + col(k_row, 2 * k + k_sel));
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma<false>(s[t][i], a, qf[t][2 * k + i][0], qf[t][2 * k + i][1]);
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t a[4] = {e4m3_to_f16x2(w[2 * i] & 0xffffu), e4m3_to_f16x2(w[2 * i + 1] & 0xffffu),
+                                       e4m3_to_f16x2(w[2 * i] >> 16), e4m3_to_f16x2(w[2 * i + 1] >> 16)};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma<false>(s[j][t], a, qf[t][2 * k + i][0], qf[t][2 * k + i][1]);
+              }
             }
-          }
         }
         if (edge) {
           // V rows outside the sequence may hold anything; 0 * NaN is NaN, so they are zeroed.
-          for (int i = lane; i < 16 * (S::kRow / 16); i += 32) {
-            const int r = i % 16, c16 = i / 16;
-            if (key0 + r >= walk.span.len || key0 + r < walk.span.first)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + col(r, c16)), "r"(0) : "memory");
-          }
+#pragma unroll
+          for (int j = 0; j < kBlocks; ++j)
+            for (int i = lane; i < 16 * (S::kRow / 16); i += 32) {
+              const int r = i % 16, c16 = i / 16, key = key0 + 16 * j + r;
+              if (key >= walk.span.len || key < walk.span.first)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + blk[j] + col(r, c16)), "r"(0) : "memory");
+            }
           __syncwarp();
         }
-        // ---- softmax weights: rows (keys) g, g + 8; columns (heads) c2, c2 + 1
-        uint32_t pb[NT][2], pl[NT][2];
+        // ---- softmax weights: rows (keys) g, g + 8 of each block; columns (heads) c2, c2 + 1
+        uint32_t pb[kBlocks][NT][2], pl[kBlocks][NT][2];
         float alpha[NT][2];
         bool grow = false;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = (s[t][0][e] + s[t][1][e]) * sc[t][e & 1];
-            if (p.cap_out != 0.f) v[e] = p.cap_out * (1.f - __fdividef(2.f, fast_exp2(v[e]) + 1.f));
-          }
-          if (edge) {
-            const int ka = key0 + g, kc = ka + 8;
-            if (ka >= walk.span.len || ka < walk.span.first) v[0] = v[1] = -INFINITY;
-            if (kc >= walk.span.len || kc < walk.span.first) v[2] = v[3] = -INFINITY;
+          for (int j = 0; j < kBlocks; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& v = s[j][t][e];
+              v *= sc[t][e & 1];
+              if (p.cap_out != 0.f) v = p.cap_out * (1.f - __fdividef(2.f, fast_exp2(v) + 1.f));
+            }
+            if (edge) {
+              const int ka = key0 + 16 * j + g, kc = ka + 8;
+              if (ka >= walk.span.len || ka < walk.span.first) s[j][t][0] = s[j][t][1] = -INFINITY;
+              if (kc >= walk.span.len || kc < walk.span.first) s[j][t][2] = s[j][t][3] = -INFINITY;
+            }
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = fmaxf(v[i], v[i + 2]);
+            float x = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j) x = fmaxf(x, fmaxf(s[j][t][i], s[j][t][i + 2]));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -532,22 +564,31 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
             grow |= mn != m[t][i];
             alpha[t][i] = fast_exp2(m[t][i] - sub);
             m[t][i] = mn;
-            v[i] = fast_exp2(v[i] - sub + kShift);
-            v[i + 2] = fast_exp2(v[i + 2] - sub + kShift);
-            l[t][i] = fmaf(l[t][i], alpha[t][i], v[i] + v[i + 2]);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j) {
+              s[j][t][i] = fast_exp2(s[j][t][i] - sub + kShift);
+              s[j][t][i + 2] = fast_exp2(s[j][t][i + 2] - sub + kShift);
+              sum += s[j][t][i] + s[j][t][i + 2];
+            }
+            l[t][i] = fmaf(l[t][i], alpha[t][i], sum);
           }
           // P^T as the B operand of O^T = V^T P^T: rows = keys, columns = heads.  A bf16
           // weight is split into two bf16 terms (16 bits of it are kept); an f16 weight is
           // rounded once, to 11 bits.
-          if (kBf16) {
-            const uint32_t x0 = pack_bf16(v[0], v[1]), x1 = pack_bf16(v[2], v[3]);
-            pb[t][0] = movm_t(x0);
-            pb[t][1] = movm_t(x1);
-            pl[t][0] = movm_t(pack_bf16(v[0] - bf16_lo(x0), v[1] - bf16_hi(x0)));
-            pl[t][1] = movm_t(pack_bf16(v[2] - bf16_lo(x1), v[3] - bf16_hi(x1)));
-          } else {
-            pb[t][0] = movm_t(pack_f16(v[0], v[1]));
-            pb[t][1] = movm_t(pack_f16(v[2], v[3]));
+#pragma unroll
+          for (int j = 0; j < kBlocks; ++j) {
+            const float* v = s[j][t];
+            if (kBf16) {
+              const uint32_t x0 = pack_bf16(v[0], v[1]), x1 = pack_bf16(v[2], v[3]);
+              pb[j][t][0] = movm_t(x0);
+              pb[j][t][1] = movm_t(x1);
+              pl[j][t][0] = movm_t(pack_bf16(v[0] - bf16_lo(x0), v[1] - bf16_hi(x0)));
+              pl[j][t][1] = movm_t(pack_bf16(v[2] - bf16_lo(x1), v[3] - bf16_hi(x1)));
+            } else {
+              pb[j][t][0] = movm_t(pack_f16(v[0], v[1]));
+              pb[j][t][1] = movm_t(pack_f16(v[2], v[3]));
+            }
           }
         }
         if (__any_sync(0xffffffffu, grow)) {
@@ -561,36 +602,46 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         // ---- O^T += V^T P^T
         if (!kFp8) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t a[4];
-            ldsm4_t(a, vb + col(v_row, 2 * i + v_sel));
+          for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              mma<kBf16>(o[t][i], a, pb[t][0], pb[t][1]);
-              if (kBf16) mma<kBf16>(o[t][i], a, pl[t][0], pl[t][1]);
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t a[4];
+              ldsm4_t(a, vb + blk[j] + col(v_row, 2 * i + v_sel));
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                mma<kBf16>(o[t][i], a, pb[j][t][0], pb[j][t][1]);
+                if (kBf16) mma<kBf16>(o[t][i], a, pl[j][t][0], pl[j][t][1]);
+              }
             }
-          }
         } else {
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t w[4];
-            ldsm4_t(w, vb + col(v_row, 2 * k + v_sel));
+          for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              // two keys of two neighbouring elements -> the two keys of each element
-              const uint32_t lo = __byte_perm(w[2 * i], 0u, 0x3120), hi = __byte_perm(w[2 * i + 1], 0u, 0x3120);
-              const uint32_t a[4] = {e4m3_to_f16x2(lo & 0xffffu), e4m3_to_f16x2(lo >> 16), e4m3_to_f16x2(hi & 0xffffu),
-                                     e4m3_to_f16x2(hi >> 16)};
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t w[4];
+              ldsm4_t(w, vb + blk[j] + col(v_row, 2 * k + v_sel));
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma<false>(o[t][2 * k + i], a, pb[t][0], pb[t][1]);
+              for (int i = 0; i < 2; ++i) {
+                // two keys of two neighbouring elements -> the two keys of each element
+                const uint32_t lo = __byte_perm(w[2 * i], 0u, 0x3120), hi = __byte_perm(w[2 * i + 1], 0u, 0x3120);
+                const uint32_t a[4] = {e4m3_to_f16x2(lo & 0xffffu), e4m3_to_f16x2(lo >> 16), e4m3_to_f16x2(hi & 0xffffu),
+                                       e4m3_to_f16x2(hi >> 16)};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma<false>(o[t][2 * k + i], a, pb[j][t][0], pb[j][t][1]);
+              }
             }
-          }
         }
         if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
+      st += S::kGroups;
+      if (st >= S::kStages) {
+        st = grp;
+        ph ^= 1;
+      }
     }
+    skip = tile - walk.t_end;
 
     // ---- join the warps --------------------------------------------------
 #pragma unroll
@@ -715,7 +766,7 @@ __global__ void __launch_bounds__(D / 2) paged_attn_join_kernel(const Params p, 
 template <int kCache, int D, int NT>
 cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
                             cudaStream_t stream) {
-  using S = Shape<kCache, D>;
+  using S = Shape<kCache, D, NT>;
   constexpr size_t smem = S::kStages * 2 * S::kHalf + sizeof(Smem<S::kWarps, D, NT>);
   static_assert(smem <= 227 * 1024, "shared memory");
   static_assert(S::kStages <= 32, "barrier arrays");

@@ -35,7 +35,8 @@ struct Params {
   float2* part_ml;   // [kGrid][2][kRows]
   Record* record;    // [kGrid]
   int64_t q_seq, q_head, batch, num_pages, max_pages;
-  int hq, hkv, group, head_blocks, page_size, box;  // box: tokens of one copy
+  int hq, hkv, group, head_blocks;
+  int page_shift, box_shift;  // log2 of a page's tokens, and of those of one copy
   int q_bf16;
   float scale_log2;  // scores to the exp2 domain
   float cap_in, cap_out;  // softcap: s2 = cap_out * tanh, tanh's argument doubled in the exp2 domain = cap_in * score; cap_out 0: none
