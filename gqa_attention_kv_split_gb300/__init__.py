@@ -23,6 +23,9 @@ missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -243,9 +246,31 @@ def nvfp4_paged_ctx_attn(q_fp8, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr
     return out
 
 
-def _opt(t, name: str):
-    """Reference to a descriptor, or NULL for None."""
-    return None if t is None else _ref(_desc(t, name))
+_binding_module = None
+
+
+def _binding():
+    """The compiled marshalling of the paged-cache calls (csrc/binding.c), bound to the loaded library."""
+    global _binding_module
+    if _binding_module is None:
+        L = lib()
+        with _lock:
+            if _binding_module is None:
+                path = os.path.join(_HERE, "_binding.so")
+                if not os.path.exists(path):
+                    raise RuntimeError(f"_binding.so is not built ({path}); call gqa_attention_kv_split_gb300.build() first")
+                loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+                m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+                loader.exec_module(m)
+                m.setup(torch.Tensor, _raw_stream, tuple(_DTYPES.items()),
+                        tuple(ctypes.cast(f, ctypes.c_void_p).value
+                              for f in (L.gqa_paged_append_t, L.nvfp4_paged_append_t, L.gqa_paged_attn_t)))
+                _binding_module = m
+    return _binding_module
+
+
+# The handle of a device's current stream, without the stream object that torch.cuda.current_stream builds (2 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
 def gqa_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, *, qo_indptr=None, rope=None,
@@ -262,10 +287,10 @@ def gqa_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, *, qo_indp
     """
     if q is not None and q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    _check(lib().gqa_paged_append_t(
-        _opt(q, "q"), _opt(k, "k"), _opt(v, "v"), _opt(k_pages, "k_pages"), _opt(v_pages, "v_pages"),
-        _opt(block_table, "block_table"), _opt(kv_lens, "kv_lens"), _opt(qo_indptr, "qo_indptr"), _opt(rope, "rope"),
-        _opt(q_out, "q_out"), 1 if interleaved else 0, float(k_scale), float(v_scale), _stream_for(k)))
+    st = _binding().append(q, k, v, k_pages, v_pages, block_table, kv_lens, qo_indptr, rope, q_out, interleaved, k_scale,
+                           v_scale)
+    if st:
+        _check(st)
     return q_out
 
 
@@ -277,13 +302,14 @@ def nvfp4_paged_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr
     codes (or writes `q_out`; None without q)."""
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=torch.uint8, device=q.device)
-    _check(lib().nvfp4_paged_append_t(
-        _opt(q, "q"), _opt(k, "k"), _opt(v, "v"), _opt(k_fp4, "k_fp4"), _opt(k_sf, "k_sf"), _opt(v_fp4, "v_fp4"),
-        _opt(v_sf, "v_sf"), _opt(block_table, "block_table"), _opt(qo_indptr, "qo_indptr"), _opt(kv_lens, "kv_lens"),
-        _opt(rope, "rope"), _opt(q_out, "q_out"), 1 if interleaved else 0, float(q_scale), _stream_for(k)))
+    st = _binding().nvfp4_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, rope, q_out, interleaved,
+                                 q_scale)
+    if st:
+        _check(st)
     return q_out
 
 
+@functools.lru_cache(maxsize=None)
 def gqa_paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int) -> int:
     """Bytes of workspace of a gqa_paged_attn call, whatever its batch and lengths."""
     return int(lib().gqa_paged_attn_workspace(int(q_heads), int(kv_heads), int(head_dim)))
@@ -303,11 +329,10 @@ def gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=
     if workspace is None and q.is_cuda and q.dim() == 3 and k_pages.dim() == 4:
         workspace = torch.empty(gqa_paged_attn_workspace(q.shape[1], k_pages.shape[1], q.shape[2]), dtype=torch.uint8,
                                 device=q.device)
-    ws, n = (_p(workspace), workspace.numel()) if workspace is not None else (None, 1 << 62)
-    _check(lib().gqa_paged_attn_t(
-        _opt(q, "q"), _opt(k_pages, "k_pages"), _opt(v_pages, "v_pages"), _opt(block_table, "block_table"),
-        _opt(seq_lens, "seq_lens"), _opt(out, "out"), _opt(lse, "lse"), float(q_scale), float(k_scale), float(v_scale),
-        int(window), float(softcap), ws, n, _stream_for(q)))
+    st = _binding().attn(q, k_pages, v_pages, block_table, seq_lens, out, lse, workspace, q_scale, k_scale, v_scale, window,
+                         softcap)
+    if st:
+        _check(st)
     return out
 
 

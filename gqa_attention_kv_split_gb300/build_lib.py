@@ -16,11 +16,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgqa.so")
+BINDING = os.path.join(HERE, "_binding.so")  # csrc/binding.c: Python calls of the paged-cache entry points
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cpp", "decode.cu", "ctx_nvfp4.cu", "ctx_study.cu", "append.cu", "paged_attn.cpp", "paged_attn_f16.cu",
@@ -38,9 +40,9 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "gqa.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -50,7 +52,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if not force and not _stale():
         return LIB
     _compile_and_link(ARCH, OBJ, LIB, verbose, ptxas_verbose)
+    _build_binding()
     return LIB
+
+
+def _build_binding() -> None:
+    """Compile csrc/binding.c (plain C, the interpreter's headers) into _binding.so."""
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-Wextra", "-Werror", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.c"), "-o", tmp]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("binding build failed:\n" + r.stdout)
+    os.replace(tmp, BINDING)
 
 
 def build_other_arch(arch: str = "sm_100a") -> str:
