@@ -2,6 +2,8 @@
 // workspace layout, choice of the instance.
 #include <cuda.h>  // CUtensorMap and the cuTensorMapEncodeTiled prototype (resolved at run time)
 
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <mutex>
 
@@ -47,13 +49,22 @@ cudaError_t make_map(const void* pages, const PagedAttnArgs& a, int64_t s_page, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A 64-bit number that no earlier call, of this process or another, is likely to have
+// left in a workspace: steps of an odd number (which meet every value once) from a
+// start that differs from process to process.
+uint64_t next_nonce() {
+  static std::atomic<uint64_t> counter{(uint64_t)std::chrono::system_clock::now().time_since_epoch().count() * 0x100000001b3ull ^
+                                       (uint64_t)reinterpret_cast<uintptr_t>(&g_encode)};
+  return counter.fetch_add(0x9e3779b97f4a7c15ull, std::memory_order_relaxed);
+}
+
 int rows_of(int group) { return group > 8 ? 16 : 8; }  // query heads of a unit
 
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int hq, int hkv, int d) {
   const size_t rows = (size_t)pa::kGrid * 2 * rows_of(hq / hkv);
-  return rows * d * sizeof(float) + rows * sizeof(float2) + pa::kGrid * sizeof(pa::Record);
+  return rows * d * sizeof(float) + rows * sizeof(float2) + pa::kGrid * 2 * sizeof(uint64_t);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStream_t stream) {
@@ -70,7 +81,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   const size_t n = (size_t)pa::kGrid * 2 * rows;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + n * a.d);
-  p.record = reinterpret_cast<pa::Record*>(p.part_ml + n);
+  p.words = reinterpret_cast<uint64_t*>(p.part_ml + n);
+  p.nonce = next_nonce();
   p.q_seq = a.q_seq;
   p.q_head = a.q_head;
   p.batch = a.batch;

@@ -23,7 +23,10 @@
 //    all (sequence, KV head, block of heads) units, in order, whatever the
 //    lengths -- the shares are computed on the device from seq_lens.  A unit that
 //    lies inside one block is written by it; the pieces of one that does not go
-//    to the workspace (at most two per block) and a second kernel joins them.
+//    to the workspace (at most two per block), and the last block to write one joins
+//    them, in the order of the tiles.  No block waits for another.  The last one is
+//    found by exchanges of a 64-bit number of the call's own, so that the workspace
+//    needs no preparation.
 //  * A producer warp moves tiles of 64 (32) tokens with tensor-map TMA copies
 //    into a ring of about 190 KB: any page size and cache order is a box of the
 //    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
@@ -77,6 +80,28 @@ struct Shape {
   static_assert(kStages >= kGroups, "ring too small");
 };
 
+// A unit that lies in several blocks' shares.
+struct Piece {
+  int64_t tile0;    // its first tile, counted over the call
+  int b, unit;      // sequence, unit within it
+  int tiles;
+  int first, last;  // the blocks that hold it
+  int first_slot;   // which of the first block's two pieces it is (it is the first one of the others)
+  int join;         // this block was the last to write a piece of it
+  __device__ __forceinline__ int word(int block) const { return 2 * block + (block == first ? first_slot : 0); }
+};
+
+// Block i of n has the tiles [total * i / n, total * (i + 1) / n).  (32-bit divisions where they do.)
+__device__ __forceinline__ int64_t share_begin(int i, int64_t total, int n) {
+  const int64_t x = total * i;
+  return x >> 32 ? x / n : (int64_t)((uint32_t)x / (uint32_t)n);
+}
+// The block that has a tile: the last one whose share begins at or before it.
+__device__ __forceinline__ int share_of(int64_t tile, int64_t total, int n) {
+  const int64_t x = (tile + 1) * n + total - 1;
+  return (int)(x >> 32 ? x / total : (int64_t)((uint32_t)x / (uint32_t)total)) - 1;
+}
+
 template <int kWarps, int D, int NT>
 struct Smem {
   static constexpr int kRows = 8 * NT;
@@ -90,7 +115,11 @@ struct Smem {
   uint64_t q_empty[2];
   int64_t scan[kWarps + 1];
   int64_t total;  // tiles of the whole call
-  int64_t b0, rem;
+  int n_blocks;   // blocks with a share
+  int64_t end;    // of this block's share
+  int64_t rem;    // the share's first tile within its first sequence,
+  int b0;         // and that sequence
+  Piece piece[2];  // the units of this block's two pieces
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t r[4], uint32_t addr) {
@@ -160,47 +189,98 @@ struct Span {
   }
 };
 
-// Walks the units of a block's share [pos, end) of the call's tiles.
+// Walks the units of a block's share of the call's tiles.  (A share has fewer than 2^31
+// tiles: the host sees to it.)
 template <int kTile>
 struct Walk {
-  int64_t pos, end, b;
+  int left;   // tiles of the share from the piece's first one on
+  int b;      // sequence
   int unit;   // within the sequence: kv head * head blocks + head block
   int t_beg;  // first tile of the piece within the unit, and one past its last
   int t_end;
   Span<kTile> span;
-  int units;
-  __device__ __forceinline__ Walk(const Params& p, int64_t pos_, int64_t end_, int64_t b_, int64_t rem)
-      : pos(pos_), end(end_), b(b_), span(p, b_), units(p.hkv * p.head_blocks) {
+  __device__ __forceinline__ Walk(const Params& p, int left_, int b_, int64_t rem) : left(left_), b(b_), span(p, b_) {
     unit = (int)(rem / span.tiles);
     t_beg = (int)(rem - (int64_t)unit * span.tiles);
-    clip();
-  }
-  __device__ __forceinline__ void clip() {
-    const int64_t left = end - pos;
-    t_end = left < span.tiles - t_beg ? t_beg + (int)left : span.tiles;
+    t_end = min(span.tiles, t_beg + left);
   }
   // To the next piece; false at the end of the share.
   __device__ __forceinline__ bool next(const Params& p) {
-    pos += t_end - t_beg;
-    if (pos >= end) return false;
+    left -= t_end - t_beg;
+    if (left <= 0) return false;
     t_beg = 0;
-    if (++unit == units) {
+    if (++unit == p.hkv * p.head_blocks) {
       unit = 0;
       do {
         span = Span<kTile>(p, ++b);
       } while (span.tiles == 0);
     }
-    clip();
+    t_end = min(span.tiles, left);
     return true;
   }
   __device__ __forceinline__ bool whole() const { return t_beg == 0 && t_end == span.tiles; }
 };
 
+// Elements d, d + 1 of a head's output from sums relative to exp2(mm), and its lse.
+template <int D>
+__device__ __forceinline__ void store_out(const Params& p, int64_t row, int d, float x, float y, float mm, float l) {
+  const float inv = p.v_scale / l;
+  const uint32_t pk = p.q_bf16 ? pack_bf16(x * inv, y * inv) : pack_f16(x * inv, y * inv);
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (row * D + d) * 2) = pk;
+  if (d == 0 && p.lse) p.lse[row] = mm * 0.6931471805599453f + logf(l);
+}
+
 namespace {
+
+// (volatile: the compiler would otherwise put each load next to its use)
+__device__ __forceinline__ float2 load_l2(const float2* p) {
+  float2 v;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+
+// Joins the pieces of a unit, in the order of its tiles: thread i of n takes the pairs of
+// elements i, i + n, ...
+template <int D, int NT>
+__device__ __forceinline__ void join_pieces(const Params& p, const Piece& u, int i, int n) {
+  constexpr int kRows = 8 * NT, kBatch = 8;
+  const int kvh = u.unit / p.head_blocks;
+  const int h0 = kvh * p.group + (u.unit - kvh * p.head_blocks) * kRows;
+  const int pairs = min(kRows, (kvh + 1) * p.group - h0) * (D / 2);
+  const int first = u.first, last = u.last, first_slot = u.first_slot;
+  for (int j = i; j < pairs; j += n) {
+    const int r = j / (D / 2), d = j % (D / 2) * 2;
+    // (m, l, o) so far; the smaller maximum's side is scaled down.  kBatch pieces' loads are
+    // in flight at a time (the last piece's again behind the end).
+    float m = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
+    for (int b = first; b <= last; b += kBatch) {
+      float2 ml[kBatch], v[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int c = min(b + e, last);
+        const int64_t at = (int64_t)(2 * c + (c == first ? first_slot : 0)) * kRows + r;
+        ml[e] = load_l2(p.part_ml + at);
+        v[e] = load_l2(reinterpret_cast<const float2*>(p.part_o + at * D + d));
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const float me = b + e <= last ? ml[e].x : -INFINITY;
+        const float mn = fmaxf(m, me);
+        const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+        const float g = me == -INFINITY ? 0.f : fast_exp2(me - mn);
+        m = mn;
+        l = fmaf(l, f, ml[e].y * g);
+        x = fmaf(x, f, v[e].x * g);
+        y = fmaf(y, f, v[e].y * g);
+      }
+    }
+    store_out<D>(p, (int64_t)u.b * p.hq + h0 + r, d, x, y, m, l);
+  }
+}
 
 template <int kCache, int D, int NT>
 __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
-    paged_attn_kernel(const Params p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    paged_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   uint32_t* const err = &g_paged_attn_err;
   using S = Shape<kCache, D, NT>;
   constexpr bool kBf16 = kCache == kCacheBf16;
@@ -266,9 +346,15 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   before += incl - mine;
   before *= units;
   total *= units;
-  const int64_t n_blocks = total < kGrid ? total : kGrid;  // blocks with a share: none is empty
-  const int64_t beg = blockIdx.x < n_blocks ? total * blockIdx.x / n_blocks : 0;
-  const int64_t end = blockIdx.x < n_blocks ? total * (blockIdx.x + 1) / n_blocks : 0;
+  const int n_blocks = total < kGrid ? (int)total : kGrid;  // blocks with a share: none is empty
+  const bool has_share = blockIdx.x < n_blocks;
+  const int64_t beg = has_share ? share_begin(blockIdx.x, total, n_blocks) : 0;
+  const int64_t end = has_share ? share_begin(blockIdx.x + 1, total, n_blocks) : 0;
+  if (threadIdx.x == 0) {
+    sm.total = total;
+    sm.n_blocks = n_blocks;
+    sm.end = end;
+  }
   if (beg < end && beg >= before && beg < before + mine * units) {
     int64_t rem = beg - before;
     int64_t b = s0;
@@ -277,15 +363,12 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       if (rem < n) break;
       rem -= n;
     }
-    sm.b0 = b;
+    sm.b0 = (int)b;
     sm.rem = rem;
   }
   __syncthreads();
-  if (beg >= end) {
-    if (threadIdx.x == 0) p.record[blockIdx.x].unit = -1;
-    return;
-  }
-  Walk<kTile> walk(p, beg, end, sm.b0, sm.rem);
+  if (beg >= end) return;
+  Walk<kTile> walk(p, (int)(end - beg), sm.b0, sm.rem);
 
   if (warp == kWarps) {
     // ---------------- producer ------------------------------------------------
@@ -311,11 +394,11 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       if (lane == 0) mbar_arrive_expect_tx(qf, (uint32_t)heads * D * 2);
       __syncwarp();
       if (lane < heads)
-        bulk_g2s_hint(smem_u32(sm.q[qb][lane]), static_cast<const uint8_t*>(p.q) + (walk.b * p.q_seq + (h0 + lane) * p.q_head) * 2,
+        bulk_g2s_hint(smem_u32(sm.q[qb][lane]), static_cast<const uint8_t*>(p.q) + ((int64_t)walk.b * p.q_seq + (h0 + lane) * p.q_head) * 2,
                       D * 2, qf, policy_evict_last());
       ++seg;
       // Page numbers, 32 copies' worth at a time and one such group ahead (lane l has those of copy l).
-      const int32_t* row = p.block_table + walk.b * p.max_pages;
+      const int32_t* row = p.block_table + (int64_t)walk.b * p.max_pages;
       int c = ((walk.span.tile0 + walk.t_beg) << (kTileShift - box_shift)) + lane;  // this lane's copy, counted from the sequence's first token
       const int c_end = ((walk.span.len - 1) >> box_shift) + 1;                     // copies behind the last token are not made
       const int c_first = walk.span.first >> box_shift;                             // nor those before the window
@@ -402,6 +485,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   int skip = grp;        // tiles to this group's next one
   int seg = 0;
   bool dead = false;  // a wait has expired: nothing more is waited for or computed
+  int pieces = 0;     // bit i: this block has written its piece i
   do {
     const int kvh = walk.unit / p.head_blocks;
     const int h0 = kvh * p.group + (walk.unit - kvh * p.head_blocks) * kRows;
@@ -657,7 +741,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
         }
       }
     const bool whole = walk.whole();
-    const int slot = walk.pos == beg ? 0 : 1;
+    const int slot = seg == 1 ? 0 : 1;
     const int64_t piece = ((int64_t)blockIdx.x * 2 + slot) * kRows;
     named_bar_sync(1, kWarps * 32);
 #pragma unroll
@@ -701,11 +785,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
         }
         if (dead) continue;
         if (whole) {
-          const int64_t at = walk.b * p.hq + h0 + r;
-          const float inv = p.v_scale / ll;
-          const uint32_t pk = p.q_bf16 ? pack_bf16(x * inv, y * inv) : pack_f16(x * inv, y * inv);
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (at * D + d) * 2) = pk;
-          if (d == 0 && p.lse) p.lse[at] = (mm - kShift) * 0.6931471805599453f + logf(ll);
+          store_out<D>(p, (int64_t)walk.b * p.hq + h0 + r, d, x, y, mm - kShift, ll);
         } else {
           *reinterpret_cast<float2*>(p.part_o + (piece + r) * D + d) = make_float2(x, y);
           if (d == 0) p.part_ml[piece + r] = make_float2(mm - kShift, ll);
@@ -713,54 +793,67 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       }
       named_bar_sync(1, kWarps * 32);  // the buffers are free again
     }
-    // A unit that begins here and ends beyond this share: its last tile's block.
-    if (threadIdx.x == 0 && walk.pos + (walk.t_end - walk.t_beg) >= end) {
-      Record r{-1, 0, 0, 0};
-      if (!whole && walk.t_beg == 0) {
-        const int64_t last_tile = walk.pos + walk.span.tiles - 1;
-        r.unit = (int32_t)(walk.b * units + walk.unit);
-        r.last = (int32_t)(((last_tile + 1) * n_blocks + total - 1) / total - 1);
-        r.slot = slot;
+    if (!whole) {
+      pieces |= 1 << slot;
+      if (threadIdx.x == 0) {
+        Piece& u = sm.piece[slot];
+        u.tile0 = sm.end - walk.left - walk.t_beg;
+        u.b = walk.b;
+        u.unit = walk.unit;
+        u.tiles = walk.span.tiles;
       }
-      p.record[blockIdx.x] = r;
     }
   } while (walk.next(p));
-}
+  if (!pieces) return;
 
-// Joins the pieces of each unit that lies in several blocks' shares: one block per
-// (share in which a unit begins, row).
-template <int D>
-__global__ void __launch_bounds__(D / 2) paged_attn_join_kernel(const Params p, int rows) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Record rec = p.record[blockIdx.x];
-  if (rec.unit < 0) return;
-  const int r = blockIdx.y;
-  const int units = p.hkv * p.head_blocks;
-  const int64_t b = rec.unit / units;
-  const int u = rec.unit - (int)b * units;
-  const int kvh = u / p.head_blocks;
-  const int h0 = kvh * p.group + (u - kvh * p.head_blocks) * rows;
-  if (h0 + r >= (kvh + 1) * p.group) return;
-  const int d = threadIdx.x * 2;
-  const int first = (int)blockIdx.x;
-  float mm = -INFINITY;
-  for (int i = first; i <= rec.last; ++i)
-    mm = fmaxf(mm, p.part_ml[((int64_t)i * 2 + (i == first ? rec.slot : 0)) * rows + r].x);
-  float l = 0.f, x = 0.f, y = 0.f;
-  for (int i = first; i <= rec.last; ++i) {
-    const int64_t at = ((int64_t)i * 2 + (i == first ? rec.slot : 0)) * rows + r;
-    const float2 ml = p.part_ml[at];
-    const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mm);
-    const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + d);
-    l = fmaf(ml.y, f, l);
-    x = fmaf(v.x, f, x);
-    y = fmaf(v.y, f, y);
+  // ---- units that lie in several blocks' shares: the last to end joins the pieces ----
+  // Both pieces of this block at once, at its end: a unit's last block writes its piece
+  // at the start of its share, long before the others have theirs.  Each piece has a
+  // word in the workspace.  Two pieces meet in one exchange: the first block leaves the
+  // call's nonce in the word and goes, the second one finds it.  Of more pieces, each
+  // block sets its own word and looks whether all are set, a sequentially consistent
+  // fence between: of blocks that end together at least one sees them all (should two,
+  // they write the same values).  Nobody waits, and who joins clears the words: a replay
+  // of a captured call has the same nonce.
+  if (warp == 0) {
+    if (lane == 0) __threadfence();  // (the last barrier ordered the pieces' stores before it)
+    __syncwarp();
+    unsigned long long* const words = reinterpret_cast<unsigned long long*>(p.words);
+    bool many = false;  // lane i: piece i is one of more than two, and its word is set
+    if (lane < 2) {
+      Piece& u = sm.piece[lane];
+      u.join = 0;
+      if ((pieces >> lane) & 1) {
+        u.first = share_of(u.tile0, sm.total, sm.n_blocks);
+        u.last = share_of(u.tile0 + u.tiles - 1, sm.total, sm.n_blocks);
+        u.first_slot = share_begin(u.first, sm.total, sm.n_blocks) == u.tile0 ? 0 : 1;
+        many = u.last - u.first > 1;
+        if (many) {
+          *reinterpret_cast<volatile unsigned long long*>(words + u.word(blockIdx.x)) = p.nonce;
+        } else if (atomicExch(words + u.word(u.last), p.nonce) == p.nonce) {
+          words[u.word(u.last)] = 0;
+          u.join = 1;
+        }
+      }
+    }
+    const unsigned look = __ballot_sync(0xffffffffu, many);
+    __threadfence();
+    for (int i = 0; i < 2; ++i) {
+      if (!((look >> i) & 1)) continue;
+      const Piece& u = sm.piece[i];
+      bool all = true;
+      for (int b = u.first + lane; b <= u.last; b += 32)
+        all &= *reinterpret_cast<volatile unsigned long long*>(words + u.word(b)) == p.nonce;
+      if (__all_sync(0xffffffffu, all)) {
+        __threadfence();
+        for (int b = u.first + lane; b <= u.last; b += 32) words[u.word(b)] = 0;
+        if (lane == 0) sm.piece[i].join = 1;
+      }
+    }
   }
-  const int64_t at = b * p.hq + h0 + r;
-  const float inv = p.v_scale / l;
-  const uint32_t pk = p.q_bf16 ? pack_bf16(x * inv, y * inv) : pack_f16(x * inv, y * inv);
-  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (at * D + d) * 2) = pk;
-  if (d == 0 && p.lse) p.lse[at] = mm * 0.6931471805599453f + logf(l);
+  named_bar_sync(1, kWarps * 32);
+  for (int i = 0; i < 2; ++i)
+    if (sm.piece[i].join) join_pieces<D, NT>(p, sm.piece[i], threadIdx.x, kWarps * 32);
 }
 
 template <int kCache, int D, int NT>
@@ -781,17 +874,7 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUt
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
   paged_attn_kernel<kCache, D, NT><<<kGrid, S::kThreads, smem, stream>>>(p, k_map, v_map);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kGrid, 8 * NT);
-  cfg.blockDim = dim3(D / 2);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D>, p, 8 * NT);
+  return cudaGetLastError();
 }
 
 template <int kCache>

@@ -16,15 +16,6 @@ constexpr int kGrid = 152;  // blocks: one per SM
 // Tokens per ring stage, from the bytes of a token's row: 16 to 32 KB of K and V a stage.
 constexpr int tile_of(int row_bytes) { return row_bytes > 256 ? 32 : 64; }
 
-// One record per block: the unit that begins in the block's share and ends
-// beyond it, and the last block that holds a piece of it.
-struct Record {
-  int32_t unit;  // (sequence * hkv + kv head) * head blocks + head block; -1: none
-  int32_t last;
-  int32_t slot;  // which of the block's two pieces
-  int32_t pad;
-};
-
 struct Params {
   const void* q;
   void* out;
@@ -33,7 +24,8 @@ struct Params {
   const int32_t* seq_lens;
   float* part_o;     // [kGrid][2][kRows][D]
   float2* part_ml;   // [kGrid][2][kRows]
-  Record* record;    // [kGrid]
+  uint64_t* words;   // [kGrid][2]: tell whether a piece has been written
+  uint64_t nonce;    // of this call
   int64_t q_seq, q_head, batch, num_pages, max_pages;
   int hq, hkv, group, head_blocks;
   int page_shift, box_shift;  // log2 of a page's tokens, and of those of one copy
