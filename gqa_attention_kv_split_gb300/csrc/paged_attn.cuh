@@ -27,7 +27,7 @@
 //    them, in the order of the tiles.  No block waits for another.  The last one is
 //    found by exchanges of a 64-bit number of the call's own, so that the workspace
 //    needs no preparation.
-//  * A producer warp moves tiles of 64 (32) tokens with tensor-map TMA copies
+//  * Producer warps move tiles of 64 (32) tokens with tensor-map TMA copies
 //    into a ring of about 190 KB: any page size and cache order is a box of the
 //    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
 //  * Eight consumer warps (four at head dim 256), each with its own 32 keys of a tile and its own
@@ -64,7 +64,11 @@ struct Shape {
   // Consumer warps: eight, or four where the accumulators need more than the 168
   // registers a thread that nine warps leave.
   static constexpr int kWarps = D > 128 ? 4 : 8;
-  static constexpr int kThreads = (kWarps + 1) * 32;
+  // Four producer warps: for K and V, and for the even and the odd tiles.  (An issued
+  // copy takes its warp about 130 cycles; with pages of 16 tokens a tile of E4M3 has
+  // eight.  They cost no registers: five to twelve warps round up alike.)
+  static constexpr int kProducers = 4;
+  static constexpr int kThreads = (kWarps + kProducers) * 32;
   // 16-key blocks that a warp takes of a tile: two give it two independent sums of
   // products and one reduction for 32 keys (1.28x over one block on 48 sequences of up
   // to 16001 tokens in E4M3 pages of 64); with 16 heads and long rows the registers that the second one
@@ -77,7 +81,7 @@ struct Shape {
   // A whole number of groups' turns, so that a stage always belongs to one group (a
   // wait on its barrier can then never be a phase behind).
   static constexpr int kStages = kRoom / (2 * kHalf) / kGroups * kGroups;
-  static_assert(kStages >= kGroups, "ring too small");
+  static_assert(kStages >= kGroups && kStages % (kProducers / 2) == 0, "whole turns of groups and producers");
 };
 
 // A unit that lies in several blocks' shares.
@@ -113,7 +117,7 @@ struct Smem {
   uint64_t empty[32];
   uint64_t q_full[2];
   uint64_t q_empty[2];
-  int64_t scan[kWarps + 1];
+  int64_t scan[kWarps + 4];
   int64_t total;  // tiles of the whole call
   int n_blocks;   // blocks with a share
   int64_t end;    // of this block's share
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(smem_u32(&sm.full[i]), 1);
+      mbar_init(smem_u32(&sm.full[i]), 2);
       mbar_init(smem_u32(&sm.empty[i]), S::kGroupWarps);
     }
     for (int i = 0; i < 2; ++i) {
@@ -370,36 +374,42 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   if (beg >= end) return;
   Walk<kTile> walk(p, (int)(end - beg), sm.b0, sm.rem);
 
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
     // ---------------- producer ------------------------------------------------
     if (p.starve) return;
+    const bool is_v = (warp - kWarps) & 1;
+    const int pair = (warp - kWarps) >> 1;
+    constexpr int kPairs = S::kProducers / 2;
     const uint64_t pol = p.head_blocks == 1 ? policy_evict_first() : policy_evict_last();
     // (a box and a page are powers of two: the loop below has no division)
     const int box_shift = p.box_shift, page_shift = p.page_shift;
     const int boxes = kTile >> box_shift;  // copies per tile of K (and of V)
     const uint32_t box_bytes = (uint32_t)S::kRow << box_shift;
     const uint32_t lane_dst = smem_u32(ring) + lane * box_bytes;
-    int st = 0, ph = 1;  // stage, and the parity of the phase that frees it (the first one is free)
-    int issued = 0;      // stages issued, up to all of them
-    int seg = 0;         // pieces begun
+    int st = pair, ph = 1;  // this pair's next stage, and the parity of the phase that frees it (the first one is free)
+    int skip = pair;        // tiles to this pair's next one
+    int issued = 0;         // stages issued, up to all of this pair's
+    int seg = 0;            // pieces begun
     bool ok = true;
     do {
       const int kvh = walk.unit / p.head_blocks;
       const int h0 = kvh * p.group + (walk.unit - kvh * p.head_blocks) * kRows;
       const int heads = min(kRows, (kvh + 1) * p.group - h0);
-      const int qb = seg & 1;
-      if (seg >= 2 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_empty[qb]), ((seg >> 1) - 1) & 1, err))) ok = false;
-      if (!ok) break;
-      const uint32_t qf = smem_u32(&sm.q_full[qb]);
-      if (lane == 0) mbar_arrive_expect_tx(qf, (uint32_t)heads * D * 2);
-      __syncwarp();
-      if (lane < heads)
-        bulk_g2s_hint(smem_u32(sm.q[qb][lane]), static_cast<const uint8_t*>(p.q) + ((int64_t)walk.b * p.q_seq + (h0 + lane) * p.q_head) * 2,
-                      D * 2, qf, policy_evict_last());
+      if (warp == kWarps) {
+        const int qb = seg & 1;
+        if (seg >= 2 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_empty[qb]), ((seg >> 1) - 1) & 1, err))) break;
+        const uint32_t qf = smem_u32(&sm.q_full[qb]);
+        if (lane == 0) mbar_arrive_expect_tx(qf, (uint32_t)heads * D * 2);
+        __syncwarp();
+        if (lane < heads)
+          bulk_g2s_hint(smem_u32(sm.q[qb][lane]),
+                        static_cast<const uint8_t*>(p.q) + ((int64_t)walk.b * p.q_seq + (h0 + lane) * p.q_head) * 2, D * 2, qf,
+                        policy_evict_last());
+      }
       ++seg;
       // Page numbers, 32 copies' worth at a time and one such group ahead (lane l has those of copy l).
       const int32_t* row = p.block_table + (int64_t)walk.b * p.max_pages;
-      int c = ((walk.span.tile0 + walk.t_beg) << (kTileShift - box_shift)) + lane;  // this lane's copy, counted from the sequence's first token
+      int c = ((walk.span.tile0 + walk.t_beg + skip) << (kTileShift - box_shift)) + lane;  // this lane's copy, counted from the sequence's first token
       const int c_end = ((walk.span.len - 1) >> box_shift) + 1;                     // copies behind the last token are not made
       const int c_first = walk.span.first >> box_shift;                             // nor those before the window
       auto page_of = [&](int copy) {
@@ -413,7 +423,8 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       };
       int cur = page_of(c), nxt = page_of(c + 32);
       int at = 0;  // copies of this piece so far, within a group of 32
-      for (int t = walk.t_beg; t < walk.t_end; ++t) {
+      int t = walk.t_beg + skip;
+      for (; t < walk.t_end; t += kPairs) {
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.empty[st]), ph, err))) {
           ok = false;
           break;
@@ -421,34 +432,38 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
         const int pg = __shfl_sync(0xffffffffu, cur, (at + lane) & 31);
         const bool live = lane < boxes && c >= c_first && c < c_end;
         const uint32_t bar = smem_u32(&sm.full[st]);
-        const uint32_t bytes = 2u * box_bytes * __popc(__ballot_sync(0xffffffffu, live));
+        const uint32_t bytes = box_bytes * __popc(__ballot_sync(0xffffffffu, live));
         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();
         if (live) {
           const uint32_t dst = lane_dst + st * 2 * S::kHalf;
           const int slot = (c << box_shift) & ((1 << page_shift) - 1);
-          tma_5d(dst, &k_map, slot, kvh, pg, bar, pol);
-          tma_5d(dst + S::kHalf, &v_map, slot, kvh, pg, bar, pol);
+          if (is_v)
+            tma_5d(dst + S::kHalf, &v_map, slot, kvh, pg, bar, pol);
+          else
+            tma_5d(dst, &k_map, slot, kvh, pg, bar, pol);
         }
-        c += boxes;
-        at += boxes;
+        c += kPairs * boxes;
+        at += kPairs * boxes;
         if (at == 32) {
           at = 0;
           cur = nxt;
           nxt = page_of(c + 32);
         }
-        issued = min(issued + 1, S::kStages);
-        if (++st == S::kStages) {
-          st = 0;
+        issued = min(issued + 1, S::kStages / kPairs);
+        st += kPairs;
+        if (st >= S::kStages) {
+          st = pair;
           ph ^= 1;
         }
       }
+      skip = t - walk.t_end;
     } while (ok && walk.next(p));
     // No copy may land after the block has gone.
     if (lane == 0) {
       // (stages before st were last filled in the present round, the others in the one before)
-      for (int i = 0; i < issued; ++i) mbar_wait(smem_u32(&sm.full[i]), i < st ? ph ^ 1 : ph, err);
-      for (int i = seg > 2 ? seg - 2 : 0; i < seg; ++i) mbar_wait(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1, err);
+      for (int i = pair; i < pair + kPairs * issued; i += kPairs) mbar_wait(smem_u32(&sm.full[i]), i < st ? ph ^ 1 : ph, err);
+      for (int i = seg > 2 ? seg - 2 : 0; warp == kWarps && i < seg; ++i) mbar_wait(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1, err);
     }
     return;
   }
