@@ -42,7 +42,8 @@ LIB_PATH = os.path.join(_HERE, "libgqa.so")
 HQ, HKV, D, PAGE = 32, 8, 128, 64
 
 _STATUS = {0: "GQA_OK", 1: "GQA_ERR_INVALID_ARG", 2: "GQA_ERR_UNSUPPORTED", 3: "GQA_ERR_DEVICE_MISMATCH",
-           4: "GQA_ERR_CUDA", 5: "GQA_ERR_OOM", 6: "GQA_ERR_TIMEOUT"}
+           4: "GQA_ERR_CUDA", 5: "GQA_ERR_OOM", 6: "GQA_ERR_TIMEOUT", 7: "GQA_ERR_WORKSPACE"}
+_ERR_WORKSPACE = 7
 
 
 class GqaTensor(ctypes.Structure):
@@ -321,16 +322,19 @@ def gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=
     include/gqa.h): q [B,Hq,D] f16 or bf16, k_pages / v_pages
     [num_pages,Hkv,page_size,D] of q's type or E4M3, in any order in memory,
     block_table [B,max_pages_per_seq] and seq_lens [B] int32.  Writes `lse`
-    [B,Hq] f32 if given.  The workspace is allocated for the call unless one
-    of at least gqa_paged_attn_workspace(Hq, Hkv, D) bytes (uint8) is given;
-    calls that can run at the same time need one each."""
+    [B,Hq] f32 if given.  The workspace is the library's for the stream (in
+    a captured call: one from the graph's memory pool) unless one of at least
+    gqa_paged_attn_workspace(Hq, Hkv, D) bytes (uint8) is given; calls that
+    can run at the same time need one each."""
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if workspace is None and q.is_cuda and q.dim() == 3 and k_pages.dim() == 4:
+    args = (q_scale, k_scale, v_scale, window, softcap)
+    call = _binding().attn
+    st = call(q, k_pages, v_pages, block_table, seq_lens, out, lse, workspace, *args)
+    if st == _ERR_WORKSPACE:  # being captured: one from the graph's memory pool
         workspace = torch.empty(gqa_paged_attn_workspace(q.shape[1], k_pages.shape[1], q.shape[2]), dtype=torch.uint8,
                                 device=q.device)
-    st = _binding().attn(q, k_pages, v_pages, block_table, seq_lens, out, lse, workspace, q_scale, k_scale, v_scale, window,
-                         softcap)
+        st = call(q, k_pages, v_pages, block_table, seq_lens, out, lse, workspace, *args)
     if st:
         _check(st)
     return out

@@ -136,13 +136,17 @@ struct Workspace {
   size_t bytes = 0;
 };
 std::mutex g_ws_mu;
-std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
+using WorkspaceMap = std::map<std::pair<int, uintptr_t>, Workspace>;
+WorkspaceMap g_ws;
+// Of gqa_paged_attn_t's calls without a workspace (a map of their own: growing one
+// never moves the other, which a captured call may have been given).
+WorkspaceMap g_paged_ws;
 
-gqa_status workspace(int dev, cudaStream_t stream, size_t bytes, void** out) {
+gqa_status workspace(int dev, cudaStream_t stream, size_t bytes, void** out, WorkspaceMap& map = g_ws) {
   *out = nullptr;
   if (bytes == 0) return GQA_OK;
   std::lock_guard<std::mutex> lk(g_ws_mu);
-  Workspace& w = g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}];
+  Workspace& w = map[{dev, reinterpret_cast<uintptr_t>(stream)}];
   if (w.bytes < bytes) {
     if (w.ptr) {
       // Work queued on this stream may still use the old buffer.
@@ -999,12 +1003,13 @@ gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, cons
   if (window < 0) return fail(GQA_ERR_INVALID_ARG, "window %d is negative", window);
   if (!std::isfinite(softcap) || softcap < 0.f) return fail(GQA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
   const int64_t need = gqa_paged_attn_workspace(qs[1], ps[1], qs[2]);
-  if (workspace_bytes < need)
+  if (workspace_ && workspace_bytes < need)
     return fail(GQA_ERR_INVALID_ARG, "workspace of %lld bytes; %lld are needed", (long long)workspace_bytes, (long long)need);
   gqa_tensor ws = *q;  // the workspace's place is checked with the tensors'
   ws.data = workspace_;
   std::vector<Named> ts = {{q, "q"}, {k_pages, "k_pages"}, {v_pages, "v_pages"}, {block_table, "block_table"},
-                           {seq_lens, "seq_lens"}, {out, "out"}, {&ws, "workspace"}};
+                           {seq_lens, "seq_lens"}, {out, "out"}};
+  if (workspace_) ts.push_back({&ws, "workspace"});
   gqa_tensor l;
   if (lse) {
     l = *lse;
@@ -1045,7 +1050,15 @@ gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, cons
   a.starve = gqa::starve_producers();
   ScopedDevice sd(where.device);
   if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", where.device);
-  GQA_CUDA_TRY(gqa::launch_paged_attn(a, workspace_, reinterpret_cast<cudaStream_t>(stream)), "paged attention launch");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!workspace_) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    GQA_CUDA_TRY(cudaStreamIsCapturing(s, &capture), "cudaStreamIsCapturing");
+    if (capture != cudaStreamCaptureStatusNone)
+      return fail(GQA_ERR_WORKSPACE, "a captured call needs a workspace of its own (%lld bytes)", (long long)need);
+    GQA_TRY(workspace(where.device, s, (size_t)need, &workspace_, g_paged_ws));
+  }
+  GQA_CUDA_TRY(gqa::launch_paged_attn(a, workspace_, s), "paged attention launch");
   return GQA_OK;
 }
 
@@ -1053,13 +1066,15 @@ gqa_status gqa_release_workspace(void) {
   std::lock_guard<std::mutex> lk(g_ws_mu);
   int prev = -1;
   cudaGetDevice(&prev);
-  for (auto& kv : g_ws) {
-    if (kv.second.ptr) {
-      cudaSetDevice(kv.first.first);
-      cudaFree(kv.second.ptr);
+  for (WorkspaceMap* map : {&g_ws, &g_paged_ws}) {
+    for (auto& kv : *map) {
+      if (kv.second.ptr) {
+        cudaSetDevice(kv.first.first);
+        cudaFree(kv.second.ptr);
+      }
     }
+    map->clear();
   }
-  g_ws.clear();
   if (prev >= 0) cudaSetDevice(prev);
   return GQA_OK;
 }

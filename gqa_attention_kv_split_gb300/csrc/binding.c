@@ -5,9 +5,8 @@
  * and calls the library, which does every check.  It is compiled because a decode
  * step makes these calls once per layer, on tensors whose kernels run for a few
  * microseconds: filling a descriptor from Python takes 1.6 us, ten of them longer
- * than the kernel; from here it is about 0.3 us (see tests/test_paged_cache.py for
- * what it accepts).  No torch header is needed: the attributes are read through
- * the Python objects.
+ * than the kernel; from here it is about 0.25 us.  No torch header is needed: the
+ * attributes are read through the Python objects.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -27,7 +26,16 @@ static gqa_status (*g_nvfp4_append)(const gqa_tensor*, const gqa_tensor*, const 
                                     const gqa_tensor*, gqa_tensor*, int, float, gqa_stream_t);
 static gqa_status (*g_attn)(const gqa_tensor*, const gqa_tensor*, const gqa_tensor*, const gqa_tensor*, const gqa_tensor*,
                             gqa_tensor*, gqa_tensor*, float, float, float, int, float, void*, int64_t, gqa_stream_t);
-static PyObject *s_data_ptr, *s_dtype, *s_get_device, *s_shape, *s_stride;
+/* torch.Tensor's own descriptors, looked up once: methods and attributes */
+static PyObject *m_data_ptr, *m_get_device, *m_stride, *a_dtype, *a_shape;
+
+static PyObject* call(PyObject* method, PyObject* t) {
+  PyObject* args[2] = {NULL, t};
+  return PyObject_Vectorcall(method, args + 1, 1 | PY_VECTORCALL_ARGUMENTS_OFFSET, NULL);
+}
+static PyObject* get(PyObject* attribute, PyObject* t) {
+  return Py_TYPE(attribute)->tp_descr_get(attribute, t, (PyObject*)Py_TYPE(t));
+}
 
 static int read_ints(PyObject* tuple, int64_t* out, int n) {
   for (int i = 0; i < n; ++i) {
@@ -47,19 +55,19 @@ static int fill(PyObject* t, const char* name, gqa_tensor* d, gqa_tensor** ref) 
   }
   PyObject *shape = NULL, *stride = NULL, *x = NULL;
   int rc = -1;
-  if (!(x = PyObject_CallMethodNoArgs(t, s_data_ptr))) goto done;
+  if (!(x = call(m_data_ptr, t))) goto done;
   d->data = PyLong_AsVoidPtr(x);
   if (!d->data && PyErr_Occurred()) goto done;
   Py_CLEAR(x);
-  if (!(x = PyObject_GetAttr(t, s_dtype))) goto done;
+  if (!(x = get(a_dtype, t))) goto done;
   d->dtype = 0;
   for (int i = 0; i < g_n_dtypes; ++i)
     if (x == g_dtypes[i]) d->dtype = g_codes[i];
   Py_CLEAR(x);
-  if (!(x = PyObject_CallMethodNoArgs(t, s_get_device))) goto done;
+  if (!(x = call(m_get_device, t))) goto done;
   d->device = (int32_t)PyLong_AsLong(x);
   if (d->device == -1 && PyErr_Occurred()) goto done;
-  if (!(shape = PyObject_GetAttr(t, s_shape)) || !(stride = PyObject_CallMethodNoArgs(t, s_stride))) goto done;
+  if (!(shape = get(a_shape, t)) || !(stride = call(m_stride, t))) goto done;
   if (!PyTuple_Check(shape) || !PyTuple_Check(stride) || PyTuple_GET_SIZE(shape) != PyTuple_GET_SIZE(stride)) {
     PyErr_Format(PyExc_TypeError, "%s: shape and strides are not tuples of one length", name);
     goto done;
@@ -175,7 +183,7 @@ static PyObject* py_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       stream_of(r[0], &stream))
     return NULL;
   void* ws = NULL;
-  int64_t bytes = INT64_MAX; /* (no workspace: refused as a null pointer) */
+  int64_t bytes = 0;
   if (r[7]) {
     if (r[7]->dtype != GQA_U8 || r[7]->ndim != 1 || (r[7]->shape[0] > 1 && r[7]->strides[0] != 1)) {
       PyErr_SetString(PyExc_ValueError, "workspace must be a dense 1-d uint8 tensor");
@@ -218,6 +226,14 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
     g_codes[i] = code;
   }
   g_n_dtypes = (int)n;
+  if (!(m_data_ptr = PyObject_GetAttrString(tensor, "data_ptr")) || !(m_get_device = PyObject_GetAttrString(tensor, "get_device")) ||
+      !(m_stride = PyObject_GetAttrString(tensor, "stride")) || !(a_dtype = PyObject_GetAttrString(tensor, "dtype")) ||
+      !(a_shape = PyObject_GetAttrString(tensor, "shape")))
+    return NULL;
+  if (!Py_TYPE(a_dtype)->tp_descr_get || !Py_TYPE(a_shape)->tp_descr_get) {
+    PyErr_SetString(PyExc_TypeError, "setup: torch.Tensor.dtype and shape are no descriptors");
+    return NULL;
+  }
   Py_INCREF(tensor);
   g_tensor = (PyTypeObject*)tensor;
   Py_INCREF(stream);
@@ -237,9 +253,5 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__binding(void) {
-  if (!(s_data_ptr = PyUnicode_InternFromString("data_ptr")) || !(s_dtype = PyUnicode_InternFromString("dtype")) ||
-      !(s_get_device = PyUnicode_InternFromString("get_device")) || !(s_shape = PyUnicode_InternFromString("shape")) ||
-      !(s_stride = PyUnicode_InternFromString("stride")))
-    return NULL;
   return PyModule_Create(&module);
 }

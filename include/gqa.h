@@ -57,7 +57,8 @@ typedef enum gqa_status {
   GQA_ERR_DEVICE_MISMATCH = 3,    /* pointers on different devices / host+device mix */
   GQA_ERR_CUDA = 4,               /* a CUDA runtime call failed */
   GQA_ERR_OOM = 5,                /* workspace allocation failed */
-  GQA_ERR_TIMEOUT = 6             /* a kernel's bounded wait expired (see gqa_check_device_errors) */
+  GQA_ERR_TIMEOUT = 6,            /* a kernel's bounded wait expired (see gqa_check_device_errors) */
+  GQA_ERR_WORKSPACE = 7           /* a captured call without a workspace (see gqa_paged_attn_t) */
 } gqa_status;
 
 /*
@@ -432,10 +433,14 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
  *   seq_lens     [batch]  int32, read on the device
  *   out          [batch, q_heads, d]  q's type, dense, written
  *   lse          [batch, q_heads]  f32, dense, written; or NULL
- *   workspace    device memory of at least gqa_paged_attn_workspace(q_heads,
- *                kv_heads, d) bytes, 16-byte aligned; its contents mean nothing
- *                before or after a call.  The caller owns it: calls that can run
- *                at the same time (on two streams, in two graphs) need one each
+ *   workspace    NULL: the library's own for (device, stream), like the other
+ *                entry points'.  Or device memory of at least
+ *                gqa_paged_attn_workspace(q_heads, kv_heads, d) bytes, 16-byte
+ *                aligned, whose contents mean nothing before or after a call: one
+ *                each for calls that can run at the same time.  A call that is
+ *                being captured has to be given one (GQA_ERR_WORKSPACE without:
+ *                two graphs captured on one stream may be replayed at once), which
+ *                belongs to the graph as long as it is replayed
  *   batch 1 .. 65535; d 64, 128 or 256; 1 .. 1024 query heads, a multiple of the
  *   kv_heads; page_size 16, 32, 64, 128 or 256; page_size * max_pages_per_seq at
  *   most 2^30

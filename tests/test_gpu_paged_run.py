@@ -188,6 +188,25 @@ def test_workspace_of_the_caller_holds_anything():
         assert torch.equal(t.attend(tq, tl, workspace=ws), tw)
 
 
+def test_captured_call_without_workspace_is_refused_by_the_library():
+    """The entry point asks for one (the binding then takes it from the graph's pool); the library's own is not captured."""
+    s = Server(B=2, seed=9)
+    lens = torch.tensor([1, 1], dtype=torch.int32, device=DEV)
+    q = s.append(s.new([1, 1]).to(DEV), lens, None)
+    out = torch.empty_like(q)
+    args = (q, *s.pages, s.d_table, lens, out, None, None, 1.0, 1.0, 1.0, 0, 0.0)
+    assert gqa._binding().attn(*args) == 0
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        status = gqa._binding().attn(*args)
+    assert status == 7 and b"workspace of its own" in gqa.lib().gqa_last_error()
+    gqa.gqa_release_workspace()
+    again = s.attend(q, lens)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+
+
 def test_threads_and_streams():
     """Calls from several threads, each on a stream of its own, give what one call gives."""
     s = Server(B=4, hq=16, hkv=2, cap=2048, page=32, seed=7)

@@ -116,10 +116,27 @@ def attn_args(B=2, hq=4, hkv=2, d=64, page=16, dtype=torch.float16, cache=None, 
     (dict(k_scale=0.0), "k_scale must be finite and > 0"),
     (dict(workspace=torch.zeros(64, dtype=torch.uint8)), "workspace of 64 bytes"),
     (dict(), "gqa_paged_attn takes device tensors only"),
+    (dict(workspace=None), "gqa_paged_attn takes device tensors only"),
 ])
 def test_attention_refusals(change, match):
     with pytest.raises(gqa.GqaError, match=match):
         gqa.gqa_paged_attn(**{**attn_args(), **change})
+
+
+def test_workspace_has_to_be_bytes():
+    with pytest.raises(ValueError, match="dense 1-d uint8"):
+        gqa.gqa_paged_attn(**{**attn_args(), "workspace": torch.zeros(1 << 20)})
+
+
+def test_binding_takes_tensors_only():
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        gqa.gqa_paged_append(**{**append_args(), "q": [1.0], "q_out": fake((3, 4, 64))})
+    with pytest.raises(ValueError, match="k has more than 6 dimensions"):
+        gqa.gqa_paged_append(**{**append_args(), "k": fake((1,) * 7)})
+    with pytest.raises(TypeError):
+        gqa.gqa_paged_attn(**attn_args(), q_scale="1")
+    with pytest.raises(OverflowError):
+        gqa.gqa_paged_attn(**attn_args(), window=1 << 40)
 
 
 def test_attention_refuses_other_head_dims():
