@@ -111,6 +111,16 @@ __device__ __forceinline__ float amax8(const float f[8]) {
   for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
   return m;
 }
+// x / s by one multiplication with r = 1 / s and one correction step (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): the f32 quotient but for values
+// within 2^-47 of a midpoint between two f32 numbers.  The E2M1 code that it is rounded to is that of the
+// true quotient's f32 rounding: for a border t between two codes, t * s is an f32 number (of 7 significant
+// bits at most), so that x is t * s, and the step gives t, or at least one f32 spacing away from it, and the
+// quotient more than half a spacing away from t.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = __fmul_rn(x, r);
+  return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+}
 // E4M3 scale byte of a block's largest magnitude, and the scale's value.
 __device__ __forceinline__ uint32_t block_scale(float amax, float* value) {
   const uint32_t byte = f32x2_to_e4m3x2(__fdiv_rn(amax, 6.f), 0.f);
@@ -122,10 +132,17 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float* value) {
 // Eight elements -> 4 bytes of codes; all codes 0 where the scale is 0 or NaN.
 __device__ __forceinline__ uint32_t codes8(const float f[8], float scale) {
   if (!(scale > 0.f)) return 0u;
+  const float inv = __fdiv_rn(1.f, scale);
   uint32_t r = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    r |= f32x2_to_e2m1x2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)) << (8 * i);
+    r |= f32x2_to_e2m1x2(quotient(f[2 * i], scale, inv), quotient(f[2 * i + 1], scale, inv)) << (8 * i);
+  if (scale == 448.f) {  // the largest scale: there may be infinities, whose correction is NaN
+    r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r |= f32x2_to_e2m1x2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)) << (8 * i);
+  }
   return r;
 }
 
@@ -183,44 +200,36 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   const int n_tok = (int)(a.total < t0 + a.tok_per_block ? a.total - t0 : a.tok_per_block);
   const int rows = (a.q ? a.hq : 0) + 2 * a.hkv;  // of one token: q heads, k heads, v heads
   const int hq = a.q ? a.hq : 0;
-  const uint32_t n_items = (uint32_t)n_tok * rows * kLanes;
   const int turned = a.rope ? a.rot / 16 : 0;  // lanes of a row that rotate
 
-  struct Item {
+  // A thread's rows: kStep apart, over the block's tokens.
+  constexpr int kStep = kAppendThreads / kLanes;
+  const int j = threadIdx.x % kLanes;
+  struct Row {
+    int tok, row;
     uint4 lo, hi;
   };
-  // Item i: (token, row, lane of the row) and its two vectors' numbers within the row.
-  auto where = [&](uint32_t i, int& tok, int& row, int& j) {
-    j = (int)(i % kLanes);
-    const uint32_t r = i / kLanes;
-    tok = (int)(r / (uint32_t)rows);
-    row = (int)(r - (uint32_t)tok * rows);
-  };
-  auto vectors = [&](int row, int j, int& v0, int& v1) {
-    const bool split = row < hq + a.hkv && j < turned && !a.interleaved;
-    v0 = split ? j : 2 * j;
-    v1 = split ? j + turned : 2 * j + 1;
-  };
-  auto load = [&](uint32_t i) {
-    Item it{};
-    if (i < n_items) {
-      int tok, row, j, v0, v1;
-      where(i, tok, row, j);
-      vectors(row, j, v0, v1);
-      const T* src;
-      if (row < hq)
-        src = static_cast<const T*>(a.q) + (t0 + tok) * a.q_tok + row * a.q_head;
-      else if (row < hq + a.hkv)
-        src = static_cast<const T*>(a.k) + (t0 + tok) * a.k_tok + (row - hq) * a.k_head;
-      else
-        src = static_cast<const T*>(a.v) + (t0 + tok) * a.v_tok + (row - hq - a.hkv) * a.v_head;
-      it.lo = *reinterpret_cast<const uint4*>(src + 8 * v0);
-      it.hi = *reinterpret_cast<const uint4*>(src + 8 * v1);
+  auto split = [&](int row) { return row < hq + a.hkv && j < turned && !a.interleaved; };  // a half-split rotation
+  auto load = [&](Row& x) {
+    while (x.row >= rows) {
+      x.row -= rows;
+      ++x.tok;
     }
-    return it;
+    if (x.tok >= n_tok) return;
+    const T* src;
+    if (x.row < hq)
+      src = static_cast<const T*>(a.q) + (t0 + x.tok) * a.q_tok + x.row * a.q_head;
+    else if (x.row < hq + a.hkv)
+      src = static_cast<const T*>(a.k) + (t0 + x.tok) * a.k_tok + (x.row - hq) * a.k_head;
+    else
+      src = static_cast<const T*>(a.v) + (t0 + x.tok) * a.v_tok + (x.row - hq - a.hkv) * a.v_head;
+    const bool sp = split(x.row);
+    x.lo = *reinterpret_cast<const uint4*>(src + 8 * (sp ? j : 2 * j));
+    x.hi = *reinterpret_cast<const uint4*>(src + 8 * (sp ? j + turned : 2 * j + 1));
   };
 
-  Item cur = load(threadIdx.x);
+  Row next{0, (int)threadIdx.x / kLanes, make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  load(next);
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.indptr && a.indptr[a.batch] > a.total)
     atomicOr(&g_append_err, kErrBadIndptr);
   if (warp < n_tok) {
@@ -229,21 +238,21 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   }
   __syncthreads();
 
-  const uint32_t n_round = (n_items + kAppendThreads - 1) / kAppendThreads;
-  for (uint32_t n = 0; n < n_round; ++n) {
-    const uint32_t i = n * kAppendThreads + threadIdx.x;
-    const Item it = cur;
-    cur = load(i + kAppendThreads);
-    int tok = 0, row = 0, j = 0, v0, v1;
-    const bool have = i < n_items;
-    if (have) where(i, tok, row, j);
-    vectors(row, j, v0, v1);
-    const TokenPlace p = place[tok];
-    const bool live = have && p.pos >= 0;
+  // (NVFP4: a warp's four rows are of one token and one kind -- 32 or 0 q heads, 8 of k and
+  // 8 of v -- so that its lanes take every branch together and the shuffles are whole.)
+  while (next.tok < n_tok) {
+    const Row cur = next;
+    next.row += kStep;
+    load(next);
+    const TokenPlace p = place[cur.tok];
+    if (p.pos < 0) continue;
+    const int row = cur.row;
+    const bool sp = split(row);
+    const int v0 = sp ? j : 2 * j, v1 = sp ? j + turned : 2 * j + 1;
     float x[8], y[8];
-    unpack8(it.lo, x, T());
-    unpack8(it.hi, y, T());
-    if (live && row < hq + a.hkv && j < turned) {
+    unpack8(cur.lo, x, T());
+    unpack8(cur.hi, y, T());
+    if (row < hq + a.hkv && j < turned) {
       const float* cs = a.rope + p.pos * a.rot + 8 * j;
       float c[8], s[8];
       *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs);
@@ -269,30 +278,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
         }
       }
     }
-    // The largest magnitudes of an NVFP4 block: a rotated half-split row has its
-    // blocks in two neighbouring lanes (rot is a multiple of 32, so lanes 2i and
-    // 2i+1 hold the halves of one block, twice); otherwise a lane has a whole one.
-    float ax = 0.f, ay = 0.f;
-    const bool split = v1 != v0 + 1;
-    if (kMode == kAppendNvfp4) {
-      ax = amax8(x);
-      ay = amax8(y);
-      const float ox = __shfl_xor_sync(0xffffffffu, ax, 1), oy = __shfl_xor_sync(0xffffffffu, ay, 1);
-      if (split) {
-        ax = max_nan(ax, ox);
-        ay = max_nan(ay, oy);
-      } else {
-        ax = max_nan(ax, ay);
-      }
-    }
-    if (!live) continue;
     if (row < hq) {
       if (kMode == kAppendNvfp4) {
-        uint8_t* dst = static_cast<uint8_t*>(a.q_out) + (t0 + tok) * a.qo_tok + row * a.qo_head;
+        uint8_t* dst = static_cast<uint8_t*>(a.q_out) + (t0 + cur.tok) * a.qo_tok + row * a.qo_head;
         *reinterpret_cast<uint2*>(dst + 8 * v0) = pack8_e4m3(x, a.inv_q);
         *reinterpret_cast<uint2*>(dst + 8 * v1) = pack8_e4m3(y, a.inv_q);
       } else {
-        T* dst = static_cast<T*>(a.q_out) + (t0 + tok) * a.qo_tok + row * a.qo_head;
+        T* dst = static_cast<T*>(a.q_out) + (t0 + cur.tok) * a.qo_tok + row * a.qo_head;
         *reinterpret_cast<uint4*>(dst + 8 * v0) = pack8(x, T());
         *reinterpret_cast<uint4*>(dst + 8 * v1) = pack8(y, T());
       }
@@ -304,9 +296,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
       const int64_t r = (p.page * kHkv + h) * kPage + p.slot;
       uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + r * (D / 2);
       uint8_t* sf = (is_v ? a.v_sf : a.k_sf) + r * (D / 16);
-      float sx, sy;
-      if (split) {
-        const uint32_t bx = block_scale(ax, &sx), by = block_scale(ay, &sy);
+      // A rotated half-split row has its blocks in two neighbouring lanes (rot is a
+      // multiple of 32: lanes 2i and 2i+1 hold the halves of one block, twice);
+      // otherwise a lane has a whole one.
+      float ax = amax8(x), ay = amax8(y), sx, sy;
+      const float ox = __shfl_xor_sync(0xffffffffu, ax, 1), oy = __shfl_xor_sync(0xffffffffu, ay, 1);
+      if (sp) {
+        const uint32_t bx = block_scale(max_nan(ax, ox), &sx), by = block_scale(max_nan(ay, oy), &sy);
         *reinterpret_cast<uint32_t*>(codes + 4 * v0) = codes8(x, sx);
         *reinterpret_cast<uint32_t*>(codes + 4 * v1) = codes8(y, sy);
         if ((j & 1) == 0) {
@@ -314,7 +310,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
           sf[v1 / 2] = (uint8_t)by;
         }
       } else {
-        sf[j] = (uint8_t)block_scale(ax, &sx);
+        sf[j] = (uint8_t)block_scale(max_nan(ax, ay), &sx);
         *reinterpret_cast<uint2*>(codes + 8 * j) = make_uint2(codes8(x, sx), codes8(y, sx));
       }
     } else {
@@ -337,14 +333,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 
 template <typename T, int kMode>
 cudaError_t launch_d(const AppendArgs& a, unsigned grid, cudaStream_t stream) {
-  if (kMode == kAppendNvfp4) {
+  if constexpr (kMode == kAppendNvfp4) {
     append_kernel<T, kD, kMode><<<grid, kAppendThreads, 0, stream>>>(a);
-    return cudaGetLastError();
-  }
-  switch (a.d) {
-    case 64: append_kernel<T, 64, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
-    case 128: append_kernel<T, 128, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
-    default: append_kernel<T, 256, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
+  } else {
+    switch (a.d) {
+      case 64: append_kernel<T, 64, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
+      case 128: append_kernel<T, 128, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
+      default: append_kernel<T, 256, kMode><<<grid, kAppendThreads, 0, stream>>>(a); break;
+    }
   }
   return cudaGetLastError();
 }
