@@ -993,8 +993,8 @@ gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, cons
   if (ps[0] < 1 || ps[0] > 2147483647LL) return fail(GQA_ERR_INVALID_ARG, "num_pages %lld out of range", (long long)ps[0]);
   if (bs[1] < 1 || bs[1] > (int64_t(1) << 30) / ps[2])
     return fail(GQA_ERR_INVALID_ARG, "max_pages_per_seq %lld out of range", (long long)bs[1]);
-  // (a block of the kernel counts the tiles, of 32 tokens at least, of its share in 31 bits)
-  if (qs[0] * ps[1] * ((qs[1] / ps[1] + 7) / 8) > (int64_t(1) << 38) / (bs[1] * ps[2] / 32 + 1))
+  // (a block of the kernel counts the work of its share, in tiles of 32 tokens at least, in 31 bits)
+  if (qs[0] * ps[1] * ((qs[1] / ps[1] + 7) / 8) > (int64_t(1) << 38) / (bs[1] * ps[2] / 32 + 16))
     return fail(GQA_ERR_UNSUPPORTED, "batch %lld x %lld KV heads x %lld tokens of capacity are too many", (long long)qs[0],
                 (long long)ps[1], (long long)(bs[1] * ps[2]));
   if (!std::isfinite(q_scale)) return fail(GQA_ERR_INVALID_ARG, "q_scale is not finite");

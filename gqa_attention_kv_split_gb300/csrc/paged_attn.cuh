@@ -28,7 +28,7 @@
 //    found by exchanges of a 64-bit number of the call's own, so that the workspace
 //    needs no preparation.
 //  * Producer warps move tiles of 64 (32) tokens with tensor-map TMA copies
-//    into a ring of about 190 KB: any page size and cache order is a box of the
+//    into a ring of 128 KB: any page size and cache order is a box of the
 //    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
 //  * Eight consumer warps (four at head dim 256), each with its own 32 keys of a tile and its own
 //    (m, l, o); groups of warps take tiles in turn, so that one tile's softmax
@@ -77,7 +77,12 @@ struct Shape {
   static constexpr int kGroupWarps = kTile / (16 * kBlocks);  // warps that share a tile
   static constexpr int kGroups = kWarps / kGroupWarps;      // tiles in work at a time
   static constexpr int kHalf = kTile * kRow;                // bytes of K (and of V) of a stage
-  static constexpr int kRoom = D > 128 ? 128 * 1024 : 192 * 1024;  // the join's buffers take the rest
+  // What starting and ending a unit costs, in tiles: about the time of 96 KB of K and V
+  // for 8 heads, twice that for 16.  (12 sequences of up to 8192 tokens in bf16: 43.0 us
+  // without it, 38.3 with 2 or 8 tiles; with 16 heads a KV head 62.6 us, 47.5 with 2,
+  // 43.9 with 8; 48 of up to 16001 in E4M3: 147.4, 140.5 with 2, 136.4 with 8.)
+  static constexpr int kUnitWork = NT * 96 * 1024 / (2 * kHalf);
+  static constexpr int kRoom = 128 * 1024;  // the warps' join takes up to 68 KB
   // A whole number of groups' turns, so that a stage always belongs to one group (a
   // wait on its barrier can then never be a phase behind).
   static constexpr int kStages = kRoom / (2 * kHalf) / kGroups * kGroups;
@@ -86,7 +91,7 @@ struct Shape {
 
 // A unit that lies in several blocks' shares.
 struct Piece {
-  int64_t tile0;    // its first tile, counted over the call
+  int64_t tile0;    // its first tile in the work of the call
   int b, unit;      // sequence, unit within it
   int tiles;
   int first, last;  // the blocks that hold it
@@ -110,7 +115,7 @@ template <int kWarps, int D, int NT>
 struct Smem {
   static constexpr int kRows = 8 * NT;
   alignas(16) uint8_t q[2][kRows][D * 2 + 16];
-  alignas(16) float o[kWarps][4][D + 4];  // four heads at a time; the odd row length spreads the banks
+  alignas(16) float o[kWarps][kRows][D + 4];  // (the odd row length spreads the banks)
   float m[kWarps][kRows];
   float l[kWarps][kRows];
   alignas(8) uint64_t full[32];
@@ -119,7 +124,7 @@ struct Smem {
   uint64_t q_empty[2];
   int64_t scan[kWarps + 4];
   int most[kWarps + 4];
-  int64_t total;  // tiles of the whole call
+  int64_t total;  // work of the whole call
   int n_blocks;   // blocks with a share
   int64_t end;    // of this block's share
   int64_t rem;    // the share's first tile within its first sequence,
@@ -194,27 +199,40 @@ struct Span {
   }
 };
 
-// Walks the units of a block's share, which is counted in tiles, or in whole units.  (A
-// share has fewer than 2^31 tiles: the host sees to it.)
-template <int kTile>
+// Walks the units of a block's share.  Shares are counted in the work of a unit: its
+// tiles and, before them, what starting and ending a unit costs in tiles (kUnitWork);
+// or, by_unit, in whole units.  (A share has less than 2^31: the host sees to it.)
+template <int kTile, int kUnitWork>
 struct Walk {
-  int left;   // of the share from the piece's start on
+  int left;   // of the share: from the piece's first tile on; by_unit: units behind this one
   int b;      // sequence
   int unit;   // within the sequence: kv head * head blocks + head block
   int t_beg;  // first tile of the piece within the unit, and one past its last
   int t_end;
   Span<kTile> span;
   bool by_unit;
-  __device__ __forceinline__ Walk(const Params& p, int left_, int b_, int64_t rem, bool by_unit_)
-      : left(left_), b(b_), span(p, b_), by_unit(by_unit_) {
-    unit = by_unit ? (int)rem : (int)(rem / span.tiles);
-    t_beg = by_unit ? 0 : (int)(rem - (int64_t)unit * span.tiles);
-    t_end = by_unit ? span.tiles : min(span.tiles, t_beg + left);
+  // From `rem` into the sequence's work on; valid() says whether there is a tile.
+  __device__ __forceinline__ Walk(const Params& p, int share, int b_, int64_t rem, bool by_unit_)
+      : b(b_), span(p, b_), by_unit(by_unit_) {
+    if (by_unit) {
+      unit = (int)rem;
+      t_beg = 0;
+      t_end = span.tiles;
+      left = share - 1;
+    } else {
+      const int work = span.tiles + kUnitWork;
+      unit = (int)(rem / work);
+      const int at = (int)(rem - (int64_t)unit * work);
+      t_beg = max(0, at - kUnitWork);
+      left = share - max(0, kUnitWork - at);
+      t_end = min(span.tiles, t_beg + left);
+    }
   }
+  __device__ __forceinline__ bool valid() const { return by_unit || left > 0; }
   // To the next piece; false at the end of the share.
   __device__ __forceinline__ bool next(const Params& p) {
-    left -= by_unit ? 1 : t_end - t_beg;
-    if (left <= 0) return false;
+    left -= by_unit ? 1 : t_end - t_beg + kUnitWork;
+    if (by_unit ? left < 0 : left <= 0) return false;
     t_beg = 0;
     if (++unit == p.hkv * p.head_blocks) {
       unit = 0;
@@ -292,6 +310,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   using S = Shape<kCache, D, NT>;
   constexpr bool kBf16 = kCache == kCacheBf16;
   constexpr bool kFp8 = kCache == kCacheE4m3;
+  constexpr int kUnitWork = S::kUnitWork;
   constexpr int kTile = S::kTile, kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr int kRows = 8 * NT;
   constexpr int kTileShift = kTile == 32 ? 5 : kTile == 64 ? 6 : 7;
@@ -318,7 +337,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 
-  // ---- this block's share: tiles [T * block / n, T * (block + 1) / n), or one whole
+  // ---- this block's share: of the work [T * block / n, T * (block + 1) / n), or one whole
   // unit if there are no more units than blocks and none has more than kWholeTiles tiles:
   // to read them takes less time than to join the pieces of a split unit (2 sequences
   // of up to 200 tokens, 8 KV heads: 8.9 us split, 6.6 us whole).
@@ -364,7 +383,10 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   }
   before += incl - mine;
   const bool by_unit = most <= kWholeTiles && (total >> kCountAt) * units <= kGrid;
-  auto counted = [&](int64_t sum) { return (by_unit ? sum >> kCountAt : sum & ((int64_t(1) << kCountAt) - 1)) * units; };
+  auto counted = [&](int64_t sum) {
+    const int64_t n = sum >> kCountAt;
+    return (by_unit ? n : (sum & ((int64_t(1) << kCountAt) - 1)) + n * kUnitWork) * units;
+  };
   before = counted(before);
   total = counted(total);
   mine = counted(mine);
@@ -382,7 +404,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     int64_t b = s0;
     for (;; ++b) {
       const int tiles = Span<kTile>(p, b).tiles;
-      const int64_t n = (int64_t)(by_unit ? tiles > 0 : tiles) * units;
+      const int64_t n = (int64_t)(tiles == 0 ? 0 : by_unit ? 1 : tiles + kUnitWork) * units;
       if (rem < n) break;
       rem -= n;
     }
@@ -391,7 +413,8 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   }
   __syncthreads();
   if (beg >= end) return;
-  Walk<kTile> walk(p, (int)(end - beg), sm.b0, sm.rem, by_unit);
+  Walk<kTile, kUnitWork> walk(p, (int)(end - beg), sm.b0, sm.rem, by_unit);
+  if (!walk.valid()) return;  // (a share that lies before a unit's first tile)
 
   if (warp >= kWarps) {
     // ---------------- producer ------------------------------------------------
@@ -761,7 +784,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     }
     skip = tile - walk.t_end;
 
-    // ---- join the warps --------------------------------------------------
+    // ---- join the warps: (m, l) and o as they are, put together by the reading threads ----
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -769,63 +792,54 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
         l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
         l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
         l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
-        if (g == 0) {
-          sm.m[warp][8 * t + c2 + i] = m[t][i];
-          sm.l[warp][8 * t + c2 + i] = l[t][i];
-        }
       }
     const bool whole = walk.whole();
     const int slot = seg == 1 ? 0 : 1;
     const int64_t piece = ((int64_t)blockIdx.x * 2 + slot) * kRows;
+    if (seg > 1) named_bar_sync(1, kWarps * 32);  // the last unit has been read
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (8 * t + c2 >= heads) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (g == 0) {
+          sm.m[warp][8 * t + c2 + i] = m[t][i];
+          sm.l[warp][8 * t + c2 + i] = l[t][i];
+        }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // element of the head dim in row g (+ 8) of this 16-row block
+          const int d = kFp8 ? 16 * i + 2 * g + (e >> 1) : 16 * i + g + 8 * (e >> 1);
+          sm.o[warp][8 * t + c2 + (e & 1)][d] = o[t][i][e];
+        }
+    }
     named_bar_sync(1, kWarps * 32);
+    for (int i = threadIdx.x; i < heads * (D / 2); i += kWarps * 32) {
+      const int r = i / (D / 2), d = (i % (D / 2)) * 2;
+      float mw[kWarps], mm = -INFINITY;
 #pragma unroll
-    for (int q4 = 0; q4 < 2 * NT; ++q4) {
-      if (4 * q4 >= heads) break;  // the same for every warp
-      constexpr int kHeads = 4;
-      const int t = q4 / 2;
-      if ((c2 >> 2) == (q4 & 1)) {
-        float f[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mm = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][8 * t + c2 + i]);
-          f[i] = m[t][i] == -INFINITY ? 0.f : fast_exp2(m[t][i] - mm);
-        }
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // element of the head dim in row g (+ 8) of this 16-row block
-            const int d = kFp8 ? 16 * i + 2 * g + (e >> 1) : 16 * i + g + 8 * (e >> 1);
-            sm.o[warp][(c2 & 3) + (e & 1)][d] = o[t][i][e] * f[e & 1];
-          }
+      for (int w = 0; w < kWarps; ++w) {
+        mw[w] = sm.m[w][r];
+        mm = fmaxf(mm, mw[w]);
       }
-      named_bar_sync(1, kWarps * 32);
-      const int hn = min(kHeads, heads - kHeads * q4);
-      for (int i = threadIdx.x; i < hn * (D / 2); i += kWarps * 32) {
-        const int h = i / (D / 2), d = (i % (D / 2)) * 2;
-        const int r = kHeads * q4 + h;
-        float mm = -INFINITY;
+      float ll = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
-        float ll = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (sm.m[w][r] != -INFINITY) ll = fmaf(sm.l[w][r], fast_exp2(sm.m[w][r] - mm), ll);
-          const float2 u = *reinterpret_cast<const float2*>(&sm.o[w][h][d]);
-          x += u.x;
-          y += u.y;
-        }
-        if (dead) continue;
-        if (whole) {
-          store_out<D>(p, (int64_t)walk.b * p.hq + h0 + r, d, x, y, mm - kShift, ll);
-        } else {
-          *reinterpret_cast<float2*>(p.part_o + (piece + r) * D + d) = make_float2(x, y);
-          if (d == 0) p.part_ml[piece + r] = make_float2(mm - kShift, ll);
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = mw[w] == -INFINITY ? 0.f : fast_exp2(mw[w] - mm);  // 0: a warp that saw no key
+        const float2 u = *reinterpret_cast<const float2*>(&sm.o[w][r][d]);
+        ll = fmaf(sm.l[w][r], f, ll);
+        x = fmaf(u.x, f, x);
+        y = fmaf(u.y, f, y);
       }
-      named_bar_sync(1, kWarps * 32);  // the buffers are free again
+      if (dead) continue;
+      if (whole) {
+        store_out<D>(p, (int64_t)walk.b * p.hq + h0 + r, d, x, y, mm - kShift, ll);
+      } else {
+        *reinterpret_cast<float2*>(p.part_o + (piece + r) * D + d) = make_float2(x, y);
+        if (d == 0) p.part_ml[piece + r] = make_float2(mm - kShift, ll);
+      }
     }
     if (!whole) {
       pieces |= 1 << slot;
@@ -849,8 +863,9 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   // fence between: of blocks that end together at least one sees them all (should two,
   // they write the same values).  Nobody waits, and who joins clears the words: a replay
   // of a captured call has the same nonce.
+  named_bar_sync(1, kWarps * 32);
   if (warp == 0) {
-    if (lane == 0) __threadfence();  // (the last barrier ordered the pieces' stores before it)
+    if (lane == 0) __threadfence();  // (the barrier ordered every thread's part of the pieces before it)
     __syncwarp();
     unsigned long long* const words = reinterpret_cast<unsigned long long*>(p.words);
     bool many = false;  // lane i: piece i is one of more than two, and its word is set
@@ -860,7 +875,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       if ((pieces >> lane) & 1) {
         u.first = share_of(u.tile0, sm.total, sm.n_blocks);
         u.last = share_of(u.tile0 + u.tiles - 1, sm.total, sm.n_blocks);
-        u.first_slot = share_begin(u.first, sm.total, sm.n_blocks) == u.tile0 ? 0 : 1;
+        u.first_slot = share_begin(u.first, sm.total, sm.n_blocks) >= u.tile0 - kUnitWork ? 0 : 1;
         many = u.last - u.first > 1;
         if (many) {
           *reinterpret_cast<volatile unsigned long long*>(words + u.word(blockIdx.x)) = p.nonce;
