@@ -1041,8 +1041,8 @@ gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, cons
   a.hkv = (int)ps[1];
   a.d = (int)qs[2];
   a.page_size = (int)ps[2];
-  a.q_bf16 = q->dtype == GQA_BF16;
-  a.cache = e4m3 ? gqa::kCacheE4m3 : a.q_bf16 ? gqa::kCacheBf16 : gqa::kCacheF16;
+  const bool bf16 = q->dtype == GQA_BF16;
+  a.cache = e4m3 ? (bf16 ? gqa::kCacheE4m3 : gqa::kCacheE4m3F16) : bf16 ? gqa::kCacheBf16 : gqa::kCacheF16;
   a.scale = (float)((double)q_scale * k_scale / std::sqrt((double)qs[2]));
   a.v_scale = v_scale;
   a.softcap = softcap;

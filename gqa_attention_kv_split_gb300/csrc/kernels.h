@@ -166,7 +166,9 @@ cudaError_t append_read_errors(uint32_t* word);
 
 // ---- one-token attention over a paged cache ---------------------------------
 
-enum CacheType { kCacheF16 = 0, kCacheBf16 = 1, kCacheE4m3 = 2 };
+// The pages' type, and with it the queries' and outputs': f16 pages, bf16 pages, E4M3
+// pages with bf16 queries, E4M3 pages with f16 queries.
+enum CacheType { kCacheF16 = 0, kCacheBf16 = 1, kCacheE4m3 = 2, kCacheE4m3F16 = 3 };
 
 struct PagedAttnArgs {
   const void* q;               // [batch, hq, d] f16 or bf16
@@ -178,7 +180,8 @@ struct PagedAttnArgs {
   int64_t q_seq, q_head;       // elements
   int64_t kp_page, kp_head, kp_slot, vp_page, vp_head, vp_slot;  // elements
   int64_t batch, num_pages, max_pages_per_seq;
-  int hq, hkv, d, page_size, q_bf16, cache;
+  int hq, hkv, d, page_size;
+  int cache;                   // a CacheType
   float scale, v_scale;        // of the scores (q_scale * k_scale / sqrt(d)) and of the output
   float softcap;               // 0: none
   int window;                  // 0: none

@@ -31,7 +31,7 @@ cudaError_t make_map(const void* pages, const PagedAttnArgs& a, int64_t s_page, 
       g_encode = reinterpret_cast<EncodeTiledFn>(fn);
   });
   if (!g_encode) return cudaErrorNotSupported;
-  const int64_t esz = a.cache == kCacheE4m3 ? 1 : 2;
+  const int64_t esz = a.cache >= kCacheE4m3 ? 1 : 2;
   const int64_t row = a.d * esz, chunk = row < 128 ? row : 128;
   const cuuint64_t dims[5] = {(cuuint64_t)chunk, (cuuint64_t)a.page_size, (cuuint64_t)(row / chunk), (cuuint64_t)a.hkv,
                               (cuuint64_t)a.num_pages};
@@ -68,7 +68,7 @@ size_t paged_attn_workspace_bytes(int hq, int hkv, int d) {
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStream_t stream) {
-  const int row_bytes = a.d * (a.cache == kCacheE4m3 ? 1 : 2);
+  const int row_bytes = a.d * (a.cache >= kCacheE4m3 ? 1 : 2);
   const int tile = pa::tile_of(row_bytes);
   pa::Params p;
   p.q = a.q;
@@ -96,7 +96,6 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   }
   for (p.box_shift = 0; (1 << p.box_shift) < box; ++p.box_shift) {
   }
-  p.q_bf16 = a.q_bf16;
   const double log2e = 1.4426950408889634;
   p.scale_log2 = (float)(a.scale * log2e);
   p.cap_in = a.softcap > 0.f ? (float)(2.0 * log2e * a.scale / a.softcap) : 0.f;
@@ -111,7 +110,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   switch (a.cache) {
     case kCacheF16: return pa::launch_f16(p, a.d, k_map, v_map, stream);
     case kCacheBf16: return pa::launch_bf16(p, a.d, k_map, v_map, stream);
-    default: return pa::launch_e4m3(p, a.d, k_map, v_map, stream);
+    case kCacheE4m3: return pa::launch_e4m3(p, a.d, k_map, v_map, stream);
+    default: return pa::launch_e4m3_f16(p, a.d, k_map, v_map, stream);
   }
 }
 

@@ -56,7 +56,7 @@ __device__ uint32_t g_paged_attn_err;  // of this translation unit's kernels
 
 template <int kCache, int D, int NT>
 struct Shape {
-  static constexpr int kEsz = kCache == kCacheE4m3 ? 1 : 2;
+  static constexpr int kEsz = kCache >= kCacheE4m3 ? 1 : 2;
   static constexpr int kRow = D * kEsz;                     // bytes of a token's row
   static constexpr int kChunk = kRow < 128 ? kRow : 128;    // bytes of a swizzled row in shared memory
   static constexpr int kChunks = kRow / kChunk;
@@ -173,6 +173,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ float f16_lo(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)x)); }
+__device__ __forceinline__ float f16_hi(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
@@ -247,10 +249,10 @@ struct Walk {
 };
 
 // Elements d, d + 1 of a head's output from sums relative to exp2(mm), and its lse.
-template <int D>
+template <int D, bool kQBf16>
 __device__ __forceinline__ void store_out(const Params& p, int64_t row, int d, float x, float y, float mm, float l) {
   const float inv = p.v_scale / l;
-  const uint32_t pk = p.q_bf16 ? pack_bf16(x * inv, y * inv) : pack_f16(x * inv, y * inv);
+  const uint32_t pk = kQBf16 ? pack_bf16(x * inv, y * inv) : pack_f16(x * inv, y * inv);
   *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (row * D + d) * 2) = pk;
   if (d == 0 && p.lse) p.lse[row] = mm * 0.6931471805599453f + logf(l);
 }
@@ -266,7 +268,7 @@ __device__ __forceinline__ float2 load_l2(const float2* p) {
 
 // Joins the pieces of a unit, in the order of its tiles: thread i of n takes the pairs of
 // elements i, i + n, ...
-template <int D, int NT>
+template <int D, int NT, bool kQBf16>
 __device__ __forceinline__ void join_pieces(const Params& p, const Piece& u, int i, int n) {
   constexpr int kRows = 8 * NT, kBatch = 8;
   const int kvh = u.unit / p.head_blocks;
@@ -299,7 +301,7 @@ __device__ __forceinline__ void join_pieces(const Params& p, const Piece& u, int
         y = fmaf(y, f, v[e].y * g);
       }
     }
-    store_out<D>(p, (int64_t)u.b * p.hq + h0 + r, d, x, y, m, l);
+    store_out<D, kQBf16>(p, (int64_t)u.b * p.hq + h0 + r, d, x, y, m, l);
   }
 }
 
@@ -309,7 +311,13 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   uint32_t* const err = &g_paged_attn_err;
   using S = Shape<kCache, D, NT>;
   constexpr bool kBf16 = kCache == kCacheBf16;
-  constexpr bool kFp8 = kCache == kCacheE4m3;
+  constexpr bool kFp8 = kCache >= kCacheE4m3;
+  constexpr bool kQBf16 = kBf16 || kCache == kCacheE4m3;  // the type of q and of the output
+  // A weight enters the product with V as two terms of the cache's type (22 bits of it,
+  // 16 in bf16), so that its rounding stays below the output's.  For E4M3 pages and bf16
+  // queries one f16 term does: its 11 bits are three more than the output's (48 sequences
+  // of up to 16001 tokens, 16 heads a KV head: 170 us with one, 197 with two).
+  constexpr bool kTwo = !kFp8 || !kQBf16;
   constexpr int kUnitWork = S::kUnitWork;
   constexpr int kTile = S::kTile, kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr int kRows = 8 * NT;
@@ -571,7 +579,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
         }
       }
       sc[t][0] = sc[t][1] = 1.f;
-      if (kFp8 && p.q_bf16) {
+      if (kFp8 && kQBf16) {
         // bf16 rows enter the f16 product scaled by a power of two that brings their
         // largest element into [1, 2): exact but for elements below 2^-14 of it, whose
         // rounding is at most 2^-25 of the largest.
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
           __syncwarp();
         }
         // ---- softmax weights: rows (keys) g, g + 8 of each block; columns (heads) c2, c2 + 1
-        uint32_t pb[kBlocks][NT][2], pl[kBlocks][NT][2];
+        uint32_t pb[kBlocks][NT][2], pl[kBlocks][NT][2];  // the weights' two terms
         float alpha[NT][2];
         bool grow = false;
 #pragma unroll
@@ -714,9 +722,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
             }
             l[t][i] = fmaf(l[t][i], alpha[t][i], sum);
           }
-          // P^T as the B operand of O^T = V^T P^T: rows = keys, columns = heads.  A bf16
-          // weight is split into two bf16 terms (16 bits of it are kept); an f16 weight is
-          // rounded once, to 11 bits.
+          // P^T as the B operand of O^T = V^T P^T: rows = keys, columns = heads
 #pragma unroll
           for (int j = 0; j < kBlocks; ++j) {
             const float* v = s[j][t];
@@ -727,8 +733,13 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
               pl[j][t][0] = movm_t(pack_bf16(v[0] - bf16_lo(x0), v[1] - bf16_hi(x0)));
               pl[j][t][1] = movm_t(pack_bf16(v[2] - bf16_lo(x1), v[3] - bf16_hi(x1)));
             } else {
-              pb[j][t][0] = movm_t(pack_f16(v[0], v[1]));
-              pb[j][t][1] = movm_t(pack_f16(v[2], v[3]));
+              const uint32_t x0 = pack_f16(v[0], v[1]), x1 = pack_f16(v[2], v[3]);
+              pb[j][t][0] = movm_t(x0);
+              pb[j][t][1] = movm_t(x1);
+              if (kTwo) {
+                pl[j][t][0] = movm_t(pack_f16(v[0] - f16_lo(x0), v[1] - f16_hi(x0)));
+                pl[j][t][1] = movm_t(pack_f16(v[2] - f16_lo(x1), v[3] - f16_hi(x1)));
+              }
             }
           }
         }
@@ -751,7 +762,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 mma<kBf16>(o[t][i], a, pb[j][t][0], pb[j][t][1]);
-                if (kBf16) mma<kBf16>(o[t][i], a, pl[j][t][0], pl[j][t][1]);
+                if (kTwo) mma<kBf16>(o[t][i], a, pl[j][t][0], pl[j][t][1]);
               }
             }
         } else {
@@ -768,7 +779,10 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
                 const uint32_t a[4] = {e4m3_to_f16x2(lo & 0xffffu), e4m3_to_f16x2(lo >> 16), e4m3_to_f16x2(hi & 0xffffu),
                                        e4m3_to_f16x2(hi >> 16)};
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma<false>(o[t][2 * k + i], a, pb[j][t][0], pb[j][t][1]);
+                for (int t = 0; t < NT; ++t) {
+                  mma<false>(o[t][2 * k + i], a, pb[j][t][0], pb[j][t][1]);
+                  if (kTwo) mma<false>(o[t][2 * k + i], a, pl[j][t][0], pl[j][t][1]);
+                }
               }
             }
         }
@@ -835,7 +849,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       }
       if (dead) continue;
       if (whole) {
-        store_out<D>(p, (int64_t)walk.b * p.hq + h0 + r, d, x, y, mm - kShift, ll);
+        store_out<D, kQBf16>(p, (int64_t)walk.b * p.hq + h0 + r, d, x, y, mm - kShift, ll);
       } else {
         *reinterpret_cast<float2*>(p.part_o + (piece + r) * D + d) = make_float2(x, y);
         if (d == 0) p.part_ml[piece + r] = make_float2(mm - kShift, ll);
@@ -902,7 +916,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   }
   named_bar_sync(1, kWarps * 32);
   for (int i = 0; i < 2; ++i)
-    if (sm.piece[i].join) join_pieces<D, NT>(p, sm.piece[i], threadIdx.x, kWarps * 32);
+    if (sm.piece[i].join) join_pieces<D, NT, kQBf16>(p, sm.piece[i], threadIdx.x, kWarps * 32);
 }
 
 template <int kCache, int D, int NT>

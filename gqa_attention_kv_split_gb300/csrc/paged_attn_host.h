@@ -29,7 +29,6 @@ struct Params {
   int64_t q_seq, q_head, batch, num_pages, max_pages;
   int hq, hkv, group, head_blocks;
   int page_shift, box_shift;  // log2 of a page's tokens, and of those of one copy
-  int q_bf16;
   float scale_log2;  // scores to the exp2 domain
   float cap_in, cap_out;  // softcap: s2 = cap_out * tanh, tanh's argument doubled in the exp2 domain = cap_in * score; cap_out 0: none
   float v_scale;
@@ -40,6 +39,7 @@ struct Params {
 cudaError_t launch_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_bf16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_e4m3(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_e4m3_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t read_errors_f16(uint32_t* word);
 cudaError_t read_errors_bf16(uint32_t* word);
 cudaError_t read_errors_e4m3(uint32_t* word);

@@ -91,11 +91,12 @@ def check_attention(got, got_lse, q, k_pages, v_pages, table, lens, **kw):
     of a tensor-core step each (D <= 256): |error| <= 16 * 2^-23 * sum |q_i k_i| * scale; capping adds
     at most 4 roundings of an exponential's 2^-22 times the cap; the logarithm and the scale 2^-20 (1 +
     |lse|).  A weight is off by twice the scores' error (its own and the sum's) and by its rounding for
-    the product with V: 2^-11 for f16 (f16 and E4M3 pages), 2^-16 for a bf16 pair.  An output is a
-    weighted sum, off by that times sum p |v|, and is rounded once by half a step of its type."""
+    the product with V: 2^-16 for a pair of terms, 2^-11 for the one f16 term of E4M3 pages and bf16
+    queries.  An output is a weighted sum, off by that times sum p |v|, and is rounded once by half a step
+    of its type."""
     out, lse, mag, reach = attention(q.cpu(), k_pages.cpu(), v_pages.cpu(), table.cpu(), lens.cpu(), **kw)
     s_err = 2.0 ** -19 * reach + 2.0 ** -20 * kw.get("softcap", 0.0) + 2.0 ** -20
-    w = 2.0 ** -16 if k_pages.dtype == torch.bfloat16 else 2.0 ** -11
+    w = 2.0 ** -11 if k_pages.dtype == torch.float8_e4m3fn and q.dtype == torch.bfloat16 else 2.0 ** -16
     fin = torch.finfo(got.dtype)
     tol = fin.eps / 2 * out.abs() + (1 + fin.eps) * (w + 2 * s_err)[..., None] * mag + fin.smallest_normal * fin.eps
     err = (got.cpu().double() - out).abs()
