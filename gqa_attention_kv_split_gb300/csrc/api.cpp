@@ -17,6 +17,7 @@
 #include <initializer_list>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <string>
@@ -252,6 +253,18 @@ gqa_status check_devices(std::initializer_list<std::pair<const gqa_tensor*, cons
     gqa_status _s = (expr);            \
     if (_s != GQA_OK) return _s;       \
   } while (0)
+
+// Runs an entry point's body; no exception (a failed allocation on the host) crosses the boundary.
+template <typename F>
+gqa_status guarded(F&& body) {
+  try {
+    return body();
+  } catch (const std::exception& e) {
+    return fail(GQA_ERR_OOM, "%s", e.what());
+  } catch (...) {
+    return fail(GQA_ERR_OOM, "an exception");
+  }
+}
 
 std::atomic<int> g_starve{0};
 std::atomic<int> g_ctx_stages{0}, g_ctx_slots{0}, g_decode_stages{0}, g_ctx_grid{0};
@@ -761,13 +774,13 @@ gqa_status check_strided(const gqa_tensor* t, const char* name, std::initializer
     return fail(GQA_ERR_INVALID_ARG, "%s: the last dimension is not dense (stride %lld)", name, (long long)t->strides[nd - 1]);
   for (int d = 0; d < nd - 1; ++d) {
     if (t->shape[d] <= 1) continue;
-    if (t->strides[d] < 0 || t->strides[d] * esz % 16 != 0 || t->strides[d] > (int64_t(1) << 38))
+    if (t->strides[d] < 0 || t->strides[d] > (int64_t(1) << 38) || t->strides[d] * esz % 16 != 0)
       return fail(GQA_ERR_INVALID_ARG, "%s: stride %lld in dimension %d is not a multiple of 16 bytes in [0, 2^38]", name,
                   (long long)t->strides[d], d);
   }
   if (!written) return GQA_OK;
   // Dimensions from the smallest stride up: each steps over all that the smaller ones cover.
-  int64_t covered = t->shape[nd - 1];
+  __int128 covered = t->shape[nd - 1];
   bool used[6] = {};
   for (int k = 0; k < nd - 1; ++k) {
     int at = -1;
@@ -777,7 +790,7 @@ gqa_status check_strided(const gqa_tensor* t, const char* name, std::initializer
     used[at] = true;
     if (t->strides[at] < covered)
       return fail(GQA_ERR_INVALID_ARG, "%s overlaps itself (stride %lld in dimension %d)", name, (long long)t->strides[at], at);
-    covered += t->strides[at] * (t->shape[at] - 1);
+    covered += (__int128)t->strides[at] * (t->shape[at] - 1);
   }
   return GQA_OK;
 }
@@ -903,64 +916,68 @@ gqa_status gqa_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gq
                               gqa_tensor* v_pages, const gqa_tensor* block_table, const gqa_tensor* kv_lens,
                               const gqa_tensor* qo_indptr, const gqa_tensor* rope, gqa_tensor* q_out, int interleaved,
                               float k_scale, float v_scale, gqa_stream_t stream) {
-  gqa::AppendArgs a;
-  std::vector<Named> ts;
-  if (!k) return fail(GQA_ERR_INVALID_ARG, "k: null descriptor");
-  GQA_TRY(append_common(q, k, v, block_table, kv_lens, qo_indptr, rope, q_out, {k->dtype}, -1, -1, -1, 16, interleaved, &a, &ts));
-  int64_t ps[4];
-  GQA_TRY(check_strided(k_pages, "k_pages", {k->dtype, GQA_E4M3, GQA_U8}, {-1, a.hkv, -1, a.d}, true, ps));
-  const bool e4m3 = k_pages->dtype != k->dtype;
-  GQA_TRY(e4m3 ? check_strided(v_pages, "v_pages", {GQA_E4M3, GQA_U8}, {ps[0], a.hkv, ps[2], a.d}, true)
-               : check_strided(v_pages, "v_pages", {k->dtype}, {ps[0], a.hkv, ps[2], a.d}, true));
-  if (a.total > 0 && (ps[2] < 1 || ps[2] > (1 << 20)))
-    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "page size %lld outside [1, 2^20]", (long long)ps[2]);
-  GQA_TRY(check_scale(k_scale, "k_scale"));
-  GQA_TRY(check_scale(v_scale, "v_scale"));
-  if (!e4m3 && (k_scale != 1.f || v_scale != 1.f))
-    return fail(GQA_ERR_INVALID_ARG, "k_scale and v_scale belong to E4M3 pages: 1 is wanted");
-  a.mode = e4m3 ? gqa::kAppendE4m3 : gqa::kAppendSame;
-  a.inv_k = 1.f / k_scale;
-  a.inv_v = 1.f / v_scale;
-  a.k_pages = k_pages->data;
-  a.v_pages = v_pages->data;
-  a.kp_page = stride_of(k_pages, 0);
-  a.kp_head = stride_of(k_pages, 1);
-  a.kp_slot = stride_of(k_pages, 2);
-  a.vp_page = stride_of(v_pages, 0);
-  a.vp_head = stride_of(v_pages, 1);
-  a.vp_slot = stride_of(v_pages, 2);
-  a.num_pages = ps[0];
-  a.page_size = (int)ps[2];
-  ts.push_back({k_pages, "k_pages"});
-  ts.push_back({v_pages, "v_pages"});
-  return run_append(a, ts, "gqa_paged_append", stream);
+  return guarded([&]() -> gqa_status {
+    gqa::AppendArgs a;
+    std::vector<Named> ts;
+    if (!k) return fail(GQA_ERR_INVALID_ARG, "k: null descriptor");
+    GQA_TRY(append_common(q, k, v, block_table, kv_lens, qo_indptr, rope, q_out, {k->dtype}, -1, -1, -1, 16, interleaved, &a, &ts));
+    int64_t ps[4];
+    GQA_TRY(check_strided(k_pages, "k_pages", {k->dtype, GQA_E4M3, GQA_U8}, {-1, a.hkv, -1, a.d}, true, ps));
+    const bool e4m3 = k_pages->dtype != k->dtype;
+    GQA_TRY(e4m3 ? check_strided(v_pages, "v_pages", {GQA_E4M3, GQA_U8}, {ps[0], a.hkv, ps[2], a.d}, true)
+                 : check_strided(v_pages, "v_pages", {k->dtype}, {ps[0], a.hkv, ps[2], a.d}, true));
+    if (a.total > 0 && (ps[2] < 1 || ps[2] > (1 << 20)))
+      return fail(GQA_ERR_UNSUPPORTED_SHAPE, "page size %lld outside [1, 2^20]", (long long)ps[2]);
+    GQA_TRY(check_scale(k_scale, "k_scale"));
+    GQA_TRY(check_scale(v_scale, "v_scale"));
+    if (!e4m3 && (k_scale != 1.f || v_scale != 1.f))
+      return fail(GQA_ERR_INVALID_ARG, "k_scale and v_scale belong to E4M3 pages: 1 is wanted");
+    a.mode = e4m3 ? gqa::kAppendE4m3 : gqa::kAppendSame;
+    a.inv_k = 1.f / k_scale;
+    a.inv_v = 1.f / v_scale;
+    a.k_pages = k_pages->data;
+    a.v_pages = v_pages->data;
+    a.kp_page = stride_of(k_pages, 0);
+    a.kp_head = stride_of(k_pages, 1);
+    a.kp_slot = stride_of(k_pages, 2);
+    a.vp_page = stride_of(v_pages, 0);
+    a.vp_head = stride_of(v_pages, 1);
+    a.vp_slot = stride_of(v_pages, 2);
+    a.num_pages = ps[0];
+    a.page_size = (int)ps[2];
+    ts.push_back({k_pages, "k_pages"});
+    ts.push_back({v_pages, "v_pages"});
+    return run_append(a, ts, "gqa_paged_append", stream);
+  });
 }
 
 gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, gqa_tensor* k_fp4,
                                 gqa_tensor* k_sf, gqa_tensor* v_fp4, gqa_tensor* v_sf, const gqa_tensor* block_table,
                                 const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens, const gqa_tensor* rope,
                                 gqa_tensor* q_out, int interleaved, float q_scale, gqa_stream_t stream) {
-  gqa::AppendArgs a;
-  std::vector<Named> ts;
-  if (!k) return fail(GQA_ERR_INVALID_ARG, "k: null descriptor");
-  GQA_TRY(append_common(q, k, v, block_table, kv_lens, qo_indptr, rope, q_out, {GQA_E4M3, GQA_U8}, 32, 8, 128, 32, interleaved, &a,
-                        &ts));
-  int64_t ps[4];
-  GQA_TRY(check_desc(k_fp4, "k_fp4", {GQA_U8}, {-1, 8, 64, 64}, ps));
-  GQA_TRY(check_desc(k_sf, "k_sf", {GQA_E4M3, GQA_U8}, {ps[0], 8, 64, 8}));
-  GQA_TRY(check_desc(v_fp4, "v_fp4", {GQA_U8}, {ps[0], 8, 64, 64}));
-  GQA_TRY(check_desc(v_sf, "v_sf", {GQA_E4M3, GQA_U8}, {ps[0], 8, 64, 8}));
-  GQA_TRY(check_scale(q_scale, "q_scale"));
-  a.mode = gqa::kAppendNvfp4;
-  a.inv_q = 1.f / q_scale;
-  a.k_pages = k_fp4->data;
-  a.v_pages = v_fp4->data;
-  a.k_sf = static_cast<uint8_t*>(k_sf->data);
-  a.v_sf = static_cast<uint8_t*>(v_sf->data);
-  a.num_pages = ps[0];
-  a.page_size = 64;
-  for (const Named& t : {Named{k_fp4, "k_fp4"}, Named{k_sf, "k_sf"}, Named{v_fp4, "v_fp4"}, Named{v_sf, "v_sf"}}) ts.push_back(t);
-  return run_append(a, ts, "nvfp4_paged_append", stream);
+  return guarded([&]() -> gqa_status {
+    gqa::AppendArgs a;
+    std::vector<Named> ts;
+    if (!k) return fail(GQA_ERR_INVALID_ARG, "k: null descriptor");
+    GQA_TRY(append_common(q, k, v, block_table, kv_lens, qo_indptr, rope, q_out, {GQA_E4M3, GQA_U8}, 32, 8, 128, 32, interleaved, &a,
+                          &ts));
+    int64_t ps[4];
+    GQA_TRY(check_desc(k_fp4, "k_fp4", {GQA_U8}, {-1, 8, 64, 64}, ps));
+    GQA_TRY(check_desc(k_sf, "k_sf", {GQA_E4M3, GQA_U8}, {ps[0], 8, 64, 8}));
+    GQA_TRY(check_desc(v_fp4, "v_fp4", {GQA_U8}, {ps[0], 8, 64, 64}));
+    GQA_TRY(check_desc(v_sf, "v_sf", {GQA_E4M3, GQA_U8}, {ps[0], 8, 64, 8}));
+    GQA_TRY(check_scale(q_scale, "q_scale"));
+    a.mode = gqa::kAppendNvfp4;
+    a.inv_q = 1.f / q_scale;
+    a.k_pages = k_fp4->data;
+    a.v_pages = v_fp4->data;
+    a.k_sf = static_cast<uint8_t*>(k_sf->data);
+    a.v_sf = static_cast<uint8_t*>(v_sf->data);
+    a.num_pages = ps[0];
+    a.page_size = 64;
+    for (const Named& t : {Named{k_fp4, "k_fp4"}, Named{k_sf, "k_sf"}, Named{v_fp4, "v_fp4"}, Named{v_sf, "v_sf"}}) ts.push_back(t);
+    return run_append(a, ts, "nvfp4_paged_append", stream);
+  });
 }
 
 int64_t gqa_paged_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t d) {
@@ -972,94 +989,102 @@ gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, cons
                             const gqa_tensor* block_table, const gqa_tensor* seq_lens, gqa_tensor* out, gqa_tensor* lse,
                             float q_scale, float k_scale, float v_scale, int window, float softcap, void* workspace_,
                             int64_t workspace_bytes, gqa_stream_t stream) {
-  int64_t qs[3], ps[4], bs[2];
-  GQA_TRY(check_strided(q, "q", {GQA_F16, GQA_BF16}, {-1, -1, -1}, false, qs));
-  GQA_TRY(check_strided(k_pages, "k_pages", {q->dtype, GQA_E4M3, GQA_U8}, {-1, -1, -1, qs[2]}, true, ps));
-  const bool e4m3 = k_pages->dtype != q->dtype;
-  GQA_TRY(e4m3 ? check_strided(v_pages, "v_pages", {GQA_E4M3, GQA_U8}, {ps[0], ps[1], ps[2], qs[2]}, true)
-               : check_strided(v_pages, "v_pages", {q->dtype}, {ps[0], ps[1], ps[2], qs[2]}, true));
-  GQA_TRY(check_desc(seq_lens, "seq_lens", {GQA_I32}, {qs[0]}));
-  GQA_TRY(check_desc(block_table, "block_table", {GQA_I32}, {qs[0], -1}, bs));
-  GQA_TRY(check_desc(out, "out", {q->dtype}, {qs[0], qs[1], qs[2]}));
-  if (lse) GQA_TRY(check_desc(lse, "lse", {GQA_F32}, {qs[0], qs[1]}));
-  if (qs[0] < 1 || qs[0] > 65535) return fail(GQA_ERR_UNSUPPORTED, "batch %lld outside [1, 65535]", (long long)qs[0]);
-  if (qs[2] != 64 && qs[2] != 128 && qs[2] != 256)
-    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "head dim %lld is not 64, 128 or 256", (long long)qs[2]);
-  if (ps[1] < 1 || qs[1] < 1 || qs[1] > 1024 || qs[1] % ps[1] != 0)
-    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld query heads over %lld KV heads: 1 to 1024, a multiple, are taken",
-                (long long)qs[1], (long long)ps[1]);
-  if (ps[2] != 16 && ps[2] != 32 && ps[2] != 64 && ps[2] != 128 && ps[2] != 256)
-    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "page size %lld is not 16, 32, 64, 128 or 256", (long long)ps[2]);
-  if (ps[0] < 1 || ps[0] > 2147483647LL) return fail(GQA_ERR_INVALID_ARG, "num_pages %lld out of range", (long long)ps[0]);
-  if (bs[1] < 1 || bs[1] > (int64_t(1) << 30) / ps[2])
-    return fail(GQA_ERR_INVALID_ARG, "max_pages_per_seq %lld out of range", (long long)bs[1]);
-  // (a block of the kernel counts the work of its share, in tiles of 32 tokens at least, in 31 bits)
-  if (qs[0] * ps[1] * ((qs[1] / ps[1] + 7) / 8) > (int64_t(1) << 38) / (bs[1] * ps[2] / 32 + 16))
-    return fail(GQA_ERR_UNSUPPORTED, "batch %lld x %lld KV heads x %lld tokens of capacity are too many", (long long)qs[0],
-                (long long)ps[1], (long long)(bs[1] * ps[2]));
-  if (!std::isfinite(q_scale)) return fail(GQA_ERR_INVALID_ARG, "q_scale is not finite");
-  GQA_TRY(check_scale(k_scale, "k_scale"));
-  GQA_TRY(check_scale(v_scale, "v_scale"));
-  if (window < 0) return fail(GQA_ERR_INVALID_ARG, "window %d is negative", window);
-  if (!std::isfinite(softcap) || softcap < 0.f) return fail(GQA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
-  const int64_t need = gqa_paged_attn_workspace(qs[1], ps[1], qs[2]);
-  if (workspace_ && workspace_bytes < need)
-    return fail(GQA_ERR_INVALID_ARG, "workspace of %lld bytes; %lld are needed", (long long)workspace_bytes, (long long)need);
-  gqa_tensor ws = *q;  // the workspace's place is checked with the tensors'
-  ws.data = workspace_;
-  std::vector<Named> ts = {{q, "q"}, {k_pages, "k_pages"}, {v_pages, "v_pages"}, {block_table, "block_table"},
-                           {seq_lens, "seq_lens"}, {out, "out"}};
-  if (workspace_) ts.push_back({&ws, "workspace"});
-  gqa_tensor l;
-  if (lse) {
-    l = *lse;
-    l.dtype = GQA_I32;  // (4-byte alignment)
-    ts.push_back({&l, "lse"});
-  }
-  Where where;
-  GQA_TRY(locate_tensors(ts, "gqa_paged_attn", &where));
-  gqa::PagedAttnArgs a{};
-  a.q = q->data;
-  a.out = out->data;
-  a.lse = lse ? static_cast<float*>(lse->data) : nullptr;
-  a.k_pages = k_pages->data;
-  a.v_pages = v_pages->data;
-  a.block_table = static_cast<const int32_t*>(block_table->data);
-  a.seq_lens = static_cast<const int32_t*>(seq_lens->data);
-  a.q_seq = stride_of(q, 0);
-  a.q_head = stride_of(q, 1);
-  a.kp_page = k_pages->strides[0];
-  a.kp_head = k_pages->strides[1];
-  a.kp_slot = k_pages->strides[2];
-  a.vp_page = v_pages->strides[0];
-  a.vp_head = v_pages->strides[1];
-  a.vp_slot = v_pages->strides[2];
-  a.batch = qs[0];
-  a.num_pages = ps[0];
-  a.max_pages_per_seq = bs[1];
-  a.hq = (int)qs[1];
-  a.hkv = (int)ps[1];
-  a.d = (int)qs[2];
-  a.page_size = (int)ps[2];
-  const bool bf16 = q->dtype == GQA_BF16;
-  a.cache = e4m3 ? (bf16 ? gqa::kCacheE4m3 : gqa::kCacheE4m3F16) : bf16 ? gqa::kCacheBf16 : gqa::kCacheF16;
-  a.scale = (float)((double)q_scale * k_scale / std::sqrt((double)qs[2]));
-  a.v_scale = v_scale;
-  a.softcap = softcap;
-  a.window = window;
-  a.starve = gqa::starve_producers();
-  ScopedDevice sd(where.device);
-  if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", where.device);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!workspace_) {
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    GQA_CUDA_TRY(cudaStreamIsCapturing(s, &capture), "cudaStreamIsCapturing");
-    if (capture != cudaStreamCaptureStatusNone)
-      return fail(GQA_ERR_WORKSPACE, "a captured call needs a workspace of its own (%lld bytes)", (long long)need);
-    GQA_TRY(workspace(where.device, s, (size_t)need, &workspace_, g_paged_ws));
-  }
-  GQA_CUDA_TRY(gqa::launch_paged_attn(a, workspace_, s), "paged attention launch");
-  return GQA_OK;
+  return guarded([&]() -> gqa_status {
+    int64_t qs[3], ps[4], bs[2];
+    GQA_TRY(check_strided(q, "q", {GQA_F16, GQA_BF16}, {-1, -1, -1}, false, qs));
+    GQA_TRY(check_strided(k_pages, "k_pages", {q->dtype, GQA_E4M3, GQA_U8}, {-1, -1, -1, qs[2]}, true, ps));
+    const bool e4m3 = k_pages->dtype != q->dtype;
+    GQA_TRY(e4m3 ? check_strided(v_pages, "v_pages", {GQA_E4M3, GQA_U8}, {ps[0], ps[1], ps[2], qs[2]}, true)
+                 : check_strided(v_pages, "v_pages", {q->dtype}, {ps[0], ps[1], ps[2], qs[2]}, true));
+    GQA_TRY(check_desc(seq_lens, "seq_lens", {GQA_I32}, {qs[0]}));
+    GQA_TRY(check_desc(block_table, "block_table", {GQA_I32}, {qs[0], -1}, bs));
+    GQA_TRY(check_desc(out, "out", {q->dtype}, {qs[0], qs[1], qs[2]}));
+    if (lse) GQA_TRY(check_desc(lse, "lse", {GQA_F32}, {qs[0], qs[1]}));
+    if (qs[0] < 1 || qs[0] > 65535) return fail(GQA_ERR_UNSUPPORTED, "batch %lld outside [1, 65535]", (long long)qs[0]);
+    if (qs[2] != 64 && qs[2] != 128 && qs[2] != 256)
+      return fail(GQA_ERR_UNSUPPORTED_SHAPE, "head dim %lld is not 64, 128 or 256", (long long)qs[2]);
+    if (ps[1] < 1 || qs[1] < 1 || qs[1] > 1024 || qs[1] % ps[1] != 0)
+      return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld query heads over %lld KV heads: 1 to 1024, a multiple, are taken",
+                  (long long)qs[1], (long long)ps[1]);
+    if (ps[2] != 16 && ps[2] != 32 && ps[2] != 64 && ps[2] != 128 && ps[2] != 256)
+      return fail(GQA_ERR_UNSUPPORTED_SHAPE, "page size %lld is not 16, 32, 64, 128 or 256", (long long)ps[2]);
+    if (ps[0] < 1 || ps[0] > 2147483647LL) return fail(GQA_ERR_INVALID_ARG, "num_pages %lld out of range", (long long)ps[0]);
+    if (bs[1] < 1 || bs[1] > (int64_t(1) << 30) / ps[2])
+      return fail(GQA_ERR_INVALID_ARG, "max_pages_per_seq %lld out of range", (long long)bs[1]);
+    // (a block of the kernel counts the work of its share, in tiles of 32 tokens at least, in 31 bits)
+    if (qs[0] * ps[1] * ((qs[1] / ps[1] + 7) / 8) > (int64_t(1) << 38) / (bs[1] * ps[2] / 32 + 16))
+      return fail(GQA_ERR_UNSUPPORTED, "batch %lld x %lld KV heads x %lld tokens of capacity are too many", (long long)qs[0],
+                  (long long)ps[1], (long long)(bs[1] * ps[2]));
+    if (!std::isfinite(q_scale)) return fail(GQA_ERR_INVALID_ARG, "q_scale is not finite");
+    GQA_TRY(check_scale(k_scale, "k_scale"));
+    GQA_TRY(check_scale(v_scale, "v_scale"));
+    if (window < 0) return fail(GQA_ERR_INVALID_ARG, "window %d is negative", window);
+    if (!std::isfinite(softcap) || softcap < 0.f) return fail(GQA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+    const int64_t need = gqa_paged_attn_workspace(qs[1], ps[1], qs[2]);
+    if (workspace_ && workspace_bytes < need)
+      return fail(GQA_ERR_INVALID_ARG, "workspace of %lld bytes; %lld are needed", (long long)workspace_bytes, (long long)need);
+    gqa_tensor ws = *q;  // the workspace's place is checked with the tensors'
+    ws.data = workspace_;
+    std::vector<Named> ts = {{q, "q"}, {k_pages, "k_pages"}, {v_pages, "v_pages"}, {block_table, "block_table"},
+                             {seq_lens, "seq_lens"}, {out, "out"}};
+    if (workspace_) ts.push_back({&ws, "workspace"});
+    gqa_tensor l;
+    if (lse) {
+      l = *lse;
+      l.dtype = GQA_I32;  // (4-byte alignment)
+      ts.push_back({&l, "lse"});
+    }
+    Where where;
+    GQA_TRY(locate_tensors(ts, "gqa_paged_attn", &where));
+    gqa::PagedAttnArgs a{};
+    a.q = q->data;
+    a.out = out->data;
+    a.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+    a.k_pages = k_pages->data;
+    a.v_pages = v_pages->data;
+    a.block_table = static_cast<const int32_t*>(block_table->data);
+    a.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+    a.q_seq = stride_of(q, 0);
+    a.q_head = stride_of(q, 1);
+    a.kp_page = k_pages->strides[0];
+    a.kp_head = k_pages->strides[1];
+    a.kp_slot = k_pages->strides[2];
+    a.vp_page = v_pages->strides[0];
+    a.vp_head = v_pages->strides[1];
+    a.vp_slot = v_pages->strides[2];
+    a.batch = qs[0];
+    a.num_pages = ps[0];
+    a.max_pages_per_seq = bs[1];
+    a.hq = (int)qs[1];
+    a.hkv = (int)ps[1];
+    a.d = (int)qs[2];
+    a.page_size = (int)ps[2];
+    const bool bf16 = q->dtype == GQA_BF16;
+    a.cache = e4m3 ? (bf16 ? gqa::kCacheE4m3 : gqa::kCacheE4m3F16) : bf16 ? gqa::kCacheBf16 : gqa::kCacheF16;
+    a.scale = (float)((double)q_scale * k_scale / std::sqrt((double)qs[2]));
+    a.v_scale = v_scale;
+    a.softcap = softcap;
+    a.window = window;
+    a.starve = gqa::starve_producers();
+    ScopedDevice sd(where.device);
+    if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", where.device);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!workspace_) {
+      cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+      GQA_CUDA_TRY(cudaStreamIsCapturing(s, &capture), "cudaStreamIsCapturing");
+      if (capture != cudaStreamCaptureStatusNone)
+        return fail(GQA_ERR_WORKSPACE, "a captured call needs a workspace of its own (%lld bytes)", (long long)need);
+      // As much as the largest head layout needs, so that it never moves; and allocated
+      // without disturbing a capture of another thread.
+      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+      GQA_CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode), "cudaThreadExchangeStreamCaptureMode");
+      const gqa_status st = workspace(where.device, s, gqa::paged_attn_workspace_bytes(1024, 1, 256), &workspace_, g_paged_ws);
+      cudaThreadExchangeStreamCaptureMode(&mode);
+      GQA_TRY(st);
+    }
+    GQA_CUDA_TRY(gqa::launch_paged_attn(a, workspace_, s), "paged attention launch");
+    return GQA_OK;
+  });
 }
 
 gqa_status gqa_release_workspace(void) {

@@ -512,7 +512,9 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     // No copy may land after the block has gone.
     if (lane == 0) {
       // (stages before st were last filled in the present round, the others in the one before)
-      for (int i = pair; i < pair + kPairs * issued; i += kPairs) mbar_wait(smem_u32(&sm.full[i]), i < st ? ph ^ 1 : ph, err);
+      // (an expired wait has waited long enough for the copies behind it too)
+      for (int i = pair; i < pair + kPairs * issued; i += kPairs)
+        if (!mbar_wait(smem_u32(&sm.full[i]), i < st ? ph ^ 1 : ph, err)) break;
       for (int i = seg > 2 ? seg - 2 : 0; warp == kWarps && i < seg; ++i) mbar_wait(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1, err);
     }
     return;

@@ -261,3 +261,92 @@ def test_nvfp4_chunked_prefill():
     # the same keys in other tiles: an output may round to the other neighbour
     got, ref = val(torch.cat(parts)), val(want)
     assert ((got - ref).abs() <= 2.0 ** -3 * ref.abs() + 2.0 ** -9).all()
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^31 elements: the last pages are written and read, their neighbours 2^31 elements before are not."""
+    pages, hkv, page, d = 2 ** 31 // (8 * 64 * 128) + 40, 8, 64, 128
+    cache = [torch.zeros(pages, hkv, page, d, dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2)]
+    assert cache[0].numel() > 2 ** 31
+    g = torch.Generator().manual_seed(10)
+    n = 100
+    x = torch.randn(n, 48, d, generator=g).bfloat16().to(DEV)
+    q, k, v = x[:, :32], x[:, 32:40], x[:, 40:]
+    table = torch.tensor([[pages - 1, pages - 3]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    rope = rope_table(n, d).to(DEV)
+    turned = gqa.gqa_paged_append(q, k, v, *cache, table, lens, qo_indptr=torch.tensor([0, n], dtype=torch.int32, device=DEV), rope=rope,
+                                  k_scale=0.02, v_scale=0.02)
+    last = turned[-1:].contiguous()
+    lse = torch.empty(1, 32, device=DEV)
+    out = gqa.gqa_paged_attn(last, *cache, table, lens, lse=lse, k_scale=0.02, v_scale=0.02)
+    used = [pages - 1, pages - 3]
+    small = [c[used].cpu() for c in cache]
+    R.check_attention(out, lse, last.cpu(), *small, torch.tensor([[0, 1]]), lens.cpu(), k_scale=0.02, v_scale=0.02)
+    for c in cache:
+        written = (c.view(torch.uint8).flatten(1) != 0).any(1).nonzero().flatten().tolist()
+        assert written == sorted(used)
+    # the same rows in a small cache
+    other = [torch.zeros(2, hkv, page, d, dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2)]
+    gqa.gqa_paged_append(q, k, v, *other, torch.tensor([[0, 1]], dtype=torch.int32, device=DEV), lens,
+                         qo_indptr=torch.tensor([0, n], dtype=torch.int32, device=DEV), rope=rope, k_scale=0.02, v_scale=0.02)
+    for a, b in zip(other, small):
+        assert torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8))
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """A fresh process whose first append and attention are captured ones."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, gqa_attention_kv_split_gb300 as gqa
+d = torch.device('cuda:0')
+x = torch.randn(2, 6, 64, device=d).half()
+pages = [torch.zeros(4, 1, 16, 64, dtype=torch.float16, device=d) for _ in range(2)]
+table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device=d)
+lens = torch.tensor([1, 1], dtype=torch.int32, device=d)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    q = gqa.gqa_paged_append(x[:, :4], x[:, 4:5], x[:, 5:], *pages, table, lens)
+    out = gqa.gqa_paged_attn(q, *pages, table, lens)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, x[:, 5:].expand(-1, 4, -1)), (out, x)
+assert gqa.gqa_check_device_errors(0) == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_workspace_is_allocated_while_another_stream_is_captured():
+    """The first eager call on a stream allocates its workspace without ending a capture that is going on."""
+    s = Server(B=2, seed=11)
+    lens = torch.tensor([1, 1], dtype=torch.int32, device=DEV)
+    q = s.append(s.new([1, 1]).to(DEV), lens, None)
+    out = torch.empty_like(q)
+    want = s.attend(q, lens).clone()
+    torch.cuda.synchronize()
+    gqa.gqa_release_workspace()
+    side, ready, done, bad = torch.cuda.Stream(), threading.Event(), threading.Event(), []
+
+    def work():
+        ready.wait(60)
+        try:
+            with torch.cuda.stream(side):
+                s.attend(q, lens, out=out)
+        except Exception as e:  # pragma: no cover
+            bad.append(e)
+        done.set()
+    t = threading.Thread(target=work)
+    t.start()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = s.attend(q, lens)
+        ready.set()
+        assert done.wait(60)
+    t.join()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not bad and torch.equal(got, want) and torch.equal(out, want)
