@@ -2,8 +2,6 @@
 // workspace layout, choice of the instance.
 #include <cuda.h>  // CUtensorMap and the cuTensorMapEncodeTiled prototype (resolved at run time)
 
-#include <atomic>
-#include <chrono>
 #include <cmath>
 #include <mutex>
 
@@ -49,22 +47,13 @@ cudaError_t make_map(const void* pages, const PagedAttnArgs& a, int64_t s_page, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// A 64-bit number that no earlier call, of this process or another, is likely to have
-// left in a workspace: steps of an odd number (which meet every value once) from a
-// start that differs from process to process.
-uint64_t next_nonce() {
-  static std::atomic<uint64_t> counter{(uint64_t)std::chrono::system_clock::now().time_since_epoch().count() * 0x100000001b3ull ^
-                                       (uint64_t)reinterpret_cast<uintptr_t>(&g_encode)};
-  return counter.fetch_add(0x9e3779b97f4a7c15ull, std::memory_order_relaxed);
-}
-
 int rows_of(int group) { return group > 8 ? 16 : 8; }  // query heads of a unit
 
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int hq, int hkv, int d) {
   const size_t rows = (size_t)pa::kGrid * 2 * rows_of(hq / hkv);
-  return rows * d * sizeof(float) + rows * sizeof(float2) + pa::kGrid * 2 * sizeof(uint64_t);
+  return rows * d * sizeof(float) + rows * sizeof(float2) + pa::kGrid * sizeof(pa::Record);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStream_t stream) {
@@ -81,8 +70,6 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   const size_t n = (size_t)pa::kGrid * 2 * rows;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + n * a.d);
-  p.words = reinterpret_cast<uint64_t*>(p.part_ml + n);
-  p.nonce = next_nonce();
   p.q_seq = a.q_seq;
   p.q_head = a.q_head;
   p.batch = a.batch;
@@ -96,6 +83,13 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   }
   for (p.box_shift = 0; (1 << p.box_shift) < box; ++p.box_shift) {
   }
+  // No unit is split if there are no more than blocks and their sequences cannot be long
+  // (the kernel's own rule, by the lengths themselves); then nothing is to be joined.
+  const int64_t units = a.batch * a.hkv * p.head_blocks;
+  const bool whole = units <= pa::kGrid && a.max_pages_per_seq * a.page_size <= (int64_t)pa::kWholeTiles * tile;
+  p.record = whole ? nullptr : reinterpret_cast<pa::Record*>(p.part_ml + n);
+  p.record_by_unit = units <= pa::kGrid;
+  p.records = units <= pa::kGrid ? (int)units : pa::kGrid;
   const double log2e = 1.4426950408889634;
   p.scale_log2 = (float)(a.scale * log2e);
   p.cap_in = a.softcap > 0.f ? (float)(2.0 * log2e * a.scale / a.softcap) : 0.f;

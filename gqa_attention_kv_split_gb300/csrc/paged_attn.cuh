@@ -23,10 +23,7 @@
 //    all (sequence, KV head, block of heads) units, in order, whatever the
 //    lengths -- the shares are computed on the device from seq_lens.  A unit that
 //    lies inside one block is written by it; the pieces of one that does not go
-//    to the workspace (at most two per block), and the last block to write one joins
-//    them, in the order of the tiles.  No block waits for another.  The last one is
-//    found by exchanges of a 64-bit number of the call's own, so that the workspace
-//    needs no preparation.
+//    to the workspace (at most two per block), and a second kernel joins them.
 //  * Producer warps move tiles of 64 (32) tokens with tensor-map TMA copies
 //    into a ring of 128 KB: any page size and cache order is a box of the
 //    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
@@ -89,17 +86,6 @@ struct Shape {
   static_assert(kStages >= kGroups && kStages % (kProducers / 2) == 0, "whole turns of groups and producers");
 };
 
-// A unit that lies in several blocks' shares.
-struct Piece {
-  int64_t tile0;    // its first tile in the work of the call
-  int b, unit;      // sequence, unit within it
-  int tiles;
-  int first, last;  // the blocks that hold it
-  int first_slot;   // which of the first block's two pieces it is (it is the first one of the others)
-  int join;         // this block was the last to write a piece of it
-  __device__ __forceinline__ int word(int block) const { return 2 * block + (block == first ? first_slot : 0); }
-};
-
 // Block i of n has the tiles [total * i / n, total * (i + 1) / n).  (32-bit divisions where they do.)
 __device__ __forceinline__ int64_t share_begin(int i, int64_t total, int n) {
   const int64_t x = total * i;
@@ -129,7 +115,6 @@ struct Smem {
   int64_t end;    // of this block's share
   int64_t rem;    // the share's first tile within its first sequence,
   int b0;         // and that sequence
-  Piece piece[2];  // the units of this block's two pieces
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t r[4], uint32_t addr) {
@@ -266,45 +251,6 @@ __device__ __forceinline__ float2 load_l2(const float2* p) {
   return v;
 }
 
-// Joins the pieces of a unit, in the order of its tiles: thread i of n takes the pairs of
-// elements i, i + n, ...
-template <int D, int NT, bool kQBf16>
-__device__ __forceinline__ void join_pieces(const Params& p, const Piece& u, int i, int n) {
-  constexpr int kRows = 8 * NT, kBatch = 8;
-  const int kvh = u.unit / p.head_blocks;
-  const int h0 = kvh * p.group + (u.unit - kvh * p.head_blocks) * kRows;
-  const int pairs = min(kRows, (kvh + 1) * p.group - h0) * (D / 2);
-  const int first = u.first, last = u.last, first_slot = u.first_slot;
-  for (int j = i; j < pairs; j += n) {
-    const int r = j / (D / 2), d = j % (D / 2) * 2;
-    // (m, l, o) so far; the smaller maximum's side is scaled down.  kBatch pieces' loads are
-    // in flight at a time (the last piece's again behind the end).
-    float m = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
-    for (int b = first; b <= last; b += kBatch) {
-      float2 ml[kBatch], v[kBatch];
-#pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        const int c = min(b + e, last);
-        const int64_t at = (int64_t)(2 * c + (c == first ? first_slot : 0)) * kRows + r;
-        ml[e] = load_l2(p.part_ml + at);
-        v[e] = load_l2(reinterpret_cast<const float2*>(p.part_o + at * D + d));
-      }
-#pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        const float me = b + e <= last ? ml[e].x : -INFINITY;
-        const float mn = fmaxf(m, me);
-        const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
-        const float g = me == -INFINITY ? 0.f : fast_exp2(me - mn);
-        m = mn;
-        l = fmaf(l, f, ml[e].y * g);
-        x = fmaf(x, f, v[e].x * g);
-        y = fmaf(y, f, v[e].y * g);
-      }
-    }
-    store_out<D, kQBf16>(p, (int64_t)u.b * p.hq + h0 + r, d, x, y, m, l);
-  }
-}
-
 template <int kCache, int D, int NT>
 __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -329,6 +275,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   const int units = p.hkv * p.head_blocks;
 
   if (threadIdx.x == 0) {
+    if (p.record && !p.record_by_unit) p.record[blockIdx.x].last = -1;
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(smem_u32(&sm.full[i]), 2);
       mbar_init(smem_u32(&sm.empty[i]), S::kGroupWarps);
@@ -348,14 +295,13 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   // ---- this block's share: of the work [T * block / n, T * (block + 1) / n), or one whole
   // unit if there are no more units than blocks and none has more than kWholeTiles tiles:
   // to read them takes less time than to join the pieces of a split unit (2 sequences
-  // of up to 200 tokens, 8 KV heads: 8.9 us split, 6.6 us whole).
+  // of up to 200 tokens, 8 KV heads: 8.8 us split, 5.6 us whole; 16 of 512: 14.7 and 10.1).
   // Each thread sums the tiles of a contiguous range of sequences; a scan over the
   // threads gives the ranges' starts, and the range that holds the share's first tile
   // is walked by its thread.
   const int64_t per = (p.batch + kThreads - 1) / kThreads;
   const int64_t s0 = threadIdx.x * per < p.batch ? threadIdx.x * per : p.batch;
   const int64_t s1 = s0 + per < p.batch ? s0 + per : p.batch;
-  constexpr int kWholeTiles = 8;
   constexpr int kCountAt = 46;  // a sum holds tiles below, and sequences that have any above
   int64_t mine = 0;
   int most = 0;
@@ -369,6 +315,8 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
         for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
         if (p.lse) p.lse[(int64_t)b * p.hq + h] = -INFINITY;
       }
+      if (p.record && p.record_by_unit)
+        for (int u = 0; u < units; ++u) p.record[b * units + u].last = -1;
     }
   }
   int64_t incl = mine;
@@ -552,7 +500,6 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   int skip = grp;        // tiles to this group's next one
   int seg = 0;
   bool dead = false;  // a wait has expired: nothing more is waited for or computed
-  int pieces = 0;     // bit i: this block has written its piece i
   do {
     const int kvh = walk.unit / p.head_blocks;
     const int h0 = kvh * p.group + (walk.unit - kvh * p.head_blocks) * kRows;
@@ -857,68 +804,63 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
         if (d == 0) p.part_ml[piece + r] = make_float2(mm - kShift, ll);
       }
     }
-    if (!whole) {
-      pieces |= 1 << slot;
-      if (threadIdx.x == 0) {
-        Piece& u = sm.piece[slot];
-        u.tile0 = sm.end - walk.left - walk.t_beg;
-        u.b = walk.b;
-        u.unit = walk.unit;
-        u.tiles = walk.span.tiles;
-      }
+    if (p.record && threadIdx.x == 0 && walk.t_beg == 0 && (!whole || p.record_by_unit)) {
+      // The unit begins here; it ends in the block that has its last tile.
+      const int64_t last_tile = sm.end - walk.left + walk.span.tiles - 1;
+      Record r{walk.b, walk.unit, (int)blockIdx.x, -1, slot};
+      if (!whole) r.last = share_of(last_tile, sm.total, sm.n_blocks);
+      p.record[p.record_by_unit ? walk.b * units + walk.unit : (int)blockIdx.x] = r;
     }
   } while (walk.next(p));
-  if (!pieces) return;
+}
 
-  // ---- units that lie in several blocks' shares: the last to end joins the pieces ----
-  // Both pieces of this block at once, at its end: a unit's last block writes its piece
-  // at the start of its share, long before the others have theirs.  Each piece has a
-  // word in the workspace.  Two pieces meet in one exchange: the first block leaves the
-  // call's nonce in the word and goes, the second one finds it.  Of more pieces, each
-  // block sets its own word and looks whether all are set, a sequentially consistent
-  // fence between: of blocks that end together at least one sees them all (should two,
-  // they write the same values).  Nobody waits, and who joins clears the words: a replay
-  // of a captured call has the same nonce.
-  named_bar_sync(1, kWarps * 32);
-  if (warp == 0) {
-    if (lane == 0) __threadfence();  // (the barrier ordered every thread's part of the pieces before it)
-    __syncwarp();
-    unsigned long long* const words = reinterpret_cast<unsigned long long*>(p.words);
-    bool many = false;  // lane i: piece i is one of more than two, and its word is set
-    if (lane < 2) {
-      Piece& u = sm.piece[lane];
-      u.join = 0;
-      if ((pieces >> lane) & 1) {
-        u.first = share_of(u.tile0, sm.total, sm.n_blocks);
-        u.last = share_of(u.tile0 + u.tiles - 1, sm.total, sm.n_blocks);
-        u.first_slot = share_begin(u.first, sm.total, sm.n_blocks) >= u.tile0 - kUnitWork ? 0 : 1;
-        many = u.last - u.first > 1;
-        if (many) {
-          *reinterpret_cast<volatile unsigned long long*>(words + u.word(blockIdx.x)) = p.nonce;
-        } else if (atomicExch(words + u.word(u.last), p.nonce) == p.nonce) {
-          words[u.word(u.last)] = 0;
-          u.join = 1;
-        }
-      }
+// Joins the pieces of the units that lie in several blocks' shares, in the order of their
+// tiles: one block per record and row, in which four groups of threads take every fourth
+// piece each, eight loads of a thread in flight.  (A kernel of its own: the main kernel's
+// block that ends last would take longer than this launch to read them -- 6 units of 25
+// pieces, 16 heads of 256 elements: 60 us against 26; one unit: 21 against 11.)
+template <int D, int NT, bool kQBf16>
+__global__ void __launch_bounds__(2 * D) paged_attn_join_kernel(const __grid_constant__ Params p) {
+  constexpr int kGroups = 4, kBatch = 8;
+  __shared__ float part[kGroups][D / 2][4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Record u = p.record[blockIdx.x];
+  if (u.last < 0) return;
+  const int kvh = u.unit / p.head_blocks, r = blockIdx.y, first = u.first;
+  const int head = kvh * p.group + (u.unit - kvh * p.head_blocks) * 8 * NT + r;
+  if (head >= (kvh + 1) * p.group) return;
+  const int grp = threadIdx.x / (D / 2), i = threadIdx.x % (D / 2);
+  float m = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
+  auto add = [&](float m2, float l2, float x2, float y2) {
+    const float mn = fmaxf(m, m2);
+    const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn), g = m2 == -INFINITY ? 0.f : fast_exp2(m2 - mn);
+    m = mn;
+    l = fmaf(l, f, l2 * g);
+    x = fmaf(x, f, x2 * g);
+    y = fmaf(y, f, y2 * g);
+  };
+  for (int c0 = first + grp; c0 <= u.last; c0 += kGroups * kBatch) {
+    float2 ml[kBatch], v[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int c = min(c0 + e * kGroups, u.last);
+      const int64_t at = (int64_t)(2 * c + (c == first ? u.first_slot : 0)) * (8 * NT) + r;
+      ml[e] = load_l2(p.part_ml + at);
+      v[e] = load_l2(reinterpret_cast<const float2*>(p.part_o + at * D + 2 * i));
     }
-    const unsigned look = __ballot_sync(0xffffffffu, many);
-    __threadfence();
-    for (int i = 0; i < 2; ++i) {
-      if (!((look >> i) & 1)) continue;
-      const Piece& u = sm.piece[i];
-      bool all = true;
-      for (int b = u.first + lane; b <= u.last; b += 32)
-        all &= *reinterpret_cast<volatile unsigned long long*>(words + u.word(b)) == p.nonce;
-      if (__all_sync(0xffffffffu, all)) {
-        __threadfence();
-        for (int b = u.first + lane; b <= u.last; b += 32) words[u.word(b)] = 0;
-        if (lane == 0) sm.piece[i].join = 1;
-      }
-    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (c0 + e * kGroups <= u.last) add(ml[e].x, ml[e].y, v[e].x, v[e].y);
   }
-  named_bar_sync(1, kWarps * 32);
-  for (int i = 0; i < 2; ++i)
-    if (sm.piece[i].join) join_pieces<D, NT, kQBf16>(p, sm.piece[i], threadIdx.x, kWarps * 32);
+  *reinterpret_cast<float4*>(part[grp][i]) = make_float4(m, l, x, y);
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int g = 1; g < kGroups; ++g) {
+    const float4 o = *reinterpret_cast<const float4*>(part[g][i]);
+    add(o.x, o.y, o.z, o.w);
+  }
+  store_out<D, kQBf16>(p, (int64_t)u.b * p.hq + head, 2 * i, x, y, m, l);
 }
 
 template <int kCache, int D, int NT>
@@ -939,7 +881,17 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUt
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
   paged_attn_kernel<kCache, D, NT><<<kGrid, S::kThreads, smem, stream>>>(p, k_map, v_map);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || !p.record) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.records, p.group < 8 * NT ? p.group : 8 * NT);
+  cfg.blockDim = dim3(2 * D);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, NT, kCache == kCacheBf16 || kCache == kCacheE4m3>, p);
 }
 
 template <int kCache>

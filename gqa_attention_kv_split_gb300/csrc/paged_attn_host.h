@@ -12,9 +12,17 @@ namespace gqa {
 namespace pa {
 
 constexpr int kGrid = 152;  // blocks: one per SM
+constexpr int kWholeTiles = 8;  // sequences of up to so many tiles are not split if there is a block for each unit
 
 // Tokens per ring stage, from the bytes of a token's row: 16 to 32 KB of K and V a stage.
 constexpr int tile_of(int row_bytes) { return row_bytes > 256 ? 32 : 64; }
+
+// For the joining kernel: a unit and the blocks that have a piece of it.
+struct Record {
+  int b, unit;      // sequence, unit within it
+  int first, last;  // last < 0: the unit lies inside one block (or there is no unit)
+  int first_slot;   // which of the first block's two pieces it is (it is the first one of the others)
+};
 
 struct Params {
   const void* q;
@@ -24,8 +32,9 @@ struct Params {
   const int32_t* seq_lens;
   float* part_o;     // [kGrid][2][kRows][D]
   float2* part_ml;   // [kGrid][2][kRows]
-  uint64_t* words;   // [kGrid][2]: tell whether a piece has been written
-  uint64_t nonce;    // of this call
+  Record* record;    // [records], or null: no unit can be split (there is no second kernel)
+  int records;       // one for each unit, or for each block the unit that begins there and
+  int record_by_unit;  // ends elsewhere
   int64_t q_seq, q_head, batch, num_pages, max_pages;
   int hq, hkv, group, head_blocks;
   int page_shift, box_shift;  // log2 of a page's tokens, and of those of one copy

@@ -449,7 +449,7 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
  * the visible tokens may hold anything, NaN too.  A page outside [0, num_pages)
  * is not read: page 0 is used instead and bit 1 of the error word is set.  The
  * split is chosen on the device from the lengths, so a captured call stays
- * balanced when they change.  One kernel; host tensors are refused
+ * balanced when they change.  One kernel, or two; host tensors are refused
  * (GQA_ERR_UNSUPPORTED).
  */
 gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, const gqa_tensor* v_pages,
