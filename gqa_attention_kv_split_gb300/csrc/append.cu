@@ -9,8 +9,8 @@
 // c = rope[pos, i], s = rope[pos, rot/2 + i] -- pairs (i, i + rot/2), or
 // (2i, 2i + 1) interleaved.  Products and sums are formed in f32, each rounded
 // once (no contraction), and the result is rounded once to its stored type.
-// NVFP4: sf = E4M3(amax / 6) of a 16-element block, codes = E2M1(x / sf), true
-// f32 divisions, so a plain f32 evaluation gives the same bits.
+// NVFP4: sf = E4M3(amax / 6) of a 16-element block, codes = E2M1(x / sf), what f32
+// divisions give, so a plain f32 evaluation gives the same bits.
 //
 // What bounds it: HBM for prompts (each input read once, each output written
 // once, 3 flops per rotated element), latency for single tokens -- a chain of
@@ -111,19 +111,21 @@ __device__ __forceinline__ float amax8(const float f[8]) {
   for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
   return m;
 }
-// x / s by one multiplication with r = 1 / s and one correction step (Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990): the f32 quotient but for values
-// within 2^-47 of a midpoint between two f32 numbers.  The E2M1 code that it is rounded to is that of the
-// true quotient's f32 rounding: for a border t between two codes, t * s is an f32 number (of 7 significant
-// bits at most), so that x is t * s, and the step gives t, or at least one f32 spacing away from it, and the
-// quotient more than half a spacing away from t.
+// x / s by one multiplication with r, 1 / s to a few f32 spacings, and one correction step
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990): within 2^-44 of the quotient before its rounding to f32.  Rounded to E2M1 (s a
+// scale) or to E4M3 (s = 6) it gives what the f32 division gives: for a border t between
+// two codes, t * s is an f32 number (of 7 significant bits at most), so that x either is
+// t * s, and the step gives t, or is at least one f32 spacing away from it, and the
+// quotient more than half a spacing (by 2^-31 of it) away from t.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = __fmul_rn(x, r);
   return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
 }
 // E4M3 scale byte of a block's largest magnitude, and the scale's value.
 __device__ __forceinline__ uint32_t block_scale(float amax, float* value) {
-  const uint32_t byte = f32x2_to_e4m3x2(__fdiv_rn(amax, 6.f), 0.f);
+  const float x = amax > 4096.f ? 4096.f : amax;  // (saturates all the same, and is no infinity; NaN stays)
+  const uint32_t byte = f32x2_to_e4m3x2(quotient(x, 6.f, 1.f / 6.f), 0.f);
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)byte));
   *value = __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
@@ -132,7 +134,8 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float* value) {
 // Eight elements -> 4 bytes of codes; all codes 0 where the scale is 0 or NaN.
 __device__ __forceinline__ uint32_t codes8(const float f[8], float scale) {
   if (!(scale > 0.f)) return 0u;
-  const float inv = __fdiv_rn(1.f, scale);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
   uint32_t r = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)

@@ -396,7 +396,7 @@ gqa_status gqa_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gq
  *   sf    = E4M3_rne_sat(amax / 6) of each 16 elements of a k or v head,
  *   codes = E2M1_rne_sat(x / sf), all 0 where sf is 0 or NaN,
  *   q_out = E4M3_rne_sat(q * (1 / q_scale)), the reciprocal in f32.
- * The divisions are true f32 divisions.  A block that holds a NaN gets a NaN
+ * The codes are those of f32 divisions.  A block that holds a NaN gets a NaN
  * scale; an infinity gets the largest scale and code.  q_scale is then the
  * attention's q_scale.
  *

@@ -280,3 +280,56 @@ def test_nvfp4_append_then_context_attention_reads_it():
     assert torch.equal(R.e2m1_decode(mine[0]), R.e2m1_decode(x.k_fp4)) and torch.equal(R.e2m1_decode(mine[2]), R.e2m1_decode(x.v_fp4))
     run = lambda *p: gqa.nvfp4_paged_ctx_attn(q8, *p, table, a["qo_indptr"], a["kv_lens"], q_scale=0.01, out_scale=2.0 ** -4)
     assert torch.equal(run(kf, ks, vf, vs), run(*(t.to(DEV) for t in (x.k_fp4, x.k_sf, x.v_fp4, x.v_sf))))
+
+
+def _spread(values):
+    """Each f32 value, its two neighbours, and theirs."""
+    v = torch.tensor(values, dtype=torch.float32)
+    bits = v.view(torch.int32)
+    return torch.stack([(bits + i).view(torch.float32) for i in (-2, -1, 0, 1, 2)], -1)
+
+
+def _quantise_through_keys(rows):
+    """Codes' values and scales that the GPU gives rows [T, 64] of f32 (T <= 64 k): keys of ones turned by them."""
+    T = rows.shape[0]
+    rope = torch.cat([rows, torch.zeros(T, 64)], 1).to(DEV)
+    k = torch.ones(T, 8, 128, dtype=torch.bfloat16, device=DEV)
+    pages = (T + 63) // 64
+    z = lambda w: torch.zeros(pages, 8, 64, w, dtype=torch.uint8, device=DEV)
+    kf, ks, vf, vs = z(64), z(8), z(64), z(8)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    gqa.nvfp4_paged_append(None, k, k, kf, ks, vf, vs, torch.arange(pages, dtype=torch.int32, device=DEV)[None], i32(0, T), i32(T), rope=rope)
+    val = R.e2m1_decode(kf.cpu()).permute(0, 2, 1, 3).flatten(0, 1)[:T, 0, :64]
+    sf = ks.cpu().view(torch.float8_e4m3fn).float().permute(0, 2, 1, 3).flatten(0, 1)[:T, 0, :4]
+    return val, sf
+
+
+def test_nvfp4_codes_at_every_border_of_every_scale():
+    """x / sf next to each border between two codes (and on it), for all 126 scales: what f32 division and rounding give."""
+    scales = torch.arange(1, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    rows = []
+    for s in scales.tolist():
+        near = torch.cat([_spread([t * s for t in (.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0)]).flatten(), torch.tensor([s / 3, s * 5.9, s * 1e-9])])
+        row = torch.zeros(64)
+        row[0::16] = 6 * s  # gives every block the scale s
+        body = torch.tensor([i for i in range(64) if i % 16])
+        row[body[:len(near)]] = near * torch.where(torch.arange(len(near)) % 2 == 0, 1.0, -1.0)
+        rows.append(row)
+    rows = torch.stack(rows)
+    val, sf = _quantise_through_keys(rows)
+    want, want_sf = R.nvfp4_quantise(rows)
+    assert torch.equal(sf, want_sf) and torch.equal(sf, scales[:, None].expand(-1, 4))
+    assert torch.equal(val, want)
+
+
+def test_nvfp4_scales_at_every_border():
+    """amax / 6 next to each border between two scales: what f32 division and rounding give."""
+    e = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    near = _spread([6 * (a + b) / 2 for a, b in zip(e[:-1].tolist(), e[1:].tolist())] + [448 * 6.0, 464 * 6.0, 3e38]).flatten()
+    near = near[torch.isfinite(near)]
+    near = torch.cat([near, torch.full((-len(near) % 4,), 1.0)]).view(-1, 4)
+    rows = torch.zeros(len(near), 64)
+    rows[:, 5::16] = near
+    val, sf = _quantise_through_keys(rows)
+    want, want_sf = R.nvfp4_quantise(rows)
+    assert torch.equal(sf, want_sf) and torch.equal(val, want)
