@@ -142,6 +142,7 @@ WorkspaceMap g_ws;
 // Of gqa_paged_attn_t's calls without a workspace (a map of their own: growing one
 // never moves the other, which a captured call may have been given).
 WorkspaceMap g_paged_ws;
+std::mutex g_paged_launch_mu;
 
 gqa_status workspace(int dev, cudaStream_t stream, size_t bytes, void** out, WorkspaceMap& map = g_ws) {
   *out = nullptr;
@@ -825,10 +826,10 @@ gqa_status append_common(const gqa_tensor* q, const gqa_tensor* k, const gqa_ten
     GQA_TRY(check_strided(q, "q", {k->dtype}, {ks[0], hq, ks[2]}, false, qs));
     if (qs[1] < 1 || qs[1] > 1024) return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld query heads: 1 to 1024 are taken", (long long)qs[1]);
     GQA_TRY(check_strided(q_out, "q_out", out_dtypes, {ks[0], qs[1], ks[2]}, true));
-    if (q_out->data == q->data && q_out->dtype == q->dtype)
+    if (q_out->data && q_out->data == q->data)
       for (int d = 0; d < 2; ++d)
-        if (stride_of(q, d) != stride_of(q_out, d))
-          return fail(GQA_ERR_INVALID_ARG, "q_out may be q itself, with q's strides");
+        if (q_out->dtype != q->dtype || stride_of(q, d) != stride_of(q_out, d))
+          return fail(GQA_ERR_INVALID_ARG, "q_out may be q itself, with q's type and strides");
     ts->push_back({q, "q"});
     ts->push_back({q_out, "q_out"});
   }
@@ -1066,9 +1067,14 @@ gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, cons
     a.softcap = softcap;
     a.window = window;
     a.starve = gqa::starve_producers();
+    if (!std::isfinite(a.scale) || (softcap > 0.f && !std::isfinite((float)(4.0 * a.scale / softcap))))
+      return fail(GQA_ERR_INVALID_ARG, "q_scale * k_scale (over softcap) is out of range");
     ScopedDevice sd(where.device);
     if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", where.device);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // A call's two kernels follow each other on the stream: another thread's call on the
+    // same stream, and so with the same workspace, must not come between them.
+    std::lock_guard<std::mutex> lk(g_paged_launch_mu);
     if (!workspace_) {
       cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
       GQA_CUDA_TRY(cudaStreamIsCapturing(s, &capture), "cudaStreamIsCapturing");

@@ -15,21 +15,27 @@
 // with 16 keys (then 16 output elements) on the M side and 8 heads on the N
 // side.  The cache is the A operand straight from shared memory, a group of up
 // to 8 heads costs the same as one, and the accumulators of the output are D / 4
-// registers for each 8 heads.  The warp-level mma is enough: at HBM speed
-// it is busy for a few per cent (a tcgen05 tile has 128 rows for the 4 to 16
-// that there are, and its P would have to travel through TMEM).
+// registers for each 8 heads.  The warp-level mma is enough: at HBM speed the
+// tensor pipe is busy for 14 % (bf16) or 17 % (E4M3) of the cycles (a tcgen05
+// tile has 128 rows for the 4 to 16 that there are, and its P would have to
+// travel through TMEM).
 //
-//  * Grid: one block per SM, each with an equal share of all 16-byte-row tiles of
-//    all (sequence, KV head, block of heads) units, in order, whatever the
-//    lengths -- the shares are computed on the device from seq_lens.  A unit that
+//  * Grid: one block per SM, each with an equal share of the work of all
+//    (sequence, KV head, block of heads) units, in order, whatever the lengths --
+//    the shares are computed on the device from seq_lens.  A unit that
 //    lies inside one block is written by it; the pieces of one that does not go
 //    to the workspace (at most two per block), and a second kernel joins them.
 //  * Producer warps move tiles of 64 (32) tokens with tensor-map TMA copies
 //    into a ring of 128 KB: any page size and cache order is a box of the
 //    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
-//  * Eight consumer warps (four at head dim 256), each with its own 32 keys of a tile and its own
-//    (m, l, o); groups of warps take tiles in turn, so that one tile's softmax
-//    overlaps another one's products.  They meet at the end of a unit only.
+//  * Eight consumer warps (four at head dim 256), each with its own 32 (16) keys of
+//    a tile and its own (m, l, o); groups of warps take tiles in turn, so that one
+//    tile's softmax overlaps another one's products.  They meet at the end of a
+//    unit only.
+//
+// Measured on GB300 (time in a graph): 64 sequences of up to 8192 tokens, 32/8 heads,
+// bf16: 160 us, 6.72 TB/s; 19 of 8192 (a unit per block): 91 us, 6.98 TB/s; 48 of up to
+// 16001, 64/8 heads, E4M3: 137 us, 5.77 TB/s; 8 of 131072, f16: 602 us, 7.14 TB/s.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -50,26 +56,26 @@ __device__ uint32_t g_paged_attn_err;  // of this translation unit's kernels
 
 }  // namespace
 
-
 template <int kCache, int D, int NT>
 struct Shape {
   static constexpr int kEsz = kCache >= kCacheE4m3 ? 1 : 2;
   static constexpr int kRow = D * kEsz;                     // bytes of a token's row
   static constexpr int kChunk = kRow < 128 ? kRow : 128;    // bytes of a swizzled row in shared memory
-  static constexpr int kChunks = kRow / kChunk;
   static constexpr int kTile = tile_of(kRow);                // tokens per stage
   // Consumer warps: eight, or four where the accumulators need more than the 168
-  // registers a thread that nine warps leave.
+  // registers a thread that twelve warps leave.
   static constexpr int kWarps = D > 128 ? 4 : 8;
   // Four producer warps: for K and V, and for the even and the odd tiles.  (An issued
   // copy takes its warp about 130 cycles; with pages of 16 tokens a tile of E4M3 has
-  // eight.  They cost no registers: five to twelve warps round up alike.)
+  // eight: 197 us with one producer, 177 with two, 162 with four on 48 sequences of up to
+  // 16001 tokens.  They cost no registers: nine warps leave as many a thread as twelve.)
   static constexpr int kProducers = 4;
   static constexpr int kThreads = (kWarps + kProducers) * 32;
   // 16-key blocks that a warp takes of a tile: two give it two independent sums of
-  // products and one reduction for 32 keys (1.28x over one block on 48 sequences of up
-  // to 16001 tokens in E4M3 pages of 64); with 16 heads and long rows the registers that the second one
-  // needs would spill (64 x 8192 tokens in bf16, 16 heads a KV head: 234 us with two, 210 with one).
+  // products and one reduction for 32 keys (1.28x over one block on 48 sequences of up to
+  // 16001 tokens in E4M3 pages of 64); with 16 heads and long rows the registers that the
+  // second one needs would spill (64 x 8192 tokens in bf16, 16 heads a KV head: 234 us
+  // with two, 210 with one).
   static constexpr int kBlocks = NT == 2 && D > 64 ? 1 : 2;
   static constexpr int kGroupWarps = kTile / (16 * kBlocks);  // warps that share a tile
   static constexpr int kGroups = kWarps / kGroupWarps;      // tiles in work at a time
@@ -86,7 +92,7 @@ struct Shape {
   static_assert(kStages >= kGroups && kStages % (kProducers / 2) == 0, "whole turns of groups and producers");
 };
 
-// Block i of n has the tiles [total * i / n, total * (i + 1) / n).  (32-bit divisions where they do.)
+// Block i of n has the work [total * i / n, total * (i + 1) / n).  (32-bit divisions where they do.)
 __device__ __forceinline__ int64_t share_begin(int i, int64_t total, int n) {
   const int64_t x = total * i;
   return x >> 32 ? x / n : (int64_t)((uint32_t)x / (uint32_t)n);
@@ -224,7 +230,8 @@ struct Walk {
     if (++unit == p.hkv * p.head_blocks) {
       unit = 0;
       do {
-        span = Span<kTile>(p, ++b);
+        if (++b >= p.batch) return false;
+        span = Span<kTile>(p, b);
       } while (span.tiles == 0);
     }
     t_end = by_unit ? span.tiles : min(span.tiles, left);
@@ -253,7 +260,8 @@ __device__ __forceinline__ float2 load_l2(const float2* p) {
 
 template <int kCache, int D, int NT>
 __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
-    paged_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    paged_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map,
+                      const __grid_constant__ CUtensorMap v_map) {
   uint32_t* const err = &g_paged_attn_err;
   using S = Shape<kCache, D, NT>;
   constexpr bool kBf16 = kCache == kCacheBf16;
@@ -407,9 +415,11 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       ++seg;
       // Page numbers, 32 copies' worth at a time and one such group ahead (lane l has those of copy l).
       const int32_t* row = p.block_table + (int64_t)walk.b * p.max_pages;
-      int c = ((walk.span.tile0 + walk.t_beg + skip) << (kTileShift - box_shift)) + lane;  // this lane's copy, counted from the sequence's first token
-      const int c_end = ((walk.span.len - 1) >> box_shift) + 1;                     // copies behind the last token are not made
-      const int c_first = walk.span.first >> box_shift;                             // nor those before the window
+      // This lane's copy, counted from the sequence's first token; copies behind the last
+      // token are not made, nor those before the window.
+      int c = ((walk.span.tile0 + walk.t_beg + skip) << (kTileShift - box_shift)) + lane;
+      const int c_end = ((walk.span.len - 1) >> box_shift) + 1;
+      const int c_first = walk.span.first >> box_shift;
       auto page_of = [&](int copy) {
         if (copy < c_first || copy >= c_end) return 0;
         int g = row[copy >> (page_shift - box_shift)];
@@ -459,8 +469,8 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     } while (ok && walk.next(p));
     // No copy may land after the block has gone.
     if (lane == 0) {
-      // (stages before st were last filled in the present round, the others in the one before)
-      // (an expired wait has waited long enough for the copies behind it too)
+      // (stages before st were last filled in the present round, the others in the one
+      // before; an expired wait has waited long enough for the copies behind it too)
       for (int i = pair; i < pair + kPairs * issued; i += kPairs)
         if (!mbar_wait(smem_u32(&sm.full[i]), i < st ? ph ^ 1 : ph, err)) break;
       for (int i = seg > 2 ? seg - 2 : 0; warp == kWarps && i < seg; ++i) mbar_wait(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1, err);

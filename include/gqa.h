@@ -464,7 +464,7 @@ int64_t gqa_paged_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t d);
 /*
  * gqa_check_device_errors -- synchronise `device` and return (then clear)
  * the kernels' device error word in *word: bit 0 = a bounded wait expired,
- * bit 1 = an out-of-range page index was skipped, bit 2 = qo_indptr was not
+ * bit 1 = an out-of-range page index (or an appended position) was skipped, bit 2 = qo_indptr was not
  * non-decreasing from 0 to total_q, bit 3 = the dequantisation export's
  * self-check failed.  Returns GQA_ERR_TIMEOUT when bit 0 is set,
  * GQA_ERR_INVALID_ARG when another bit is set, GQA_OK when the word is 0.

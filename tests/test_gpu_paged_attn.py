@@ -219,3 +219,11 @@ def test_expired_waits_are_reported():
         gqa.gqa_debug_starve_producers(False)
     assert torch.equal(good, gqa.gqa_paged_attn(*x))
     assert gqa.gqa_check_device_errors(0) == 0
+
+
+def test_scales_out_of_range_are_refused():
+    x = make([20], seed=17, poison=False)
+    with pytest.raises(gqa.GqaError, match="out of range"):
+        gqa.gqa_paged_attn(*x, q_scale=3e38, k_scale=1e30)
+    with pytest.raises(gqa.GqaError, match="out of range"):
+        gqa.gqa_paged_attn(*x, q_scale=1e20, softcap=1e-30)

@@ -232,6 +232,36 @@ def test_threads_and_streams():
     assert not bad
 
 
+def test_threads_on_one_stream():
+    """Calls of several threads on one stream share its workspace: no call's kernels come between another's two."""
+    s = Server(B=3, hq=16, hkv=1, cap=4096, page=64, seed=12)
+    batches = []
+    for n in ([4000, 3, 900], [10, 3500, 2000], [1, 1, 4096], [2222, 2222, 2222]):
+        lens = torch.tensor(n, dtype=torch.int32, device=DEV)
+        q = torch.randn(3, 16, 128, device=DEV).bfloat16()
+        batches.append((q, lens))
+    full = torch.tensor([4096] * 3, dtype=torch.int32, device=DEV)
+    s.append(s.new([4096] * 3).to(DEV), full, torch.tensor([0, 4096, 8192, 12288], dtype=torch.int32, device=DEV))
+    want = [s.attend(*b) for b in batches]
+    torch.cuda.synchronize()
+    bad, stream, start = [], torch.cuda.Stream(), threading.Barrier(4)
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            out = torch.empty_like(want[i])
+            start.wait(60)
+            outs = [s.attend(*batches[i], out=out).clone() for _ in range(100)]
+        stream.synchronize()
+        if not all(torch.equal(o, want[i]) for o in outs):
+            bad.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_nvfp4_chunked_prefill():
     """A prompt appended in two chunks and attended to chunk by chunk is the prompt appended and attended to at once."""
     g = torch.Generator().manual_seed(8)

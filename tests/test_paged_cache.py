@@ -58,8 +58,14 @@ def test_append_refusals(change, match):
 def test_append_in_place_needs_the_same_strides():
     a = append_args()
     wide = fake((3, 8, 64))
-    with pytest.raises(gqa.GqaError, match="q_out may be q itself, with q's strides"):
+    with pytest.raises(gqa.GqaError, match="q_out may be q itself, with q's type and strides"):
         gqa.gqa_paged_append(**{**a, "q": wide[:, :4], "q_out": wide.view(-1)[:3 * 4 * 64].view(3, 4, 64)})
+
+
+def test_nvfp4_append_in_place_is_refused():
+    a = nvfp4_args()
+    with pytest.raises(gqa.GqaError, match="q_out may be q itself, with q's type and strides"):
+        gqa.nvfp4_paged_append(**{**a, "q_out": a["q"].view(torch.uint8)[..., :128]})
 
 
 def test_append_of_nothing_is_accepted():
@@ -113,6 +119,7 @@ def attn_args(B=2, hq=4, hkv=2, d=64, page=16, dtype=torch.float16, cache=None, 
     (dict(window=-1), "window -1 is negative"),
     (dict(softcap=-1.0), "softcap must be finite and >= 0"),
     (dict(q_scale=math.inf), "q_scale is not finite"),
+    (dict(k_scale=math.inf), "k_scale must be finite and > 0"),
     (dict(k_scale=0.0), "k_scale must be finite and > 0"),
     (dict(workspace=torch.zeros(64, dtype=torch.uint8)), "workspace of 64 bytes"),
     (dict(), "gqa_paged_attn takes device tensors only"),
