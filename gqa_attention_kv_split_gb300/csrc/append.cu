@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   constexpr int kLanes = D / 16;  // threads per row, each with two 16-byte vectors
   __shared__ TokenPlace place[kMaxTok];
   __shared__ float4 angles[kMaxTok][D / 4];
+  asm volatile("griddepcontrol.launch_dependents;");  // (the attention of this step may start; it waits for this grid's end)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = (int64_t)blockIdx.x * a.tok_per_block;
   const int n_tok = (int)(a.total < t0 + a.tok_per_block ? a.total - t0 : a.tok_per_block);

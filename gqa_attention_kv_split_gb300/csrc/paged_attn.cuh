@@ -283,7 +283,6 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   const int units = p.hkv * p.head_blocks;
 
   if (threadIdx.x == 0) {
-    if (p.record && !p.record_by_unit) p.record[blockIdx.x].last = -1;
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(smem_u32(&sm.full[i]), 2);
       mbar_init(smem_u32(&sm.empty[i]), S::kGroupWarps);
@@ -299,6 +298,10 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   for (int i = threadIdx.x; i < (int)sizeof(sm.q) / 16; i += kThreads)
     reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  // Launched as a programmatic dependent: what went before on the stream (the append of
+  // this step) has ended and is visible from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0 && p.record && !p.record_by_unit) p.record[blockIdx.x].last = -1;
 
   // ---- this block's share: of the work [T * block / n, T * (block + 1) / n), or one whole
   // unit if there are no more units than blocks and none has more than kWholeTiles tiles:
@@ -890,17 +893,20 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUt
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
-  paged_attn_kernel<kCache, D, NT><<<kGrid, S::kThreads, smem, stream>>>(p, k_map, v_map);
-  if ((e = cudaGetLastError()) != cudaSuccess || !p.record) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.records, p.group < 8 * NT ? p.group : 8 * NT);
-  cfg.blockDim = dim3(2 * D);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kGrid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<kCache, D, NT>, p, k_map, v_map)) != cudaSuccess || !p.record) return e;
+  cfg.gridDim = dim3((unsigned)p.records, p.group < 8 * NT ? p.group : 8 * NT);
+  cfg.blockDim = dim3(2 * D);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, NT, kCache == kCacheBf16 || kCache == kCacheE4m3>, p);
 }
 

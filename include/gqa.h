@@ -443,7 +443,8 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
  *                belongs to the graph as long as it is replayed
  *   batch 1 .. 65535; d 64, 128 or 256; 1 .. 1024 query heads, a multiple of the
  *   kv_heads; page_size 16, 32, 64, 128 or 256; page_size * max_pages_per_seq at
- *   most 2^30
+ *   most 2^30, and times batch * kv_heads (more for groups of over 8) at most
+ *   about 2^43; q_scale finite, the other scales > 0 too
  *
  * A sequence of length 0 produces a zero row and lse = -infinity.  Slots outside
  * the visible tokens may hold anything, NaN too.  A page outside [0, num_pages)
