@@ -107,7 +107,7 @@ def test_append_matches_plain_form(dtype, d, rot, inter):
 
 
 @pytest.mark.parametrize("layout", ["hnd", "nhd"])
-@pytest.mark.parametrize("hq,hkv,page", [(1, 1, 16), (5, 1, 32), (32, 8, 64), (12, 12, 1), (7, 7, 5), (40, 2, 128)])
+@pytest.mark.parametrize("hq,hkv,page", [(1, 1, 16), (5, 1, 32), (28, 4, 64), (12, 12, 1), (7, 7, 5), (40, 2, 128)])
 def test_append_head_counts_pages_and_orders(layout, hq, hkv, page):
     check(Case([3, 9], [130, 9], hq=hq, hkv=hkv, page=page, layout=layout, seed=hq))
 

@@ -199,6 +199,7 @@ def test_captured_call_without_workspace_is_refused_by_the_library():
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
+        lens.add_(0)  # (a graph with something in it)
         status = gqa._binding().attn(*args)
     assert status == 7 and b"workspace of its own" in gqa.lib().gqa_last_error()
     gqa.gqa_release_workspace()
