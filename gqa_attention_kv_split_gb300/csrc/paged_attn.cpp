@@ -78,6 +78,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   p.hq = a.hq;
   p.hkv = a.hkv;
   p.head_blocks = (p.group + rows - 1) / rows;
+  for (p.gang_shift = 0; p.gang_shift < pa::kGangShift && ((a.hkv * p.head_blocks) >> p.gang_shift) % 2 == 0; ++p.gang_shift) {
+  }
   const int box = a.page_size < tile ? a.page_size : tile;
   for (p.page_shift = 0; (1 << p.page_shift) < a.page_size; ++p.page_shift) {
   }

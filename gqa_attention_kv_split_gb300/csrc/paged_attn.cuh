@@ -21,10 +21,17 @@
 // travel through TMEM).
 //
 //  * Grid: one block per SM, each with an equal share of the work of all
-//    (sequence, KV head, block of heads) units, in order, whatever the lengths --
-//    the shares are computed on the device from seq_lens.  A unit that
-//    lies inside one block is written by it; the pieces of one that does not go
-//    to the workspace (at most two per block), and a second kernel joins them.
+//    (sequence, KV head, block of heads) units, whatever the lengths -- the
+//    shares are computed on the device from seq_lens.  Blocks go in gangs of 8 (fewer if
+//    8 does not divide the units of a sequence): a gang has a share of the sequences'
+//    tokens, in order, and each of its blocks goes through them for other units, so
+//    that the heads of a token are read at the same time (rows of different heads side
+//    by side in DRAM, and two blocks of heads that need the same K and V: 48 sequences
+//    of up to 16001 tokens, token-major E4M3, 137 us without gangs, 124 with; 64 x 8192
+//    head-major 160 and 155; 32 heads on one KV head, 64 x 60000, 276 and 223; against
+//    0.1 us of a small call, and 24.3 and 24.8 us for 190 sequences of 128 tokens).
+//    A unit that lies inside one block is written by it; the pieces of one that does not
+//    go to the workspace (at most two per block), and a second kernel joins them.
 //  * Producer warps move tiles of 64 (32) tokens with tensor-map TMA copies
 //    into a ring of 128 KB: any page size and cache order is a box of the
 //    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
@@ -34,8 +41,8 @@
 //    unit only.
 //
 // Measured on GB300 (time in a graph): 64 sequences of up to 8192 tokens, 32/8 heads,
-// bf16: 160 us, 6.72 TB/s; 19 of 8192 (a unit per block): 91 us, 6.98 TB/s; 48 of up to
-// 16001, 64/8 heads, E4M3: 137 us, 5.77 TB/s; 8 of 131072, f16: 602 us, 7.14 TB/s.
+// bf16: 155 us, 6.94 TB/s; 20 of 8192: 99 us, 6.75 TB/s; 48 of up to 16001, 64/8 heads,
+// E4M3: 124 us, 6.33 TB/s; 8 of 131072, f16: 585 us, 7.34 TB/s.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -92,12 +99,12 @@ struct Shape {
   static_assert(kStages >= kGroups && kStages % (kProducers / 2) == 0, "whole turns of groups and producers");
 };
 
-// Block i of n has the work [total * i / n, total * (i + 1) / n).  (32-bit divisions where they do.)
+// Gang i of n has the work [total * i / n, total * (i + 1) / n).  (32-bit divisions where they do.)
 __device__ __forceinline__ int64_t share_begin(int i, int64_t total, int n) {
   const int64_t x = total * i;
   return x >> 32 ? x / n : (int64_t)((uint32_t)x / (uint32_t)n);
 }
-// The block that has a tile: the last one whose share begins at or before it.
+// The gang that has a tile: the last one whose share begins at or before it.
 __device__ __forceinline__ int share_of(int64_t tile, int64_t total, int n) {
   const int64_t x = (tile + 1) * n + total - 1;
   return (int)(x >> 32 ? x / total : (int64_t)((uint32_t)x / (uint32_t)total)) - 1;
@@ -116,8 +123,8 @@ struct Smem {
   uint64_t q_empty[2];
   int64_t scan[kWarps + 4];
   int most[kWarps + 4];
-  int64_t total;  // work of the whole call
-  int n_blocks;   // blocks with a share
+  int64_t total;  // work of one block of each gang
+  int n_gangs;    // gangs with a share
   int64_t end;    // of this block's share
   int64_t rem;    // the share's first tile within its first sequence,
   int b0;         // and that sequence
@@ -178,13 +185,16 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
-// First token and number of tiles of a sequence.
+// Which of its gang's blocks a block is, or the one that has a unit.
+__device__ __forceinline__ int lane_of_gang(const Params& p, int i) { return i & ((1 << p.gang_shift) - 1); }
+
+// First token and number of tiles of a sequence of the given length.
 template <int kTile>
 struct Span {
   int len, first, tile0, tiles;
-  __device__ __forceinline__ Span(const Params& p, int64_t b) {
+  __device__ __forceinline__ Span(const Params& p, int32_t seq_len) {
     const int64_t cap = p.max_pages << p.page_shift;
-    const int64_t n = p.seq_lens[b];
+    const int64_t n = seq_len;
     len = (int)(n < 0 ? 0 : (n > cap ? cap : n));
     first = p.window > 0 && len > p.window ? len - p.window : 0;
     tile0 = first / kTile;
@@ -199,14 +209,14 @@ template <int kTile, int kUnitWork>
 struct Walk {
   int left;   // of the share: from the piece's first tile on; by_unit: units behind this one
   int b;      // sequence
-  int unit;   // within the sequence: kv head * head blocks + head block
+  int unit;   // within the sequence: kv head * head blocks + head block; the next one is 2^gang_shift further
   int t_beg;  // first tile of the piece within the unit, and one past its last
   int t_end;
   Span<kTile> span;
   bool by_unit;
-  // From `rem` into the sequence's work on; valid() says whether there is a tile.
+  // From `rem` into the sequence's work (of one block of a gang) on; valid() says whether there is a tile.
   __device__ __forceinline__ Walk(const Params& p, int share, int b_, int64_t rem, bool by_unit_)
-      : b(b_), span(p, b_), by_unit(by_unit_) {
+      : b(b_), span(p, p.seq_lens[b_]), by_unit(by_unit_) {
     if (by_unit) {
       unit = (int)rem;
       t_beg = 0;
@@ -220,6 +230,7 @@ struct Walk {
       left = share - max(0, kUnitWork - at);
       t_end = min(span.tiles, t_beg + left);
     }
+    unit = (unit << p.gang_shift) + lane_of_gang(p, blockIdx.x);
   }
   __device__ __forceinline__ bool valid() const { return by_unit || left > 0; }
   // To the next piece; false at the end of the share.
@@ -227,11 +238,12 @@ struct Walk {
     left -= by_unit ? 1 : t_end - t_beg + kUnitWork;
     if (by_unit ? left < 0 : left <= 0) return false;
     t_beg = 0;
-    if (++unit == p.hkv * p.head_blocks) {
-      unit = 0;
+    unit += 1 << p.gang_shift;
+    if (unit >= p.hkv * p.head_blocks) {
+      unit -= p.hkv * p.head_blocks;
       do {
         if (++b >= p.batch) return false;
-        span = Span<kTile>(p, b);
+        span = Span<kTile>(p, p.seq_lens[b]);
       } while (span.tiles == 0);
     }
     t_end = by_unit ? span.tiles : min(span.tiles, left);
@@ -281,6 +293,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   Smem<S::kWarps, D, NT>& sm = *reinterpret_cast<Smem<S::kWarps, D, NT>*>(smem_raw + S::kStages * 2 * S::kHalf);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int units = p.hkv * p.head_blocks;
+  const int turns = units >> p.gang_shift, gang = (int)blockIdx.x >> p.gang_shift, gangs = kGrid >> p.gang_shift;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -303,8 +316,8 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0 && p.record && !p.record_by_unit) p.record[blockIdx.x].last = -1;
 
-  // ---- this block's share: of the work [T * block / n, T * (block + 1) / n), or one whole
-  // unit if there are no more units than blocks and none has more than kWholeTiles tiles:
+  // ---- this block's share: of the work of every 2^gang_shift-th unit, [T * gang / n, T *
+  // (gang + 1) / n), or one whole unit if there are no more units than blocks and none has more than kWholeTiles tiles:
   // to read them takes less time than to join the pieces of a split unit (2 sequences
   // of up to 200 tokens, 8 KV heads: 8.8 us split, 5.6 us whole; 16 of 512: 14.7 and 10.1).
   // Each thread sums the tiles of a contiguous range of sequences; a scan over the
@@ -317,7 +330,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   int64_t mine = 0;
   int most = 0;
   for (int64_t b = s0; b < s1; ++b) {
-    const Span<kTile> sp(p, b);
+    const Span<kTile> sp(p, p.seq_lens[b]);
     mine += sp.tiles + (sp.tiles ? int64_t(1) << kCountAt : 0);
     most = max(most, sp.tiles);
     if (sp.tiles == 0 && b % kGrid == blockIdx.x) {  // no token: a zero row
@@ -349,29 +362,29 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     most = max(most, sm.most[w]);
   }
   before += incl - mine;
-  const bool by_unit = most <= kWholeTiles && (total >> kCountAt) * units <= kGrid;
+  const bool by_unit = most <= kWholeTiles && (total >> kCountAt) * turns <= gangs;
   auto counted = [&](int64_t sum) {
     const int64_t n = sum >> kCountAt;
-    return (by_unit ? n : (sum & ((int64_t(1) << kCountAt) - 1)) + n * kUnitWork) * units;
+    return (by_unit ? n : (sum & ((int64_t(1) << kCountAt) - 1)) + n * kUnitWork) * turns;
   };
   before = counted(before);
   total = counted(total);
   mine = counted(mine);
-  const int n_blocks = total < kGrid ? (int)total : kGrid;  // blocks with a share: none is empty
-  const bool has_share = blockIdx.x < n_blocks;
-  const int64_t beg = has_share ? share_begin(blockIdx.x, total, n_blocks) : 0;
-  const int64_t end = has_share ? share_begin(blockIdx.x + 1, total, n_blocks) : 0;
+  const int n_gangs = total < gangs ? (int)total : gangs;  // gangs with a share: none is empty
+  const bool has_share = gang < n_gangs;
+  const int64_t beg = has_share ? share_begin(gang, total, n_gangs) : 0;
+  const int64_t end = has_share ? share_begin(gang + 1, total, n_gangs) : 0;
   if (threadIdx.x == 0) {
     sm.total = total;
-    sm.n_blocks = n_blocks;
+    sm.n_gangs = n_gangs;
     sm.end = end;
   }
   if (beg < end && beg >= before && beg < before + mine) {
     int64_t rem = beg - before;
     int64_t b = s0;
     for (;; ++b) {
-      const int tiles = Span<kTile>(p, b).tiles;
-      const int64_t n = (int64_t)(tiles == 0 ? 0 : by_unit ? 1 : tiles + kUnitWork) * units;
+      const int tiles = Span<kTile>(p, p.seq_lens[b]).tiles;
+      const int64_t n = (int64_t)(tiles == 0 ? 0 : by_unit ? 1 : tiles + kUnitWork) * turns;
       if (rem < n) break;
       rem -= n;
     }
@@ -818,10 +831,10 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       }
     }
     if (p.record && threadIdx.x == 0 && walk.t_beg == 0 && (!whole || p.record_by_unit)) {
-      // The unit begins here; it ends in the block that has its last tile.
+      // The unit begins here; it ends in the gang that has its last tile.
       const int64_t last_tile = sm.end - walk.left + walk.span.tiles - 1;
-      Record r{walk.b, walk.unit, (int)blockIdx.x, -1, slot};
-      if (!whole) r.last = share_of(last_tile, sm.total, sm.n_blocks);
+      Record r{walk.b, walk.unit, gang, -1, slot};
+      if (!whole) r.last = share_of(last_tile, sm.total, sm.n_gangs);
       p.record[p.record_by_unit ? walk.b * units + walk.unit : (int)blockIdx.x] = r;
     }
   } while (walk.next(p));
@@ -839,7 +852,7 @@ __global__ void __launch_bounds__(2 * D) paged_attn_join_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Record u = p.record[blockIdx.x];
   if (u.last < 0) return;
-  const int kvh = u.unit / p.head_blocks, r = blockIdx.y, first = u.first;
+  const int kvh = u.unit / p.head_blocks, r = blockIdx.y, first = u.first, lane = lane_of_gang(p, u.unit);
   const int head = kvh * p.group + (u.unit - kvh * p.head_blocks) * 8 * NT + r;
   if (head >= (kvh + 1) * p.group) return;
   const int grp = threadIdx.x / (D / 2), i = threadIdx.x % (D / 2);
@@ -857,7 +870,7 @@ __global__ void __launch_bounds__(2 * D) paged_attn_join_kernel(const __grid_con
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) {
       const int c = min(c0 + e * kGroups, u.last);
-      const int64_t at = (int64_t)(2 * c + (c == first ? u.first_slot : 0)) * (8 * NT) + r;
+      const int64_t at = (int64_t)(2 * ((c << p.gang_shift) + lane) + (c == first ? u.first_slot : 0)) * (8 * NT) + r;
       ml[e] = load_l2(p.part_ml + at);
       v[e] = load_l2(reinterpret_cast<const float2*>(p.part_o + at * D + 2 * i));
     }

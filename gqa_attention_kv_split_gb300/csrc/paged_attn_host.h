@@ -12,16 +12,17 @@ namespace gqa {
 namespace pa {
 
 constexpr int kGrid = 152;  // blocks: one per SM
+constexpr int kGangShift = 3;  // log2 of the largest gang: 152 blocks are 19 gangs of 8
 constexpr int kWholeTiles = 8;  // sequences of up to so many tiles are not split if there is a block for each unit
 
 // Tokens per ring stage, from the bytes of a token's row: 16 to 32 KB of K and V a stage.
 constexpr int tile_of(int row_bytes) { return row_bytes > 256 ? 32 : 64; }
 
-// For the joining kernel: a unit and the blocks that have a piece of it.
+// For the joining kernel: a unit and the gangs that have a piece of it.
 struct Record {
   int b, unit;      // sequence, unit within it
   int first, last;  // last < 0: the unit lies inside one block (or there is no unit)
-  int first_slot;   // which of the first block's two pieces it is (it is the first one of the others)
+  int first_slot;   // which of the first gang's two pieces it is (it is the first one of the others)
 };
 
 struct Params {
@@ -37,6 +38,7 @@ struct Params {
   int record_by_unit;  // ends elsewhere
   int64_t q_seq, q_head, batch, num_pages, max_pages;
   int hq, hkv, group, head_blocks;
+  int gang_shift;    // log2 of the blocks of a gang: the largest power of two up to 8 that divides a sequence's units
   int page_shift, box_shift;  // log2 of a page's tokens, and of those of one copy
   float scale_log2;  // scores to the exp2 domain
   float cap_in, cap_out;  // softcap: s2 = cap_out * tanh, tanh's argument doubled in the exp2 domain = cap_in * score; cap_out 0: none

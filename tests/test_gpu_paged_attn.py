@@ -148,6 +148,14 @@ def test_split_over_long_sequences(B, hq, hkv, d):
     check(make([5000 + 777 * i for i in range(B)], hq=hq, hkv=hkv, d=d, page=64, poison=False, dtype=BF16, seed=8))
 
 
+@pytest.mark.parametrize("hq,hkv", [(5, 5), (6, 6), (12, 12), (16, 16), (24, 24), (152, 152), (20, 2), (72, 3), (160, 8)])
+@pytest.mark.parametrize("lens", [(3000, 0, 1, 700, 64, 65), (130,) * 9, (0, 40, 0, 2100)])
+def test_blocks_that_share_sequences(hq, hkv, lens):
+    """Blocks that read the same tokens for 1, 2, 4 or 8 units of a sequence, once or in several turns."""
+    check(make(lens, hq=hq, hkv=hkv, d=64, page=32, seed=hq))
+    check(make(lens, hq=hq, hkv=hkv, d=128, page=16, layout="nhd", dtype=BF16, cache=E4M3, seed=hkv))
+
+
 def test_more_sequences_than_threads():
     """Several sequences a thread in the division of the work, empty ones among them."""
     lens = [(i * 37) % 40 if i % 5 else 0 for i in range(701)]
