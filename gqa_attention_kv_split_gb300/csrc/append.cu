@@ -74,6 +74,33 @@ __device__ __forceinline__ uint4 pack8(const float f[8], __nv_bfloat16) {
   return u;
 }
 
+// Two f32 operations in one instruction, each rounded as by itself: issue slots bound the
+// NVFP4 append (8192 tokens: 32.9 us with single operations, 30.8 with these).  Sums of
+// products are left single: a packed product and a packed sum come out as one rounding.
+struct Two {
+  uint64_t v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ void split(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ void sum(Two a, Two b, float* r) {
+  float a0, a1, b0, b1;
+  a.split(a0, a1);
+  b.split(b0, b1);
+  r[0] = __fadd_rn(a0, b0);
+  r[1] = __fadd_rn(a1, b1);
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // Two f32 -> two E4M3 bytes (lo in the low byte), RNE, saturating; NaN stays NaN.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -81,12 +108,14 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ uint2 pack8_e4m3(const float f[8], float inv_scale) {
-  uint2 u;
-  u.x = f32x2_to_e4m3x2(__fmul_rn(f[0], inv_scale), __fmul_rn(f[1], inv_scale)) |
-        (f32x2_to_e4m3x2(__fmul_rn(f[2], inv_scale), __fmul_rn(f[3], inv_scale)) << 16);
-  u.y = f32x2_to_e4m3x2(__fmul_rn(f[4], inv_scale), __fmul_rn(f[5], inv_scale)) |
-        (f32x2_to_e4m3x2(__fmul_rn(f[6], inv_scale), __fmul_rn(f[7], inv_scale)) << 16);
-  return u;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    mul2(Two(f[2 * i], f[2 * i + 1]), Two(inv_scale, inv_scale)).split(lo, hi);
+    w[i] = f32x2_to_e4m3x2(lo, hi);
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 // Two f32 -> one byte of E2M1 codes (lo in the low nibble), RNE, saturating.
@@ -138,8 +167,12 @@ __device__ __forceinline__ uint32_t codes8(const float f[8], float scale) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
   uint32_t r = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r |= f32x2_to_e2m1x2(quotient(f[2 * i], scale, inv), quotient(f[2 * i + 1], scale, inv)) << (8 * i);
+  for (int i = 0; i < 4; ++i) {
+    const Two x(f[2 * i], f[2 * i + 1]), by(inv, inv), q = mul2(x, by);
+    float lo, hi;
+    fma2(fma2(q, Two(-scale, -scale), x), by, q).split(lo, hi);  // (quotient, two at a time)
+    r |= f32x2_to_e2m1x2(lo, hi) << (8 * i);
+  }
   if (scale == 448.f) {  // the largest scale: there may be infinities, whose correction is NaN
     r = 0;
 #pragma unroll
@@ -149,11 +182,15 @@ __device__ __forceinline__ uint32_t codes8(const float f[8], float scale) {
   return r;
 }
 
-// (x, y) -> (x c - y s, y c + x s), each product and sum rounded by itself.
-__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
-  const float u = x, w = y;
-  x = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
-  y = __fadd_rn(__fmul_rn(w, c), __fmul_rn(u, s));
+// (x, y) -> (x c - y s, y c + x s), each product and sum rounded by itself: the two pairs
+// (x[0], y[0]) and (x[1], y[1]), or one that lies together.
+__device__ __forceinline__ void turn_pairs(float* x, float* y, float c0, float s0, float c1, float s1) {
+  const Two u(x[0], x[1]), w(y[0], y[1]), c(c0, c1), s(s0, s1), minus_s(-s0, -s1);
+  sum(mul2(u, c), mul2(w, minus_s), x);
+  sum(mul2(w, c), mul2(u, s), y);
+}
+__device__ __forceinline__ void turn_pair(float* z, float c, float s) {
+  sum(mul2(Two(z[0], z[1]), Two(c, c)), mul2(Two(z[1], z[0]), Two(-s, s)), z);
 }
 
 // The sequence of token t: the last b with indptr[b] <= t (the whole warp).
@@ -287,10 +324,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
         if (a.interleaved) {
           float* z = i ? y : x;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) turn_pair(z[2 * e], z[2 * e + 1], c[e], s[e]);
+          for (int e = 0; e < 4; ++e) turn_pair(z + 2 * e, c[e], s[e]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) turn_pair(x[4 * i + e], y[4 * i + e], c[e], s[e]);
+          for (int e = 0; e < 4; e += 2) turn_pairs(x + 4 * i + e, y + 4 * i + e, c[e], s[e], c[e + 1], s[e + 1]);
         }
       }
     }
