@@ -656,11 +656,9 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
           __syncwarp();
         }
         // ---- softmax weights: rows (keys) g, g + 8 of each block; columns (heads) c2, c2 + 1
-        uint32_t pb[kBlocks][NT][2], pl[kBlocks][NT][2];  // the weights' two terms
-        float alpha[NT][2];
-        bool grow = false;
+        bool grow = false;  // has a score passed its head's maximum?
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int j = 0; j < kBlocks; ++j) {
 #pragma unroll
@@ -674,28 +672,43 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
               if (ka >= walk.span.len || ka < walk.span.first) s[j][t][0] = s[j][t][1] = -INFINITY;
               if (kc >= walk.span.len || kc < walk.span.first) s[j][t][2] = s[j][t][3] = -INFINITY;
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) grow |= s[j][t][e] > m[t][e & 1];
           }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float alpha[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = m[t][i];
+#pragma unroll
+              for (int j = 0; j < kBlocks; ++j) x = fmaxf(x, fmaxf(s[j][t][i], s[j][t][i + 2]));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              alpha[i] = x == -INFINITY ? 0.f : fast_exp2(m[t][i] - x);
+              m[t][i] = x;
+              l[t][i] *= alpha[i];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][i][e] *= alpha[e & 1];
+          }
+        }
+        uint32_t pb[kBlocks][NT][2], pl[kBlocks][NT][2];  // the weights' two terms
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < kBlocks; ++j) x = fmaxf(x, fmaxf(s[j][t][i], s[j][t][i + 2]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m[t][i], x);
-            const float sub = mn == -INFINITY ? 0.f : mn;
-            grow |= mn != m[t][i];
-            alpha[t][i] = fast_exp2(m[t][i] - sub);
-            m[t][i] = mn;
-            float sum = 0.f;
+            const float sub = m[t][i] == -INFINITY ? 0.f : m[t][i];
 #pragma unroll
             for (int j = 0; j < kBlocks; ++j) {
               s[j][t][i] = fast_exp2(s[j][t][i] - sub + kShift);
               s[j][t][i + 2] = fast_exp2(s[j][t][i + 2] - sub + kShift);
-              sum += s[j][t][i] + s[j][t][i + 2];
+              l[t][i] += s[j][t][i] + s[j][t][i + 2];
             }
-            l[t][i] = fmaf(l[t][i], alpha[t][i], sum);
           }
           // P^T as the B operand of O^T = V^T P^T: rows = keys, columns = heads
 #pragma unroll
@@ -717,14 +730,6 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
               }
             }
           }
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[t][i][e] *= alpha[t][e & 1];
         }
         // ---- O^T += V^T P^T
         if (!kFp8) {
