@@ -32,7 +32,7 @@
 //    0.1 us of a small call, and 24.3 and 24.8 us for 190 sequences of 128 tokens).
 //    A unit that lies inside one block is written by it; the pieces of one that does not
 //    go to the workspace (at most two per block), and a second kernel joins them.
-//  * Producer warps move tiles of 64 (32) tokens with tensor-map TMA copies
+//  * Producer warps move tiles of 32 to 128 tokens with tensor-map TMA copies
 //    into a ring of 128 KB: any page size and cache order is a box of the
 //    map.  The 128-byte (64-byte) swizzle makes every ldmatrix conflict-free.
 //  * Eight consumer warps (four at head dim 256), each with its own 32 (16) keys of

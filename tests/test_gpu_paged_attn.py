@@ -98,6 +98,15 @@ def test_window(window, d):
     check(make([0, 1, 16, 64, 65, 100, 400], d=d, window=window, seed=window), window=window)
 
 
+@pytest.mark.parametrize("window", [0, 1, 127, 128, 129])
+@pytest.mark.parametrize("cache,d", [(F16, 256), (F16, 128), (F16, 64), (E4M3, 64)])
+def test_tile_borders(window, cache, d):
+    """Lengths and windows around the tiles' 32, 64 and 128 tokens, in the smallest and the largest pages."""
+    lens = [31, 32, 33, 127, 128, 129, 255, 256, 257, 385]
+    for page in (16, 256):
+        check(make(lens, d=d, page=page, cache=cache, window=window, seed=window), window=window)
+
+
 @pytest.mark.parametrize("softcap", [0.5, 30.0])
 @pytest.mark.parametrize("dtype,cache", [(F16, F16), (BF16, E4M3)])
 def test_softcap(softcap, dtype, cache):
