@@ -80,10 +80,10 @@ struct Shape {
   static constexpr int kThreads = (kWarps + kProducers) * 32;
   // 16-key blocks that a warp takes of a tile: two give it two independent sums of
   // products and one reduction for 32 keys (1.28x over one block on 48 sequences of up to
-  // 16001 tokens in E4M3 pages of 64); with 16 heads and long rows the registers that the
-  // second one needs would spill (64 x 8192 tokens in bf16, 16 heads a KV head: 234 us
-  // with two, 210 with one).
-  static constexpr int kBlocks = NT == 2 && D > 64 ? 1 : 2;
+  // 16001 tokens in E4M3 pages of 64; 16 heads on one KV head, 64 x 60000: 83 us with two,
+  // 94 with one); with 16 heads and long rows the registers that the second one needs would
+  // spill (64 x 8192 tokens in bf16, 16 heads a KV head: 184 us with two, 164 with one).
+  static constexpr int kBlocks = NT == 2 && D > (kEsz == 1 ? 128 : 64) ? 1 : 2;
   static constexpr int kGroupWarps = kTile / (16 * kBlocks);  // warps that share a tile
   static constexpr int kGroups = kWarps / kGroupWarps;      // tiles in work at a time
   static constexpr int kHalf = kTile * kRow;                // bytes of K (and of V) of a stage

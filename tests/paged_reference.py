@@ -86,19 +86,35 @@ def attention(q, k_pages, v_pages, table, lens, *, q_scale=1.0, k_scale=1.0, v_s
     return out, lse, mag, reach
 
 
+def visible_magnitude(v_pages, table, lens, q_heads, *, v_scale=1.0, window=0, **_):
+    """sum_t |v_t| * v_scale over the visible tokens, [B, Hq, D]."""
+    cap_len = table.shape[1] * v_pages.shape[2]
+    rows = []
+    for b in range(len(lens)):
+        n = max(0, min(int(lens[b]), cap_len))
+        v = gather(v_pages, table[b], n)[:, max(0, n - window) if window else 0:]
+        rows.append(v.abs().sum(1).repeat_interleave(q_heads // v_pages.shape[1], 0) * v_scale)
+    return torch.stack(rows)
+
+
 def check_attention(got, got_lse, q, k_pages, v_pages, table, lens, **kw):
     """The bound, in its parts.  A score is a sum of D products over at most 16 chained f32 additions
     of a tensor-core step each (D <= 256): |error| <= 16 * 2^-23 * sum |q_i k_i| * scale; capping adds
     at most 4 roundings of an exponential's 2^-22 times the cap; the logarithm and the scale 2^-20 (1 +
     |lse|).  A weight is off by twice the scores' error (its own and the sum's) and by its rounding for
     the product with V: 2^-16 for a pair of terms, 2^-11 for the one f16 term of E4M3 pages and bf16
-    queries.  An output is a weighted sum, off by that times sum p |v|, and is rounded once by half a step
-    of its type."""
+    queries.  An f16 weight (f16 and E4M3 pages) also has a floor: the largest weight of a warp's keys is 2^14
+    and f16's spacing is nowhere below 2^-24, so that a weight is off by half of it, 2^-25, at most: 2^-39
+    of the largest weight and so of the weights' sum, whatever its own size.  (It shows where an output's large
+    weights all meet v = 0.)  An output is a weighted sum, off by the weights' errors times |v|, and is
+    rounded once by half a step of its type."""
     out, lse, mag, reach = attention(q.cpu(), k_pages.cpu(), v_pages.cpu(), table.cpu(), lens.cpu(), **kw)
     s_err = 2.0 ** -19 * reach + 2.0 ** -20 * kw.get("softcap", 0.0) + 2.0 ** -20
     w = 2.0 ** -11 if k_pages.dtype == torch.float8_e4m3fn and q.dtype == torch.bfloat16 else 2.0 ** -16
     fin = torch.finfo(got.dtype)
     tol = fin.eps / 2 * out.abs() + (1 + fin.eps) * (w + 2 * s_err)[..., None] * mag + fin.smallest_normal * fin.eps
+    if v_pages.dtype != torch.bfloat16:
+        tol += 2.0 ** -39 * visible_magnitude(v_pages.cpu(), table.cpu(), lens.cpu(), q.shape[1], **kw)
     err = (got.cpu().double() - out).abs()
     assert torch.isfinite(got.cpu().double()).all()
     assert (err <= tol).all(), f"out: worst {float((err / tol).max()):.2f} of the bound, |err| {float(err.max()):.3g}"
