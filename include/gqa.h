@@ -446,6 +446,11 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
  *   most 2^30, and times batch * kv_heads (more for groups of over 8) at most
  *   about 2^43; q_scale finite, the other scales > 0 too
  *
+ * Scores, maxima, sums and the output's accumulators are f32.  A softmax weight
+ * meets V as two 16-bit terms of the pages' type (f16 for E4M3 ones), 22 bits in
+ * f16 and 16 in bf16, or as one f16 term, 11 bits, for E4M3 pages and a bf16
+ * output; f16 terms are exact to 2^-39 of the largest weight at best.
+ *
  * A sequence of length 0 produces a zero row and lse = -infinity.  Slots outside
  * the visible tokens may hold anything, NaN too.  A page outside [0, num_pages)
  * is not read: page 0 is used instead and bit 1 of the error word is set.  The
