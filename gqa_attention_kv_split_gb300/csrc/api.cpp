@@ -25,6 +25,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "paged.h"
 
 namespace {
 

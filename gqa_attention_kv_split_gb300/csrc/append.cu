@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "paged.h"
 
 namespace gqa {
 namespace {

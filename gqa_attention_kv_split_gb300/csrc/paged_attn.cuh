@@ -51,7 +51,6 @@
 #include <atomic>
 
 #include "common.cuh"
-#include "kernels.h"
 #include "paged_attn_host.h"
 
 namespace gqa {

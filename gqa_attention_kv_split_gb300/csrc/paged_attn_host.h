@@ -6,7 +6,7 @@
 
 #include <cstdint>
 
-#include "kernels.h"
+#include "paged.h"
 
 namespace gqa {
 namespace pa {
