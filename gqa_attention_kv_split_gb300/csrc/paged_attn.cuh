@@ -89,7 +89,8 @@ struct Shape {
   // What starting and ending a unit costs, in tiles: about the time of 96 KB of K and V
   // for 8 heads, twice that for 16.  (12 sequences of up to 8192 tokens in bf16: 43.0 us
   // without it, 38.3 with 2 or 8 tiles; with 16 heads a KV head 62.6 us, 47.5 with 2,
-  // 43.9 with 8; 48 of up to 16001 in E4M3: 147.4, 140.5 with 2, 136.4 with 8.)
+  // 43.9 with 8; 48 of up to 16001 in E4M3: 147.4, 140.5 with 2, 136.4 with 8.  These before
+  // blocks went in gangs; with them 35.9, 40.6 and 124 us, and the same with 64 or 144 KB.)
   static constexpr int kUnitWork = NT * 96 * 1024 / (2 * kHalf);
   static constexpr int kRoom = 128 * 1024;  // the warps' join takes up to 68 KB
   // A whole number of groups' turns, so that a stage always belongs to one group (a
