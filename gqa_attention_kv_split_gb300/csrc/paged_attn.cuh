@@ -279,11 +279,8 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   constexpr bool kBf16 = kCache == kCacheBf16;
   constexpr bool kFp8 = kCache >= kCacheE4m3;
   constexpr bool kQBf16 = kBf16 || kCache == kCacheE4m3;  // the type of q and of the output
-  // A weight enters the product with V as two terms of the cache's type (22 bits of it,
-  // 16 in bf16), so that its rounding stays below the output's.  For E4M3 pages and bf16
-  // queries one f16 term does: its 11 bits are three more than the output's (48 sequences
-  // of up to 16001 tokens, 16 heads a KV head: 170 us with one, 197 with two).
-  constexpr bool kTwo = !kFp8 || !kQBf16;
+  // A weight enters the product with V as two terms of the pages' type (f16 for E4M3 ones): 22
+  // bits of it, 16 in bf16, so that its rounding stays far below the output's.
   constexpr int kUnitWork = S::kUnitWork;
   constexpr int kTile = S::kTile, kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr int kRows = 8 * NT;
@@ -724,10 +721,8 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
               const uint32_t x0 = pack_f16(v[0], v[1]), x1 = pack_f16(v[2], v[3]);
               pb[j][t][0] = movm_t(x0);
               pb[j][t][1] = movm_t(x1);
-              if (kTwo) {
-                pl[j][t][0] = movm_t(pack_f16(v[0] - f16_lo(x0), v[1] - f16_hi(x0)));
-                pl[j][t][1] = movm_t(pack_f16(v[2] - f16_lo(x1), v[3] - f16_hi(x1)));
-              }
+              pl[j][t][0] = movm_t(pack_f16(v[0] - f16_lo(x0), v[1] - f16_hi(x0)));
+              pl[j][t][1] = movm_t(pack_f16(v[2] - f16_lo(x1), v[3] - f16_hi(x1)));
             }
           }
         }
@@ -742,7 +737,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 mma<kBf16>(o[t][i], a, pb[j][t][0], pb[j][t][1]);
-                if (kTwo) mma<kBf16>(o[t][i], a, pl[j][t][0], pl[j][t][1]);
+                mma<kBf16>(o[t][i], a, pl[j][t][0], pl[j][t][1]);
               }
             }
         } else {
@@ -761,7 +756,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                   mma<false>(o[t][2 * k + i], a, pb[j][t][0], pb[j][t][1]);
-                  if (kTwo) mma<false>(o[t][2 * k + i], a, pl[j][t][0], pl[j][t][1]);
+                  mma<false>(o[t][2 * k + i], a, pl[j][t][0], pl[j][t][1]);
                 }
               }
             }

@@ -1,0 +1,55 @@
+"""GPU: what gqa_paged_attn keeps of its numbers, held to bounds that leave no room for
+a shorter weight, a query element that has lost bits, or a cap that costs the score."""
+import pytest
+import torch
+
+import gqa_attention_kv_split_gb300 as gqa
+import paged_reference as R
+from test_gpu_paged_attn import BF16, DEV, E4M3, F16, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    gqa.build()
+    yield
+    assert gqa.gqa_check_device_errors(0) == 0
+
+
+def check(x, **kw):
+    """As paged_reference.check_attention, with these two parts narrower.  A weight meets V as two terms:
+    each is off by half a step, 2^-8 in bf16 (bf16 pages) and 2^-11 in f16, of what it has to hold, so that
+    the pair is off by 2^-16 or 2^-22.  The cap c tanh(s / c) has a slope of 1 at most, so that it passes on
+    the score's error, and its own is relative: s / c is off by 2^-23 (two roundings, and tanh's condition
+    is below 1), tanh by 2^-22 (two units in the last place), and the product with c, itself rounded, by
+    2^-23: 2^-21 of the capped score, which is at most min(c, reach)."""
+    q, k, v, table, lens = x
+    lse = torch.full(q.shape[:2], 9.0, device=DEV)
+    got = gqa.gqa_paged_attn(q, k, v, table, lens, lse=lse, **kw).cpu()
+    q, k, v, table, lens = (t.cpu() for t in x)
+    out, want_lse, mag, reach = R.attention(q, k, v, table, lens, **kw)
+    s_err = 2.0 ** -19 * reach + 2.0 ** -20
+    if kw.get("softcap"):
+        s_err += 2.0 ** -21 * reach.clamp(max=kw["softcap"])
+    fin = torch.finfo(got.dtype)
+    w = 2.0 ** -16 if v.dtype == BF16 else 2.0 ** -22
+    tol = fin.eps / 2 * out.abs() + (1 + fin.eps) * (w + 2 * s_err)[..., None] * mag + fin.smallest_normal * fin.eps
+    if v.dtype != BF16:  # an f16 term is nowhere finer than 2^-24, the largest weight 2^14
+        tol += 2.0 ** -39 * R.visible_magnitude(v, table, lens, q.shape[1], **kw)
+    err = (got.double() - out).abs()
+    assert (err <= tol).all(), f"out: worst {float((err / tol).max()):.2f} of the bound"
+    e, t = (lse.cpu().double() - want_lse).abs(), s_err + 2.0 ** -20 * want_lse.abs()
+    assert (e <= t).all(), f"lse: worst {float((e / t).max()):.2f} of the bound"
+
+
+def plain(lens, **kw):
+    return make(lens, poison=False, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group", [4, 16])
+@pytest.mark.parametrize("dtype,cache", [(BF16, E4M3), (F16, E4M3), (F16, F16), (BF16, BF16)])
+def test_weights_keep_their_bits(dtype, cache, group, d):
+    """Scores near 0 over values of both signs: an output far below the values shows what the weights lost."""
+    check(plain([8, 5, 24, 300], hq=group, hkv=1, d=d, dtype=dtype, cache=cache, spread=0.02, seed=d + group))
