@@ -42,7 +42,7 @@
 //
 // Measured on GB300 (time in a graph): 64 sequences of up to 8192 tokens, 32/8 heads,
 // bf16: 155 us, 6.94 TB/s; 20 of 8192: 99 us, 6.75 TB/s; 48 of up to 16001, 64/8 heads,
-// E4M3: 124 us, 6.33 TB/s; 8 of 131072, f16: 585 us, 7.34 TB/s.
+// E4M3: 126 us, 6.27 TB/s; 8 of 131072, f16: 585 us, 7.34 TB/s.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -79,8 +79,8 @@ struct Shape {
   static constexpr int kThreads = (kWarps + kProducers) * 32;
   // 16-key blocks that a warp takes of a tile: two give it two independent sums of
   // products and one reduction for 32 keys (1.28x over one block on 48 sequences of up to
-  // 16001 tokens in E4M3 pages of 64; 16 heads on one KV head, 64 x 60000: 83 us with two,
-  // 94 with one); with 16 heads and long rows the registers that the second one needs would
+  // 16001 tokens in E4M3 pages of 64; 16 heads on one KV head, 64 x 60000: 95 us with two,
+  // 106 with one); with 16 heads and long rows the registers that the second one needs would
   // spill (64 x 8192 tokens in bf16, 16 heads a KV head: 184 us with two, 164 with one).
   static constexpr int kBlocks = NT == 2 && D > (kEsz == 1 ? 128 : 64) ? 1 : 2;
   static constexpr int kGroupWarps = kTile / (16 * kBlocks);  // warps that share a tile
@@ -280,7 +280,9 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   constexpr bool kFp8 = kCache >= kCacheE4m3;
   constexpr bool kQBf16 = kBf16 || kCache == kCacheE4m3;  // the type of q and of the output
   // A weight enters the product with V as two terms of the pages' type (f16 for E4M3 ones): 22
-  // bits of it, 16 in bf16, so that its rounding stays far below the output's.
+  // bits of it, 16 in bf16, so that its rounding stays far below the output's.  (One f16 term
+  // of 11 bits, over E4M3 pages: 48 sequences of up to 16001 tokens 124 us instead of 126,
+  // with 16 heads a KV head 84 instead of 95; but outputs 2e-4 off the f32 form's.)
   constexpr int kUnitWork = S::kUnitWork;
   constexpr int kTile = S::kTile, kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr int kRows = 8 * NT;
