@@ -555,8 +555,9 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       sc[t][0] = sc[t][1] = 1.f;
       if (kFp8 && kQBf16) {
         // bf16 rows enter the f16 product scaled by a power of two that brings their
-        // largest element into [1, 2): exact but for elements below 2^-14 of it, whose
-        // rounding is at most 2^-25 of the largest.
+        // largest element into [2^15, 2^16) (65280 is the largest bf16 number there, 65504
+        // f16's; the products are summed in f32): exact but for elements below 2^-29 of it,
+        // whose rounding is at most 2^-40 of the largest.
         uint32_t mx = 0;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -567,9 +568,9 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
           }
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int ex = min(max((int)(mx >> 7), 1), 253);  // biased exponent
-        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-        const float up = __uint_as_float((uint32_t)ex << 23);
+        const int ex = min(max((int)(mx >> 7), 16), 254);  // biased exponent
+        const float down = __uint_as_float((uint32_t)(269 - ex) << 23);
+        const float up = __uint_as_float((uint32_t)(ex - 15) << 23);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll

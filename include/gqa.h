@@ -449,6 +449,7 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
  * Scores, maxima, sums and the output's accumulators are f32.  A softmax weight
  * meets V as two 16-bit terms of the pages' type (f16 for E4M3 ones), 22 bits in
  * f16 and 16 in bf16; f16 terms are exact to 2^-39 of the largest weight at best.
+ * A bf16 query over E4M3 pages is exact to 2^-40 of its row's largest element.
  *
  * A sequence of length 0 produces a zero row and lse = -infinity.  Slots outside
  * the visible tokens may hold anything, NaN too.  A page outside [0, num_pages)

@@ -23,15 +23,21 @@ def check(x, **kw):
     the pair is off by 2^-16 or 2^-22.  The cap c tanh(s / c) has a slope of 1 at most, so that it passes on
     the score's error, and its own is relative: s / c is off by 2^-23 (two roundings, and tanh's condition
     is below 1), tanh by 2^-22 (two units in the last place), and the product with c, itself rounded, by
-    2^-23: 2^-21 of the capped score, which is at most min(c, reach)."""
-    q, k, v, table, lens = x
+    2^-23: 2^-21 of the capped score, which is at most min(c, reach).  A bf16 query over E4M3 pages enters
+    the product in f16, its row's largest element at 2^15 at least: f16's spacing is nowhere below 2^-24, so
+    that an element is off by half of it, 2^-25, at most: 2^-40 of the largest one, times |k| in the score."""
+    q = x[0]
     lse = torch.full(q.shape[:2], 9.0, device=DEV)
-    got = gqa.gqa_paged_attn(q, k, v, table, lens, lse=lse, **kw).cpu()
+    got = gqa.gqa_paged_attn(*x, lse=lse, **kw).cpu()
     q, k, v, table, lens = (t.cpu() for t in x)
     out, want_lse, mag, reach = R.attention(q, k, v, table, lens, **kw)
     s_err = 2.0 ** -19 * reach + 2.0 ** -20
     if kw.get("softcap"):
         s_err += 2.0 ** -21 * reach.clamp(max=kw["softcap"])
+    if q.dtype == BF16 and k.dtype == E4M3:
+        most = torch.stack([R.gather(k, table[b], int(n)).abs().sum(-1).amax(-1) for b, n in enumerate(lens)])  # [B, Hkv]
+        most = most.repeat_interleave(q.shape[1] // k.shape[1], 1) * abs(kw.get("q_scale", 1.0)) / q.shape[2] ** 0.5
+        s_err += 2.0 ** -40 * q.double().abs().amax(-1) * most
     fin = torch.finfo(got.dtype)
     w = 2.0 ** -16 if v.dtype == BF16 else 2.0 ** -22
     tol = fin.eps / 2 * out.abs() + (1 + fin.eps) * (w + 2 * s_err)[..., None] * mag + fin.smallest_normal * fin.eps
@@ -53,3 +59,12 @@ def plain(lens, **kw):
 def test_weights_keep_their_bits(dtype, cache, group, d):
     """Scores near 0 over values of both signs: an output far below the values shows what the weights lost."""
     check(plain([8, 5, 24, 300], hq=group, hkv=1, d=d, dtype=dtype, cache=cache, spread=0.02, seed=d + group))
+
+
+@pytest.mark.parametrize("up", [10, 20, 28])
+def test_bf16_query_elements_far_below_the_largest(up):
+    """One element of a row 2^up times the others, where the keys are zero: the others make the scores."""
+    q, k, v, table, lens = plain([80, 33], dtype=BF16, cache=E4M3, seed=up)
+    q[..., 5] = 2.0 ** up
+    k[..., 5] = 0
+    check((q, k, v, table, lens), q_scale=1 / 16)
