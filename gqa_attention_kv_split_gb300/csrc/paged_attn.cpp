@@ -2,7 +2,9 @@
 // workspace layout, choice of the instance.
 #include <cuda.h>  // CUtensorMap and the cuTensorMapEncodeTiled prototype (resolved at run time)
 
+#include <algorithm>
 #include <cmath>
+#include <limits>
 #include <mutex>
 
 #include "paged_attn_host.h"
@@ -94,8 +96,10 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   p.records = units <= pa::kGrid ? (int)units : pa::kGrid;
   const double log2e = 1.4426950408889634;
   p.scale_log2 = (float)(a.scale * log2e);
-  p.cap_in = a.softcap > 0.f ? (float)(2.0 * log2e * a.scale / a.softcap) : 0.f;
-  p.cap_out = a.softcap > 0.f ? (float)(a.softcap * log2e) : 0.f;
+  // (a cap at the end of f32's range stays finite, twice itself too)
+  const double cap = a.softcap * log2e, most = std::numeric_limits<float>::max() / 2;
+  p.cap_out = a.softcap > 0.f ? (float)std::min(cap, most) : 0.f;
+  p.cap_inv = a.softcap > 0.f ? (float)std::min(1.0 / cap, most) : 0.f;
   p.v_scale = a.v_scale;
   p.window = a.window;
   p.starve = a.starve;

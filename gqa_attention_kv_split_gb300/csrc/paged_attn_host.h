@@ -43,7 +43,7 @@ struct Params {
   int gang_shift;    // log2 of the blocks of a gang: the largest power of two up to 8 that divides a sequence's units
   int page_shift, box_shift;  // log2 of a page's tokens, and of those of one copy
   float scale_log2;  // scores to the exp2 domain
-  float cap_in, cap_out;  // softcap: s2 = cap_out * tanh, tanh's argument doubled in the exp2 domain = cap_in * score; cap_out 0: none
+  float cap_out, cap_inv;  // the cap of the scores in the exp2 domain (0: none), and its reciprocal
   float v_scale;
   int window, starve;
 };

@@ -446,7 +446,8 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
  *   most 2^30, and times batch * kv_heads (more for groups of over 8) at most
  *   about 2^43; q_scale finite, the other scales > 0 too
  *
- * Scores, maxima, sums and the output's accumulators are f32.  A softmax weight
+ * Scores, maxima, sums and the output's accumulators are f32; a cap is exact to
+ * 2^-19 of the capped score, whatever its size.  A softmax weight
  * meets V as two 16-bit terms of the pages' type (f16 for E4M3 ones), 22 bits in
  * f16 and 16 in bf16; f16 terms are exact to 2^-39 of the largest weight at best.
  * A bf16 query over E4M3 pages is exact to 2^-40 of its row's largest element.

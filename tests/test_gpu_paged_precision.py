@@ -21,9 +21,10 @@ def check(x, **kw):
     """As paged_reference.check_attention, with these two parts narrower.  A weight meets V as two terms:
     each is off by half a step, 2^-8 in bf16 (bf16 pages) and 2^-11 in f16, of what it has to hold, so that
     the pair is off by 2^-16 or 2^-22.  The cap c tanh(s / c) has a slope of 1 at most, so that it passes on
-    the score's error, and its own is relative: s / c is off by 2^-23 (two roundings, and tanh's condition
-    is below 1), tanh by 2^-22 (two units in the last place), and the product with c, itself rounded, by
-    2^-23: 2^-21 of the capped score, which is at most min(c, reach).  A bf16 query over E4M3 pages enters
+    the score's error.  Its own is relative: with |s / c| at 1/4 at least, tanh as 1 - 2 r, r = 1 / (e + 1),
+    has from the exponential e (2^-22 of it), the sum (2^-24), the reciprocal (2^-23) and the exponent's
+    roundings at most 1.6 * 2^-22, which is 2^-19 of tanh(1/4); nearer to 0 the series is off by less than
+    2^-23.  So 2^-19 of the capped score, which is at most min(c, reach).  A bf16 query over E4M3 pages enters
     the product in f16, its row's largest element at 2^15 at least: f16's spacing is nowhere below 2^-24, so
     that an element is off by half of it, 2^-25, at most: 2^-40 of the largest one, times |k| in the score."""
     q = x[0]
@@ -33,7 +34,7 @@ def check(x, **kw):
     out, want_lse, mag, reach = R.attention(q, k, v, table, lens, **kw)
     s_err = 2.0 ** -19 * reach + 2.0 ** -20
     if kw.get("softcap"):
-        s_err += 2.0 ** -21 * reach.clamp(max=kw["softcap"])
+        s_err += 2.0 ** -19 * reach.clamp(max=kw["softcap"])
     if q.dtype == BF16 and k.dtype == E4M3:
         most = torch.stack([R.gather(k, table[b], int(n)).abs().sum(-1).amax(-1) for b, n in enumerate(lens)])  # [B, Hkv]
         most = most.repeat_interleave(q.shape[1] // k.shape[1], 1) * abs(kw.get("q_scale", 1.0)) / q.shape[2] ** 0.5
@@ -68,3 +69,11 @@ def test_bf16_query_elements_far_below_the_largest(up):
     q[..., 5] = 2.0 ** up
     k[..., 5] = 0
     check((q, k, v, table, lens), q_scale=1 / 16)
+
+
+@pytest.mark.parametrize("softcap", [0.5, 50.0, 1e3, 1e6, 3e38])
+@pytest.mark.parametrize("dtype,cache", [(F16, F16), (BF16, E4M3)])
+@pytest.mark.parametrize("spread", [0.05, 4.0])
+def test_caps_of_any_size(softcap, dtype, cache, spread):
+    """A cap far above the scores leaves them as they are."""
+    check(plain([300, 5], dtype=dtype, cache=cache, spread=spread, seed=3), softcap=softcap, q_scale=1 / 16 if cache == E4M3 else 1.0)
