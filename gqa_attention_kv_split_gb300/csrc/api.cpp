@@ -26,6 +26,7 @@
 
 #include "kernels.h"
 #include "paged.h"
+#include "stream_key.h"
 
 namespace {
 
@@ -138,7 +139,7 @@ struct Workspace {
   size_t bytes = 0;
 };
 std::mutex g_ws_mu;
-using WorkspaceMap = std::map<std::pair<int, uintptr_t>, Workspace>;
+using WorkspaceMap = std::map<gqa::StreamKey, Workspace>;
 WorkspaceMap g_ws;
 // Of gqa_paged_attn_t's calls without a workspace (a map of their own: growing one
 // never moves the other, which a captured call may have been given).
@@ -149,7 +150,7 @@ gqa_status workspace(int dev, cudaStream_t stream, size_t bytes, void** out, Wor
   *out = nullptr;
   if (bytes == 0) return GQA_OK;
   std::lock_guard<std::mutex> lk(g_ws_mu);
-  Workspace& w = map[{dev, reinterpret_cast<uintptr_t>(stream)}];
+  Workspace& w = map[gqa::stream_key(dev, stream)];
   if (w.bytes < bytes) {
     if (w.ptr) {
       // Work queued on this stream may still use the old buffer.
@@ -177,6 +178,32 @@ gqa_status workspace(int dev, cudaStream_t stream, size_t bytes, void** out, Wor
   *out = w.ptr;
   return GQA_OK;
 }
+
+// Gives back a thread's g_paged_ws buffers when it ends: its per-thread stream ends with it.
+// (g_ws's stay until gqa_release_workspace: a captured call may have been given one.)
+struct ThreadEnd {
+  uint64_t thread = 0;
+  ~ThreadEnd() {
+    if (!thread) return;
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    int prev = -1;
+    cudaGetDevice(&prev);
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // (leaves a capture of another thread alone)
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    for (auto it = g_paged_ws.begin(); it != g_paged_ws.end();) {
+      if (std::get<2>(it->first) != thread) {
+        ++it;
+        continue;
+      }
+      cudaSetDevice(std::get<0>(it->first));
+      cudaStreamSynchronize(cudaStreamPerThread);
+      cudaFree(it->second.ptr);
+      it = g_paged_ws.erase(it);
+    }
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
 
 // Carves 256-byte aligned sub-buffers out of one allocation.
 struct Carver {
@@ -1081,6 +1108,10 @@ gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, cons
       GQA_CUDA_TRY(cudaStreamIsCapturing(s, &capture), "cudaStreamIsCapturing");
       if (capture != cudaStreamCaptureStatusNone)
         return fail(GQA_ERR_WORKSPACE, "a captured call needs a workspace of its own (%lld bytes)", (long long)need);
+      if (s == cudaStreamPerThread) {
+        static thread_local ThreadEnd end;
+        end.thread = gqa::thread_number();
+      }
       // As much as the largest head layout needs, so that it never moves; and allocated
       // without disturbing a capture of another thread.
       cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
@@ -1101,7 +1132,7 @@ gqa_status gqa_release_workspace(void) {
   for (WorkspaceMap* map : {&g_ws, &g_paged_ws}) {
     for (auto& kv : *map) {
       if (kv.second.ptr) {
-        cudaSetDevice(kv.first.first);
+        cudaSetDevice(std::get<0>(kv.first));
         cudaFree(kv.second.ptr);
       }
     }

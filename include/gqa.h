@@ -30,6 +30,8 @@
  * scratch workspace per (device, stream), released by
  * gqa_release_workspace().  Two calls on the same stream are ordered by the
  * stream; calls on different streams use different workspaces.
+ * cudaStreamPerThread counts as one stream of each host thread;
+ * gqa_paged_attn_t's workspace for it is released when the thread ends.
  *
  * Errors.  Every entry point returns a gqa_status; GQA_OK means the work was
  * validated and enqueued (device pointers) or completed (host pointers).  On
