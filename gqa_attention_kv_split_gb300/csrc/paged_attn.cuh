@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
 template <int D, int NT, bool kQBf16>
 __global__ void __launch_bounds__(2 * D) paged_attn_join_kernel(const __grid_constant__ Params p) {
   constexpr int kGroups = 4, kBatch = 8;
-  __shared__ float part[kGroups][D / 2][4];
+  __shared__ float4 part[kGroups][D / 2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Record u = p.record[blockIdx.x];
   if (u.last < 0) return;
@@ -896,12 +896,12 @@ __global__ void __launch_bounds__(2 * D) paged_attn_join_kernel(const __grid_con
     for (int e = 0; e < kBatch; ++e)
       if (c0 + e * kGroups <= u.last) add(ml[e].x, ml[e].y, v[e].x, v[e].y);
   }
-  *reinterpret_cast<float4*>(part[grp][i]) = make_float4(m, l, x, y);
+  part[grp][i] = make_float4(m, l, x, y);
   __syncthreads();
   if (grp != 0) return;
 #pragma unroll
   for (int g = 1; g < kGroups; ++g) {
-    const float4 o = *reinterpret_cast<const float4*>(part[g][i]);
+    const float4 o = part[g][i];
     add(o.x, o.y, o.z, o.w);
   }
   store_out<D, kQBf16>(p, (int64_t)u.b * p.hq + head, 2 * i, x, y, m, l);
