@@ -217,11 +217,7 @@ __device__ __forceinline__ TokenPlace place_token(const AppendArgs& a, int64_t t
   if (a.indptr) {
     b = find_sequence(a.indptr, a.batch, t, lane);
     const int64_t lo = a.indptr[b], hi = a.indptr[b + 1];
-    if (t < lo || t >= hi) {
-      // Behind the last sequence is a padded batch; anywhere else the offsets are wrong.
-      if (t < a.indptr[a.batch] && lane == 0) atomicOr(&g_append_err, kErrBadIndptr);
-      return p;
-    }
+    if (t < lo || t >= hi) return p;  // behind the last sequence (a padded batch), or check_offsets flags it
     behind = hi - t;
   }
   const int64_t pos = (int64_t)a.kv_lens[b] - behind;
@@ -240,6 +236,15 @@ __device__ __forceinline__ TokenPlace place_token(const AppendArgs& a, int64_t t
   p.pos = pos;
   p.slot = (int)(pos - lp * a.page_size);
   return p;
+}
+
+// The offsets run from 0 upwards and end within the inputs: all of them are looked at, the
+// grid's threads taking one each (the last warps first, which place no token in a small call).
+__device__ __forceinline__ void check_offsets(const AppendArgs& a) {
+  const int64_t me = (int64_t)blockIdx.x * kAppendThreads + (kAppendThreads - 1 - threadIdx.x);
+  bool bad = me == 0 && (a.indptr[0] != 0 || a.indptr[a.batch] > a.total);
+  for (int64_t b = me; b < a.batch; b += (int64_t)gridDim.x * kAppendThreads) bad |= a.indptr[b] > a.indptr[b + 1];
+  if (bad) atomicOr(&g_append_err, kErrBadIndptr);
 }
 
 // kMode: kAppendSame (pages of the inputs' type), kAppendE4m3, kAppendNvfp4.
@@ -284,12 +289,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 
   Row next{0, (int)threadIdx.x / kLanes, make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
   load(next);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && a.indptr && a.indptr[a.batch] > a.total)
-    atomicOr(&g_append_err, kErrBadIndptr);
   if (warp < n_tok) {
     const TokenPlace p = place_token(a, t0 + warp, lane, angles[warp]);
     if (lane == 0) place[warp] = p;
   }
+  if (a.indptr) check_offsets(a);
   __syncthreads();
   // (NVFP4: a warp's four rows are of one token and one kind -- 32 or 0 q heads, 8 of k and
   // 8 of v -- so that its lanes take every branch together and the shuffles are whole.)
