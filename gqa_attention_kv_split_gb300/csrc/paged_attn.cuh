@@ -417,7 +417,10 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     const bool is_v = (warp - kWarps) & 1;
     const int pair = (warp - kWarps) >> 1;
     constexpr int kPairs = S::kProducers / 2;
-    const uint64_t pol = p.head_blocks == 1 ? policy_evict_first() : policy_evict_last();
+    // (K and V make room for others in L2 first, also where two blocks of heads read them: the
+    // gang reads them at nearly the same time.  Kept last, 32 heads on one KV head, 64 x 60000
+    // in bf16, take 209 us instead of 207.6, 20 heads 204 instead of 202.)
+    const uint64_t pol = policy_evict_first();
     // (a box and a page are powers of two: the loop below has no division)
     const int box_shift = p.box_shift, page_shift = p.page_shift;
     const int boxes = kTile >> box_shift;  // copies per tile of K (and of V)
