@@ -366,8 +366,8 @@ gqa_status gqa_debug_dequant_pages(const void* fp4, const void* sf, const int32_
  *                batch)
  *   rope         [positions, rot]  f32, or NULL: nothing is rotated
  *   q_out        [total, q_heads, d]  q's type, written; may be q itself
- *   d            64, 128 or 256; 1 .. 1024 heads; any page_size; rot a multiple
- *                of 16, at most d
+ *   batch 1 .. 2^20; d 64, 128 or 256; 1 .. 1024 heads; page_size 1 .. 2^20; rot
+ *   a multiple of 16, at most d
  *   k_scale, v_scale  finite, > 0; 1 for pages of the inputs' type
  *
  * Strides.  q, k, v, q_out and the pages may have any strides that are
