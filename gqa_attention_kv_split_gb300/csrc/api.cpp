@@ -312,7 +312,7 @@ extern "C" {
 
 const char* gqa_last_error(void) { return t_last_error.c_str(); }
 
-int gqa_version(void) { return 400; }  // 0.4.0: gqa_paged_append_t, nvfp4_paged_append_t, gqa_paged_attn_t
+int gqa_version(void) { return 401; }  // 0.4.1: caps of any size, workspaces of per-thread streams, every offset checked
 
 namespace {
 gqa_status decode_impl(const void* q, const void* kv, const int32_t* seq_lens, void* out, int64_t batch,

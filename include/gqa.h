@@ -1,13 +1,16 @@
 /*
  * gqa.h -- C ABI of libgqa: grouped-query attention kernels for NVIDIA GB300
  * (sm_103a), head_dim 128, 32 query heads over 8 KV heads (4 query heads per
- * KV head).
+ * KV head); for paged caches of other layouts the append and the attention of
+ * one token, whose descriptors give the sizes.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Pointers.  Every tensor argument is a plain pointer to a dense, row-major
- * (C-contiguous) array with the shape stated below.  All tensor pointers of
- * one call must be either
+ * (C-contiguous) array with the shape stated below; the entry points of other
+ * cache layouts (gqa_paged_append_t, nvfp4_paged_append_t, gqa_paged_attn_t)
+ * also take strided ones, and device memory only.  All tensor pointers of one
+ * call must be either
  *   - device memory of one and the same CUDA device (cudaMalloc'd, managed,
  *     or a PyTorch CUDA tensor's data pointer): the call enqueues its kernels
  *     on `stream` and returns without synchronising; or
@@ -373,7 +376,8 @@ gqa_status gqa_debug_dequant_pages(const void* fp4, const void* sf, const int32_
  * Strides.  q, k, v, q_out and the pages may have any strides that are
  * multiples of 16 bytes as long as the last dimension is dense (slices of a
  * fused projection; token-major pages given as a permuted view); what is
- * written must not overlap itself.  Every other tensor is dense.
+ * written must not overlap itself (checked) nor any other argument (not
+ * checked), but that q_out may be q.  Every other tensor is dense.
  *
  * Rows left alone.  Tokens at and behind qo_indptr[batch] (a padded batch) and
  * tokens of negative position (a sequence with kv_lens[b] = 0) are skipped:
@@ -382,8 +386,8 @@ gqa_status gqa_debug_dequant_pages(const void* fp4, const void* sf, const int32_
  * num_pages), is skipped too and bit 1 of the error word
  * (gqa_check_device_errors) is set; offsets that are not non-decreasing from 0
  * to at most `total` set bit 2, and nothing out of range is read or written.
- * Two tokens that share a slot leave either's row.  No workspace; nothing is
- * synchronised.  Host tensors are refused (GQA_ERR_UNSUPPORTED): a cache that
+ * Two tokens that share a slot leave pieces of either's row.  No workspace;
+ * nothing is synchronised.  Host tensors are refused (GQA_ERR_UNSUPPORTED): a cache that
  * lives on the host has nothing to be appended to on the device.
  */
 gqa_status gqa_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, gqa_tensor* k_pages,
@@ -399,7 +403,9 @@ gqa_status gqa_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const gq
  *   codes = E2M1_rne_sat(x / sf), all 0 where sf is 0 or NaN,
  *   q_out = E4M3_rne_sat(q * (1 / q_scale)), the reciprocal in f32.
  * The codes are those of f32 divisions.  A block that holds a NaN gets a NaN
- * scale; an infinity gets the largest scale and code.  q_scale is then the
+ * scale; an infinity gets the largest scale and code.  There is no scale for k
+ * and v beside the blocks': a block of magnitudes up to 6 * 2^-10 is stored as
+ * zeros, and sf has its 4 bits from amax = 6 * 2^-6 on.  q_scale is then the
  * attention's q_scale.
  *
  *   q      [total, 32, 128], k, v [total, 8, 128]  f16 or bf16, strided as above
@@ -455,7 +461,9 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
  * A bf16 query over E4M3 pages is exact to 2^-40 of its row's largest element.
  *
  * A sequence of length 0 produces a zero row and lse = -infinity.  Slots outside
- * the visible tokens may hold anything, NaN too.  A page outside [0, num_pages)
+ * the visible tokens may hold anything, NaN too; an infinity among the visible
+ * values makes its element of the output infinite or NaN.  out and lse overlap
+ * no other argument.  A page outside [0, num_pages)
  * is not read: page 0 is used instead and bit 1 of the error word is set.  The
  * split is chosen on the device from the lengths, so a captured call stays
  * balanced when they change.  One kernel, or two; host tensors are refused
