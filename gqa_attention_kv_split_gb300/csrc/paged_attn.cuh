@@ -15,10 +15,12 @@
 // with 16 keys (then 16 output elements) on the M side and 8 heads on the N
 // side.  The cache is the A operand straight from shared memory, a group of up
 // to 8 heads costs the same as one, and the accumulators of the output are D / 4
-// registers for each 8 heads.  The warp-level mma is enough: at HBM speed the
-// tensor pipe is busy for 14 % (bf16) or 17 % (E4M3) of the cycles (a tcgen05
-// tile has 128 rows for the 4 to 16 that there are, and its P would have to
-// travel through TMEM).
+// registers for each 8 heads.  Up to 8 heads the warp-level mma is enough: at HBM
+// speed the tensor pipe is busy for 14 % (bf16) or 26 % (E4M3) of the cycles.
+// From 16 heads on E4M3 pages are bound by the widening and the products (64 x
+// 60000 on one KV head: 96 us for 73 of HBM), and more than 16 heads by going
+// through a tile once for each 16 (32 heads: 208 us in bf16 for 145 of HBM, 179
+// in E4M3); accumulators in TMEM, with the keys on the M side, are not tried here.
 //
 //  * Grid: one block per SM, each with an equal share of the work of all
 //    (sequence, KV head, block of heads) units, whatever the lengths -- the
@@ -27,9 +29,10 @@
 //    tokens, in order, and each of its blocks goes through them for other units, so
 //    that the heads of a token are read at the same time (rows of different heads side
 //    by side in DRAM, and two blocks of heads that need the same K and V: 48 sequences
-//    of up to 16001 tokens, token-major E4M3, 137 us without gangs, 124 with; 64 x 8192
-//    head-major 160 and 155; 32 heads on one KV head, 64 x 60000, 276 and 223; against
-//    0.1 us of a small call, and 24.3 and 24.8 us for 190 sequences of 128 tokens).
+//    of up to 16001 tokens, token-major E4M3, 137 us without gangs, 124 with (one term a
+//    weight); 64 x 8192 head-major 160 and 155; 32 heads on one KV head, 64 x 60000, 276
+//    and 223; against 0.1 us of a small call, and 24.3 and 24.8 us for 190 sequences of
+//    128 tokens).
 //    A unit that lies inside one block is written by it; the pieces of one that does not
 //    go to the workspace (at most two per block), and a second kernel joins them.
 //  * Producer warps move tiles of 32 to 128 tokens with tensor-map TMA copies
@@ -90,7 +93,8 @@ struct Shape {
   // for 8 heads, twice that for 16.  (12 sequences of up to 8192 tokens in bf16: 43.0 us
   // without it, 38.3 with 2 or 8 tiles; with 16 heads a KV head 62.6 us, 47.5 with 2,
   // 43.9 with 8; 48 of up to 16001 in E4M3: 147.4, 140.5 with 2, 136.4 with 8.  These before
-  // blocks went in gangs; with them 35.9, 40.6 and 124 us, and the same with 64 or 144 KB.)
+  // blocks went in gangs; with them 35.9, 40.6 and, one term a weight as before, 124 us, and the
+  // same with 64 or 144 KB.)
   static constexpr int kUnitWork = NT * 96 * 1024 / (2 * kHalf);
   static constexpr int kRoom = 128 * 1024;  // the warps' join takes up to 68 KB
   // A whole number of groups' turns, so that a stage always belongs to one group (a

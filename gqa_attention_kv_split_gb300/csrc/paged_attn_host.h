@@ -17,7 +17,7 @@ constexpr int kWholeTiles = 8;  // sequences of up to so many tiles are not spli
 
 // Tokens per ring stage, from the bytes of a token's row: 16 to 32 KB of K and V a stage.
 // (48 sequences of up to 16001 tokens in E4M3 pages, head dim 64: 90 us with 8 KB, 74 with
-// 16; head dim 128: 124 us with 16 KB, 126 with 32.)
+// 16; head dim 128: 124 us with 16 KB, 126 with 32; with one term a weight.)
 constexpr int tile_of(int row_bytes) { return row_bytes > 256 ? 32 : row_bytes > 64 ? 64 : 128; }
 
 // For the joining kernel: a unit and the gangs that have a piece of it.
