@@ -14,11 +14,15 @@ missing or fails to load, every call raises.
                          *, q_scale=1.0, out_scale=1.0, out=None)
     gqa_debug_dequant_pages(fp4, sf, block_table, kv_lens, max_kv)
     gqa_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, *, qo_indptr=None, rope=None,
-                     interleaved=False, k_scale=1.0, v_scale=1.0, q_out=None)
+                     interleaved=False, k_scale=1.0, v_scale=1.0, q_out=None, positions=None, q_norm=None,
+                     k_norm=None, norm_eps=1e-6)
     nvfp4_paged_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, *, rope=None,
-                       interleaved=False, q_scale=1.0, q_out=None)
+                       interleaved=False, q_scale=1.0, q_out=None, positions=None, q_norm=None, k_norm=None,
+                       norm_eps=1e-6)
     gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=None, q_scale=1.0,
-                   k_scale=1.0, v_scale=1.0, window=0, softcap=0.0, workspace=None)
+                   k_scale=1.0, v_scale=1.0, window=0, softcap=0.0, workspace=None, sinks=0)
+    gqa_tree_mask(parents, qo_indptr, kv_lens, *, max_tokens=None, window=0, sinks=0, mask=None, positions=None)
+    gqa_paged_keep(pages, block_table, qo_indptr, kv_lens, kept, num_kept, *, new_lens=None)
 """
 from __future__ import annotations
 
@@ -35,6 +39,7 @@ __all__ = [
     "GqaError", "lib", "gqa_decode", "nvfp4_paged_ctx_attn", "gqa_debug_dequant_pages",
     "gqa_check_device_errors", "gqa_release_workspace", "gqa_decode_plan", "gqa_ctx_plan", "gqa_decode_paged", "gqa_debug_wait_expiry", "gqa_decode_noalloc", "gqa_debug_starve_producers", "gqa_set_schedule", "gqa_set_ctx_grid", "LIB_PATH",
     "build", "gqa_paged_append", "nvfp4_paged_append", "gqa_paged_attn", "gqa_paged_attn_workspace",
+    "gqa_tree_mask", "gqa_paged_keep",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -142,6 +147,16 @@ def lib() -> ctypes.CDLL:
             L.nvfp4_paged_append_t.restype = c.c_int
             L.gqa_paged_attn_t.argtypes = [tp] * 7 + [f32, f32, f32, c.c_int, f32, vp, i64, vp]
             L.gqa_paged_attn_t.restype = c.c_int
+            L.gqa_paged_norm_append_t.argtypes = [tp] * 13 + [c.c_int, f32, f32, f32, vp]
+            L.gqa_paged_norm_append_t.restype = c.c_int
+            L.nvfp4_paged_norm_append_t.argtypes = [tp] * 15 + [c.c_int, f32, f32, vp]
+            L.nvfp4_paged_norm_append_t.restype = c.c_int
+            L.gqa_paged_window_attn_t.argtypes = [tp] * 7 + [f32, f32, f32, c.c_int, c.c_int, f32, vp, i64, vp]
+            L.gqa_paged_window_attn_t.restype = c.c_int
+            L.gqa_tree_mask_t.argtypes = [tp] * 5 + [c.c_int, c.c_int, vp]
+            L.gqa_tree_mask_t.restype = c.c_int
+            L.gqa_paged_keep_t.argtypes = [c.POINTER(tp), c.c_int] + [tp] * 6 + [vp]
+            L.gqa_paged_keep_t.restype = c.c_int
             L.gqa_paged_attn_workspace.argtypes = [i64, i64, i64]
             L.gqa_paged_attn_workspace.restype = i64
             L.gqa_release_workspace.argtypes = []
@@ -265,7 +280,9 @@ def _binding():
                 loader.exec_module(m)
                 m.setup(torch.Tensor, _raw_stream, tuple(_DTYPES.items()),
                         tuple(ctypes.cast(f, ctypes.c_void_p).value
-                              for f in (L.gqa_paged_append_t, L.nvfp4_paged_append_t, L.gqa_paged_attn_t)))
+                              for f in (L.gqa_paged_append_t, L.nvfp4_paged_append_t, L.gqa_paged_window_attn_t,
+                                        L.gqa_paged_norm_append_t, L.nvfp4_paged_norm_append_t, L.gqa_tree_mask_t,
+                                        L.gqa_paged_keep_t)))
                 _binding_module = m
     return _binding_module
 
@@ -275,7 +292,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d:
 
 
 def gqa_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, *, qo_indptr=None, rope=None,
-                     interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0, q_out=None):
+                     interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0, q_out=None, positions=None,
+                     q_norm=None, k_norm=None, norm_eps: float = 1e-6):
     """Rotate new q and k rows to their positions and append k and v to a
     paged cache (see include/gqa.h).
 
@@ -283,31 +301,75 @@ def gqa_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, *, qo_indp
     [num_pages,Hkv,page_size,D] of the same type or E4M3, in any order in
     memory; block_table [B,max_pages_per_seq], kv_lens [B] (the new tokens
     included) and qo_indptr [B+1] int32 (None: one token per sequence); rope
-    [positions,rot] f32, cosines then sines (None: no rotation).  Returns the
-    rotated queries (q_out, which may be q itself; None without q).
+    [positions,rot] f32, cosines then sines (None: no rotation).  With q_norm
+    or k_norm [D] (the inputs' type or f32) the heads of q or k are divided by
+    their root mean square (norm_eps under the root) and weighted before the
+    rotation; with positions [T] int32 those choose the angles (drafted tokens
+    of a tree).  Returns the rotated queries (q_out, which may be q itself;
+    None without q).
     """
     if q is not None and q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    st = _binding().append(q, k, v, k_pages, v_pages, block_table, kv_lens, qo_indptr, rope, q_out, interleaved, k_scale,
-                           v_scale)
+    st = _binding().append(q, k, v, k_pages, v_pages, block_table, kv_lens, qo_indptr, rope, q_out, positions, q_norm, k_norm,
+                           interleaved, norm_eps, k_scale, v_scale)
     if st:
         _check(st)
     return q_out
 
 
 def nvfp4_paged_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, *, rope=None,
-                       interleaved: bool = False, q_scale: float = 1.0, q_out=None):
+                       interleaved: bool = False, q_scale: float = 1.0, q_out=None, positions=None, q_norm=None,
+                       k_norm=None, norm_eps: float = 1e-6):
     """gqa_paged_append into the NVFP4 pages that nvfp4_paged_ctx_attn reads
     (see include/gqa.h): k and v quantised to E2M1 codes with one E4M3 scale
     per 16 elements.  Returns the rotated queries / q_scale as uint8 E4M3
     codes (or writes `q_out`; None without q)."""
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=torch.uint8, device=q.device)
-    st = _binding().nvfp4_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, rope, q_out, interleaved,
-                                 q_scale)
+    st = _binding().nvfp4_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, rope, q_out, positions,
+                                 q_norm, k_norm, interleaved, norm_eps, q_scale)
     if st:
         _check(st)
     return q_out
+
+
+def gqa_tree_mask(parents, qo_indptr, kv_lens, *, max_tokens: int | None = None, window: int = 0, sinks: int = 0, mask=None,
+                  positions=None):
+    """Visibility bits and positions of trees of drafted tokens (see
+    include/gqa.h): parents [T] (each token's parent within its own tree, -1
+    for one that follows the last cached token), qo_indptr [B+1] and kv_lens
+    [B] (the drafted tokens included) int32.  Returns mask [T,words] and
+    positions [T] int32 (or writes those given): made once a step, read by
+    gqa_paged_append (positions) and by the attention of every layer.  Trees
+    have up to `max_tokens` tokens, which gives words = ceil(max_tokens / 32)
+    where no mask is given.  window and sinks are those of the attention."""
+    if mask is None:
+        if max_tokens is None:
+            raise ValueError("max_tokens (the largest tree's size) or a mask is needed")
+        mask = torch.empty((parents.shape[0], (max_tokens + 31) // 32), dtype=torch.int32, device=parents.device)
+    if positions is None:
+        positions = torch.empty_like(parents, memory_format=torch.contiguous_format)
+    st = _binding().tree_mask(parents, qo_indptr, kv_lens, mask, positions, window, sinks)
+    if st:
+        _check(st)
+    return mask, positions
+
+
+def gqa_paged_keep(pages, block_table, qo_indptr, kv_lens, kept, num_kept, *, new_lens=None):
+    """Move the accepted tokens of each sequence's draft together behind its
+    cached tokens, in place, and give up the others (see include/gqa.h).
+
+    pages: up to 4 tensors [num_pages,H,page_size,w] or [layers,num_pages,H,
+    page_size,w] of any type (K and V, or the codes and scales of NVFP4
+    pages); kept [B,max_kept] int32, the accepted tokens' numbers within the
+    draft, rising; num_kept [B] int32.  Returns the sequences' new lengths [B]
+    int32 (or writes `new_lens`, which may not be kv_lens)."""
+    if new_lens is None:
+        new_lens = torch.empty_like(kv_lens, memory_format=torch.contiguous_format)
+    st = _binding().keep(tuple(pages), block_table, qo_indptr, kv_lens, kept, num_kept, new_lens)
+    if st:
+        _check(st)
+    return new_lens
 
 
 @functools.lru_cache(maxsize=None)
@@ -317,18 +379,19 @@ def gqa_paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int) -> int:
 
 
 def gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=None, q_scale: float = 1.0,
-                   k_scale: float = 1.0, v_scale: float = 1.0, window: int = 0, softcap: float = 0.0, workspace=None):
+                   k_scale: float = 1.0, v_scale: float = 1.0, window: int = 0, softcap: float = 0.0, workspace=None,
+                   sinks: int = 0):
     """Attention of one new token per sequence over a paged cache (see
     include/gqa.h): q [B,Hq,D] f16 or bf16, k_pages / v_pages
     [num_pages,Hkv,page_size,D] of q's type or E4M3, in any order in memory,
-    block_table [B,max_pages_per_seq] and seq_lens [B] int32.  Writes `lse`
-    [B,Hq] f32 if given.  The workspace is the library's for the stream (in
+    block_table [B,max_pages_per_seq] and seq_lens [B] int32.  Under a window
+    the first `sinks` tokens stay visible.  Writes `lse` [B,Hq] f32 if given.  The workspace is the library's for the stream (in
     a captured call: one from the graph's memory pool) unless one of at least
     gqa_paged_attn_workspace(Hq, Hkv, D) bytes (uint8) is given; calls that
     can run at the same time need one each."""
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    args = (q_scale, k_scale, v_scale, window, softcap)
+    args = (q_scale, k_scale, v_scale, window, softcap, sinks)
     call = _binding().attn
     st = call(q, k_pages, v_pages, block_table, seq_lens, out, lse, workspace, *args)
     if st == _ERR_WORKSPACE:  # being captured: one from the graph's memory pool

@@ -18,14 +18,17 @@ static PyObject* g_raw_stream;         /* device index -> cudaStream_t of its cu
 static PyObject *g_dtypes[8];          /* torch dtypes ... */
 static int32_t g_codes[8];             /* ... and their gqa_dtype */
 static int g_n_dtypes;
-static gqa_status (*g_append)(const gqa_tensor*, const gqa_tensor*, const gqa_tensor*, gqa_tensor*, gqa_tensor*,
-                              const gqa_tensor*, const gqa_tensor*, const gqa_tensor*, const gqa_tensor*, gqa_tensor*, int,
-                              float, float, gqa_stream_t);
-static gqa_status (*g_nvfp4_append)(const gqa_tensor*, const gqa_tensor*, const gqa_tensor*, gqa_tensor*, gqa_tensor*,
-                                    gqa_tensor*, gqa_tensor*, const gqa_tensor*, const gqa_tensor*, const gqa_tensor*,
-                                    const gqa_tensor*, gqa_tensor*, int, float, gqa_stream_t);
-static gqa_status (*g_attn)(const gqa_tensor*, const gqa_tensor*, const gqa_tensor*, const gqa_tensor*, const gqa_tensor*,
-                            gqa_tensor*, gqa_tensor*, float, float, float, int, float, void*, int64_t, gqa_stream_t);
+/* The library's entry points, in the order in which setup() gets them. */
+static __typeof__(&gqa_paged_append_t) g_append;
+static __typeof__(&nvfp4_paged_append_t) g_nvfp4_append;
+static __typeof__(&gqa_paged_window_attn_t) g_attn;
+static __typeof__(&gqa_paged_norm_append_t) g_norm_append;
+static __typeof__(&nvfp4_paged_norm_append_t) g_nvfp4_norm_append;
+static __typeof__(&gqa_tree_mask_t) g_tree_mask;
+static __typeof__(&gqa_paged_keep_t) g_keep;
+static void** const g_entries[] = {(void**)&g_append,           (void**)&g_nvfp4_append, (void**)&g_attn, (void**)&g_norm_append,
+                                   (void**)&g_nvfp4_norm_append, (void**)&g_tree_mask,    (void**)&g_keep};
+enum { kEntries = sizeof(g_entries) / sizeof(g_entries[0]) };
 /* torch.Tensor's own descriptors, looked up once: methods and attributes */
 static PyObject *m_data_ptr, *m_get_device, *m_stride, *a_dtype, *a_shape;
 
@@ -125,92 +128,150 @@ static int as_int(PyObject* x, int* out) {
   const long v = PyLong_AsLong(x);
   if (v == -1 && PyErr_Occurred()) return -1;
   if (v < INT32_MIN || v > INT32_MAX) {
-    PyErr_SetString(PyExc_OverflowError, "window does not fit 32 bits");
+    PyErr_SetString(PyExc_OverflowError, "a number does not fit 32 bits");
     return -1;
   }
   *out = (int)v;
   return 0;
 }
 
-/* append(q, k, v, k_pages, v_pages, block_table, kv_lens, qo_indptr, rope, q_out, interleaved, k_scale, v_scale) -> status */
+/* append(q, k, v, k_pages, v_pages, block_table, kv_lens, qo_indptr, rope, q_out, positions, q_norm, k_norm, interleaved,
+ * norm_eps, k_scale, v_scale) -> status */
 static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  static const char* const names[10] = {"q", "k", "v", "k_pages", "v_pages", "block_table", "kv_lens", "qo_indptr", "rope", "q_out"};
-  gqa_tensor d[10];
-  gqa_tensor* r[10];
-  float ks, vs;
+  static const char* const names[13] = {"q",         "k",    "v",     "k_pages",   "v_pages", "block_table", "kv_lens",
+                                        "qo_indptr", "rope", "q_out", "positions", "q_norm",  "k_norm"};
+  gqa_tensor d[13];
+  gqa_tensor* r[13];
+  float eps, ks, vs;
   gqa_stream_t stream;
   (void)self;
-  if (expect(n, 13) || fill_all(a, names, 10, d, r)) return NULL;
-  const int inter = PyObject_IsTrue(a[10]);
-  if (inter < 0 || as_float(a[11], &ks) || as_float(a[12], &vs) || stream_of(r[1], &stream)) return NULL;
+  if (expect(n, 17) || fill_all(a, names, 13, d, r)) return NULL;
+  const int inter = PyObject_IsTrue(a[13]);
+  if (inter < 0 || as_float(a[14], &eps) || as_float(a[15], &ks) || as_float(a[16], &vs) || stream_of(r[1], &stream)) return NULL;
   gqa_status st;
   Py_BEGIN_ALLOW_THREADS;
-  st = g_append(r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], inter, ks, vs, stream);
+  if (r[10] || r[11] || r[12])
+    st = g_norm_append(r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[10], r[11], r[12], r[9], inter, eps, ks, vs, stream);
+  else
+    st = g_append(r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], inter, ks, vs, stream);
   Py_END_ALLOW_THREADS;
   return PyLong_FromLong(st);
 }
 
-/* nvfp4_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, rope, q_out, interleaved, q_scale) -> status */
+/* nvfp4_append(q, k, v, k_fp4, k_sf, v_fp4, v_sf, block_table, qo_indptr, kv_lens, rope, q_out, positions, q_norm, k_norm,
+ * interleaved, norm_eps, q_scale) -> status */
 static PyObject* py_nvfp4_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  static const char* const names[12] = {"q",           "k",         "v",       "k_fp4", "k_sf", "v_fp4", "v_sf",
-                                        "block_table", "qo_indptr", "kv_lens", "rope",  "q_out"};
-  gqa_tensor d[12];
-  gqa_tensor* r[12];
-  float qs;
+  static const char* const names[15] = {"q",           "k",         "v",       "k_fp4", "k_sf",  "v_fp4",     "v_sf",
+                                        "block_table", "qo_indptr", "kv_lens", "rope",  "q_out", "positions", "q_norm", "k_norm"};
+  gqa_tensor d[15];
+  gqa_tensor* r[15];
+  float eps, qs;
   gqa_stream_t stream;
   (void)self;
-  if (expect(n, 14) || fill_all(a, names, 12, d, r)) return NULL;
-  const int inter = PyObject_IsTrue(a[12]);
-  if (inter < 0 || as_float(a[13], &qs) || stream_of(r[1], &stream)) return NULL;
+  if (expect(n, 18) || fill_all(a, names, 15, d, r)) return NULL;
+  const int inter = PyObject_IsTrue(a[15]);
+  if (inter < 0 || as_float(a[16], &eps) || as_float(a[17], &qs) || stream_of(r[1], &stream)) return NULL;
   gqa_status st;
   Py_BEGIN_ALLOW_THREADS;
-  st = g_nvfp4_append(r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], r[10], r[11], inter, qs, stream);
+  if (r[12] || r[13] || r[14])
+    st = g_nvfp4_norm_append(r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], r[10], r[12], r[13], r[14], r[11], inter,
+                             eps, qs, stream);
+  else
+    st = g_nvfp4_append(r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], r[10], r[11], inter, qs, stream);
   Py_END_ALLOW_THREADS;
   return PyLong_FromLong(st);
 }
 
-/* attn(q, k_pages, v_pages, block_table, seq_lens, out, lse, workspace, q_scale, k_scale, v_scale, window, softcap) -> status */
+/* A workspace tensor's memory; none for NULL.  -1 with an exception set if it is no dense row of bytes. */
+static int workspace_of(const gqa_tensor* t, void** ws, int64_t* bytes) {
+  *ws = NULL;
+  *bytes = 0;
+  if (!t) return 0;
+  if (t->dtype != GQA_U8 || t->ndim != 1 || (t->shape[0] > 1 && t->strides[0] != 1)) {
+    PyErr_SetString(PyExc_ValueError, "workspace must be a dense 1-d uint8 tensor");
+    return -1;
+  }
+  *ws = t->data;
+  *bytes = t->shape[0];
+  return 0;
+}
+
+/* attn(q, k_pages, v_pages, block_table, seq_lens, out, lse, workspace, q_scale, k_scale, v_scale, window, softcap[, sinks]) -> status */
 static PyObject* py_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   static const char* const names[8] = {"q", "k_pages", "v_pages", "block_table", "seq_lens", "out", "lse", "workspace"};
   gqa_tensor d[8];
   gqa_tensor* r[8];
   float qs, ks, vs, cap;
-  int window;
+  int window, sinks = 0;
   gqa_stream_t stream;
   (void)self;
-  if (expect(n, 13) || fill_all(a, names, 8, d, r)) return NULL;
+  if ((n != 14 && expect(n, 13)) || fill_all(a, names, 8, d, r)) return NULL;
   if (as_float(a[8], &qs) || as_float(a[9], &ks) || as_float(a[10], &vs) || as_int(a[11], &window) || as_float(a[12], &cap) ||
-      stream_of(r[0], &stream))
+      (n == 14 && as_int(a[13], &sinks)) || stream_of(r[0], &stream))
     return NULL;
-  void* ws = NULL;
-  int64_t bytes = 0;
-  if (r[7]) {
-    if (r[7]->dtype != GQA_U8 || r[7]->ndim != 1 || (r[7]->shape[0] > 1 && r[7]->strides[0] != 1)) {
-      PyErr_SetString(PyExc_ValueError, "workspace must be a dense 1-d uint8 tensor");
-      return NULL;
-    }
-    ws = r[7]->data;
-    bytes = r[7]->shape[0];
-  }
+  void* ws;
+  int64_t bytes;
+  if (workspace_of(r[7], &ws, &bytes)) return NULL;
   gqa_status st;
   Py_BEGIN_ALLOW_THREADS;
-  st = g_attn(r[0], r[1], r[2], r[3], r[4], r[5], r[6], qs, ks, vs, window, cap, ws, bytes, stream);
+  st = g_attn(r[0], r[1], r[2], r[3], r[4], r[5], r[6], qs, ks, vs, window, sinks, cap, ws, bytes, stream);
   Py_END_ALLOW_THREADS;
   return PyLong_FromLong(st);
 }
 
-/* setup(torch.Tensor, current raw stream function, ((dtype, code), ...), (three entry points' addresses)) */
+/* tree_mask(parents, qo_indptr, kv_lens, mask, positions, window, sinks) -> status */
+static PyObject* py_tree_mask(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char* const names[5] = {"parents", "qo_indptr", "kv_lens", "mask", "positions"};
+  gqa_tensor d[5];
+  gqa_tensor* r[5];
+  int window, sinks;
+  gqa_stream_t stream;
+  (void)self;
+  if (expect(n, 7) || fill_all(a, names, 5, d, r)) return NULL;
+  if (as_int(a[5], &window) || as_int(a[6], &sinks) || stream_of(r[0], &stream)) return NULL;
+  gqa_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_tree_mask(r[0], r[1], r[2], r[3], r[4], window, sinks, stream);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+/* keep((pages, ...), block_table, qo_indptr, kv_lens, kept, num_kept, new_lens) -> status */
+static PyObject* py_keep(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char* const names[6] = {"block_table", "qo_indptr", "kv_lens", "kept", "num_kept", "new_lens"};
+  static const char* const page_names[4] = {"pages[0]", "pages[1]", "pages[2]", "pages[3]"};
+  gqa_tensor d[6], pd[4];
+  gqa_tensor *r[6], *pr[4] = {NULL, NULL, NULL, NULL};
+  gqa_stream_t stream;
+  (void)self;
+  if (expect(n, 7)) return NULL;
+  if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) > 4) {
+    PyErr_SetString(PyExc_TypeError, "pages must be a tuple of up to 4 tensors");
+    return NULL;
+  }
+  const int count = (int)PyTuple_GET_SIZE(a[0]);
+  for (int i = 0; i < count; ++i)
+    if (fill(PyTuple_GET_ITEM(a[0], i), page_names[i], &pd[i], &pr[i])) return NULL;
+  if (fill_all(a + 1, names, 6, d, r) || stream_of(r[2], &stream)) return NULL;
+  gqa_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_keep((const gqa_tensor* const*)pr, count, r[0], r[1], r[2], r[3], r[4], r[5], stream);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+/* setup(torch.Tensor, current raw stream function, ((dtype, code), ...), (the entry points' addresses)) */
 static PyObject* py_setup(PyObject* self, PyObject* args) {
   PyObject *tensor, *stream, *dtypes, *addr;
   (void)self;
   if (!PyArg_ParseTuple(args, "O!OO!O!", &PyType_Type, &tensor, &stream, &PyTuple_Type, &dtypes, &PyTuple_Type, &addr)) return NULL;
   const Py_ssize_t n = PyTuple_GET_SIZE(dtypes);
-  if (n > 8 || PyTuple_GET_SIZE(addr) != 3) {
-    PyErr_SetString(PyExc_ValueError, "setup: up to 8 dtypes and 3 addresses");
+  if (n > 8 || PyTuple_GET_SIZE(addr) != kEntries) {
+    PyErr_Format(PyExc_ValueError, "setup: up to 8 dtypes and %d addresses", (int)kEntries);
     return NULL;
   }
-  void* f[3];
-  for (int i = 0; i < 3; ++i) {
+  void* f[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(addr, i));
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "setup: a null address");
@@ -238,9 +299,7 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   g_tensor = (PyTypeObject*)tensor;
   Py_INCREF(stream);
   g_raw_stream = stream;
-  *(void**)&g_append = f[0];
-  *(void**)&g_nvfp4_append = f[1];
-  *(void**)&g_attn = f[2];
+  for (int i = 0; i < kEntries; ++i) *g_entries[i] = f[i];
   Py_RETURN_NONE;
 }
 
@@ -248,6 +307,8 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, NULL},
                                 {"nvfp4_append", (PyCFunction)(void (*)(void))py_nvfp4_append, METH_FASTCALL, NULL},
                                 {"attn", (PyCFunction)(void (*)(void))py_attn, METH_FASTCALL, NULL},
+                                {"tree_mask", (PyCFunction)(void (*)(void))py_tree_mask, METH_FASTCALL, NULL},
+                                {"keep", (PyCFunction)(void (*)(void))py_keep, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -30,10 +30,55 @@ struct AppendArgs {
   int mode;                    // an AppendMode
   int tok_per_block;           // set by launch_append
   float inv_k, inv_v, inv_q;   // reciprocals of the scales of E4M3 values
+  const void *q_norm, *k_norm; // [d] weights of the heads' norms, the inputs' type or f32; or null: no norm
+  const int32_t* positions;    // [total] rows of the rope table; or null: each token's place in the cache
+  int norm_f32;
+  float norm_eps;
 };
 
-cudaError_t launch_append(AppendArgs a, cudaStream_t stream);
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t append_read_errors(uint32_t* word);
+// Of the instances with norms and positions (append_norm.cu).
+cudaError_t launch_append_norm(const AppendArgs& a, cudaStream_t stream);
+cudaError_t append_norm_read_errors(uint32_t* word);
+
+// ---- drafted tokens: trees, compaction --------------------------------------
+
+constexpr int kMaxTreeTokens = 1024;  // a row of bits has up to 32 words
+
+struct TreeMaskArgs {
+  const int32_t* parents;   // [total]
+  const int32_t* indptr;    // [batch + 1]
+  const int32_t* kv_lens;   // [batch], the drafted tokens included
+  uint32_t* mask;           // [total, words]
+  int32_t* positions;       // [total]
+  int64_t total, batch;
+  int words, window, sinks;
+};
+cudaError_t launch_tree_mask(const TreeMaskArgs& a, cudaStream_t stream);
+
+// One tensor of pages [layers, num_pages, heads, page_size, row]; strides in bytes.
+struct KeepTensor {
+  uint8_t* data;
+  int64_t s_layer, s_page, s_head, s_slot;
+  int64_t items;    // layers * heads * pieces
+  int64_t heads, pieces;  // pieces of `vec` bytes in a row
+  int vec;          // 16 or 8
+};
+constexpr int kKeepTensors = 4;
+struct KeepArgs {
+  KeepTensor t[kKeepTensors];
+  int tensors;
+  const int32_t* block_table;  // [batch, max_pages]
+  const int32_t* indptr;       // [batch + 1]
+  const int32_t* kv_lens;      // [batch], the drafted tokens included
+  const int32_t* kept;         // [batch, max_kept]
+  const int32_t* num_kept;     // [batch]
+  int32_t* new_lens;           // [batch]
+  int64_t batch, max_pages, num_pages, max_kept, page_size;
+};
+cudaError_t launch_keep(const KeepArgs& a, cudaStream_t stream);
+cudaError_t drafts_read_errors(uint32_t* word);
 
 // ---- one-token attention over a paged cache ---------------------------------
 
@@ -56,6 +101,7 @@ struct PagedAttnArgs {
   float scale, v_scale;        // of the scores (q_scale * k_scale / sqrt(d)) and of the output
   float softcap;               // 0: none
   int window;                  // 0: none
+  int sinks;                   // first tokens that stay visible under a window
   int starve;
 };
 

@@ -102,26 +102,27 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStrea
   p.cap_inv = a.softcap > 0.f ? (float)std::min(1.0 / cap, most) : 0.f;
   p.v_scale = a.v_scale;
   p.window = a.window;
+  p.sinks = a.window > 0 ? a.sinks : 0;  // (without a window every token is visible)
   p.starve = a.starve;
   CUtensorMap k_map, v_map;
   cudaError_t e;
   if ((e = make_map(a.k_pages, a, a.kp_page, a.kp_head, a.kp_slot, box, &k_map)) != cudaSuccess) return e;
   if ((e = make_map(a.v_pages, a, a.vp_page, a.vp_head, a.vp_slot, box, &v_map)) != cudaSuccess) return e;
-  switch (a.cache) {
-    case kCacheF16: return pa::launch_f16(p, a.d, k_map, v_map, stream);
-    case kCacheBf16: return pa::launch_bf16(p, a.d, k_map, v_map, stream);
-    case kCacheE4m3: return pa::launch_e4m3(p, a.d, k_map, v_map, stream);
-    default: return pa::launch_e4m3_f16(p, a.d, k_map, v_map, stream);
-  }
+  static constexpr pa::Launch plain[4] = {pa::launch_f16, pa::launch_bf16, pa::launch_e4m3, pa::launch_e4m3_f16};
+  static constexpr pa::Launch sinks[4] = {pa::launch_sinks_f16, pa::launch_sinks_bf16, pa::launch_sinks_e4m3,
+                                          pa::launch_sinks_e4m3_f16};
+  return (p.sinks ? sinks : plain)[a.cache](p, a.d, k_map, v_map, stream);
 }
 
 cudaError_t paged_attn_read_errors(uint32_t* word) {
   cudaError_t e = cudaDeviceSynchronize();
-  uint32_t w[3] = {0, 0, 0};
-  if (e == cudaSuccess) e = pa::read_errors_f16(&w[0]);
-  if (e == cudaSuccess) e = pa::read_errors_bf16(&w[1]);
-  if (e == cudaSuccess) e = pa::read_errors_e4m3(&w[2]);
-  *word = w[0] | w[1] | w[2];
+  *word = 0;
+  for (auto read : {pa::read_errors_f16, pa::read_errors_bf16, pa::read_errors_e4m3, pa::read_errors_sinks_f16,
+                    pa::read_errors_sinks_bf16, pa::read_errors_sinks_e4m3}) {
+    uint32_t w = 0;
+    if (e == cudaSuccess) e = read(&w);
+    *word |= w;
+  }
   return e;
 }
 

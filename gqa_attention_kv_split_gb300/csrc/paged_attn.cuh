@@ -5,7 +5,8 @@
 // Mathematics.  For sequence b, query head h and KV head g = h / G,
 //   s_t = cap( (q . K_t) * scale ),  cap(x) = softcap * tanh(x / softcap) if softcap > 0,
 //   out = v_scale * sum_t exp(s_t - m) V_t / sum_t exp(s_t - m),  lse = ln sum_t exp(s_t)
-// over max(0, len - window) <= t < len.  A range of tokens is summed as
+// over max(0, len - window) <= t < len, and t < sinks (kSinks: instances of their own,
+// whose units have the sinks' tiles and then the window's).  A range of tokens is summed as
 // (m, l, o) with the running maximum m, l = sum exp(s - m) and o = sum exp(s -
 // m) V in f32; ranges join by rescaling to the larger m.
 //
@@ -192,10 +193,12 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* map, int
 // Which of its gang's blocks a block is, or the one that has a unit.
 __device__ __forceinline__ int lane_of_gang(const Params& p, int i) { return i & ((1 << p.gang_shift) - 1); }
 
-// First token and number of tiles of a sequence of the given length.
-template <int kTile>
+// First token and number of tiles of a sequence of the given length.  With sinks the
+// tiles 0 .. sink_tiles - 1 come first and the others `gap` further on.
+template <int kTile, bool kSinks>
 struct Span {
   int len, first, tile0, tiles;
+  int sinks, sink_tiles, gap;
   __device__ __forceinline__ Span(const Params& p, int32_t seq_len) {
     const int64_t cap = p.max_pages << p.page_shift;
     const int64_t n = seq_len;
@@ -203,20 +206,51 @@ struct Span {
     first = p.window > 0 && len > p.window ? len - p.window : 0;
     tile0 = first / kTile;
     tiles = (len + kTile - 1) / kTile - tile0;  // (a capacity is at most 2^30 tokens)
+    if constexpr (kSinks) {
+      sinks = p.sinks < first ? p.sinks : 0;
+      sink_tiles = gap = 0;
+      if (first > 0 && sinks == 0) {  // the sinks reach the window
+        tiles += tile0;
+        first = tile0 = 0;
+      } else if (sinks > 0) {
+        sink_tiles = (sinks + kTile - 1) / kTile;
+        gap = max(0, tile0 - sink_tiles);
+        tiles += tile0 - gap;
+        tile0 = 0;
+      }
+    }
+  }
+  // Where a tile (or, scaled by 2^shift, a copy) of the unit lies in the sequence.
+  __device__ __forceinline__ int place(int i, int shift = 0) const {
+    if constexpr (kSinks) return i < (sink_tiles << shift) ? i : i + (gap << shift);
+    return i;
+  }
+  // Is there a visible one, and an invisible one, among the tokens [key, key + n)?
+  __device__ __forceinline__ bool any(int key, int n) const {
+    if constexpr (kSinks) return key < len && (key + n > first || key < sinks);
+    return key < len && key + n > first;
+  }
+  __device__ __forceinline__ bool edge(int key, int n) const {
+    if constexpr (kSinks) return key + n > len || (key < first && key + n > sinks);
+    return key + n > len || key < first;
+  }
+  __device__ __forceinline__ bool hidden(int key) const {
+    if constexpr (kSinks) return key >= len || (key < first && key >= sinks);
+    return key >= len || key < first;
   }
 };
 
 // Walks the units of a block's share.  Shares are counted in the work of a unit: its
 // tiles and, before them, what starting and ending a unit costs in tiles (kUnitWork);
 // or, by_unit, in whole units.  (A share has less than 2^31: the host sees to it.)
-template <int kTile, int kUnitWork>
+template <int kTile, int kUnitWork, bool kSinks>
 struct Walk {
   int left;   // of the share: from the piece's first tile on; by_unit: units behind this one
   int b;      // sequence
   int unit;   // within the sequence: kv head * head blocks + head block; the next one is 2^gang_shift further
   int t_beg;  // first tile of the piece within the unit, and one past its last
   int t_end;
-  Span<kTile> span;
+  Span<kTile, kSinks> span;
   bool by_unit;
   // From `rem` into the sequence's work (of one block of a gang) on; valid() says whether there is a tile.
   __device__ __forceinline__ Walk(const Params& p, int share, int b_, int64_t rem, bool by_unit_)
@@ -247,7 +281,7 @@ struct Walk {
       unit -= p.hkv * p.head_blocks;
       do {
         if (++b >= p.batch) return false;
-        span = Span<kTile>(p, p.seq_lens[b]);
+        span = Span<kTile, kSinks>(p, p.seq_lens[b]);
       } while (span.tiles == 0);
     }
     t_end = by_unit ? span.tiles : min(span.tiles, left);
@@ -290,7 +324,7 @@ __device__ __forceinline__ float2 load_l2(const float2* p) {
   return v;
 }
 
-template <int kCache, int D, int NT>
+template <int kCache, int D, int NT, bool kSinks>
 __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map) {
@@ -349,7 +383,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   int64_t mine = 0;
   int most = 0;
   for (int64_t b = s0; b < s1; ++b) {
-    const Span<kTile> sp(p, p.seq_lens[b]);
+    const Span<kTile, kSinks> sp(p, p.seq_lens[b]);
     mine += sp.tiles + (sp.tiles ? int64_t(1) << kCountAt : 0);
     most = max(most, sp.tiles);
     if (sp.tiles == 0 && b % kGrid == blockIdx.x) {  // no token: a zero row
@@ -402,7 +436,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     int64_t rem = beg - before;
     int64_t b = s0;
     for (;; ++b) {
-      const int tiles = Span<kTile>(p, p.seq_lens[b]).tiles;
+      const int tiles = Span<kTile, kSinks>(p, p.seq_lens[b]).tiles;
       const int64_t n = (int64_t)(tiles == 0 ? 0 : by_unit ? 1 : tiles + kUnitWork) * turns;
       if (rem < n) break;
       rem -= n;
@@ -412,7 +446,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
   }
   __syncthreads();
   if (beg >= end) return;
-  Walk<kTile, kUnitWork> walk(p, (int)(end - beg), sm.b0, sm.rem, by_unit);
+  Walk<kTile, kUnitWork, kSinks> walk(p, (int)(end - beg), sm.b0, sm.rem, by_unit);
   if (!walk.valid()) return;  // (a share that lies before a unit's first tile)
 
   if (warp >= kWarps) {
@@ -458,8 +492,12 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
       int c = ((walk.span.tile0 + walk.t_beg + skip) << (kTileShift - box_shift)) + lane;
       const int c_end = ((walk.span.len - 1) >> box_shift) + 1;
       const int c_first = walk.span.first >> box_shift;
+      const int c_sinks = kSinks ? ((walk.span.sinks - 1) >> box_shift) + 1 : 0;  // one past the last copy that has a sink
+      auto place = [&](int copy) { return walk.span.place(copy, kTileShift - box_shift); };
+      auto wanted = [&](int copy) { return (copy >= c_first || (kSinks && copy < c_sinks)) && copy < c_end; };
       auto page_of = [&](int copy) {
-        if (copy < c_first || copy >= c_end) return 0;
+        copy = place(copy);
+        if (!wanted(copy)) return 0;
         int g = row[copy >> (page_shift - box_shift)];
         if (g < 0 || g >= p.num_pages) {
           atomicOr(err, kErrBadIndex);
@@ -476,14 +514,15 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
           break;
         }
         const int pg = __shfl_sync(0xffffffffu, cur, (at + lane) & 31);
-        const bool live = lane < boxes && c >= c_first && c < c_end;
+        const int at_c = place(c);
+        const bool live = lane < boxes && wanted(at_c);
         const uint32_t bar = smem_u32(&sm.full[st]);
         const uint32_t bytes = box_bytes * __popc(__ballot_sync(0xffffffffu, live));
         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();
         if (live) {
           const uint32_t dst = lane_dst + st * 2 * S::kHalf;
-          const int slot = (c << box_shift) & ((1 << page_shift) - 1);
+          const int slot = (at_c << box_shift) & ((1 << page_shift) - 1);
           if (is_v)
             tma_5d(dst + S::kHalf, &v_map, slot, kvh, pg, bar, pol);
           else
@@ -624,14 +663,14 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     int tile = walk.t_beg + skip;
     for (; tile < walk.t_end; tile += S::kGroups) {
       if (dead) continue;
-      const int key0 = (walk.span.tile0 + tile) * kTile + row0;  // this warp's first key
+      const int key0 = walk.span.place(walk.span.tile0 + tile) * kTile + row0;  // this warp's first key
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), ph, err))) {
         dead = true;
         continue;
       }
       const uint32_t kb = ring_u + st * 2 * S::kHalf, vb = kb + S::kHalf;
-      if (key0 < walk.span.len && key0 + kKeys > walk.span.first) {
-        const bool edge = key0 + kKeys > walk.span.len || key0 < walk.span.first;
+      if (walk.span.any(key0, kKeys)) {
+        const bool edge = walk.span.edge(key0, kKeys);
         // ---- S^T = K Q^T
         float s[kBlocks][NT][4];
 #pragma unroll
@@ -672,7 +711,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
           for (int j = 0; j < kBlocks; ++j)
             for (int i = lane; i < 16 * (S::kRow / 16); i += 32) {
               const int r = i % 16, c16 = i / 16, key = key0 + 16 * j + r;
-              if (key >= walk.span.len || key < walk.span.first)
+              if (walk.span.hidden(key))
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + blk[j] + col(r, c16)), "r"(0) : "memory");
             }
           __syncwarp();
@@ -691,8 +730,8 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
             }
             if (edge) {
               const int ka = key0 + 16 * j + g, kc = ka + 8;
-              if (ka >= walk.span.len || ka < walk.span.first) s[j][t][0] = s[j][t][1] = -INFINITY;
-              if (kc >= walk.span.len || kc < walk.span.first) s[j][t][2] = s[j][t][3] = -INFINITY;
+              if (walk.span.hidden(ka)) s[j][t][0] = s[j][t][1] = -INFINITY;
+              if (walk.span.hidden(kc)) s[j][t][2] = s[j][t][3] = -INFINITY;
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) grow |= s[j][t][e] > m[t][e & 1];
@@ -914,7 +953,7 @@ __global__ void __launch_bounds__(2 * D) paged_attn_join_kernel(const __grid_con
   store_out<D, kQBf16>(p, (int64_t)u.b * p.hq + head, 2 * i, x, y, m, l);
 }
 
-template <int kCache, int D, int NT>
+template <int kCache, int D, int NT, bool kSinks>
 cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
                             cudaStream_t stream) {
   using S = Shape<kCache, D, NT>;
@@ -927,7 +966,7 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUt
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<kCache, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(paged_attn_kernel<kCache, D, NT, kSinks>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
@@ -941,27 +980,27 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUt
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<kCache, D, NT>, p, k_map, v_map)) != cudaSuccess || !p.record) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<kCache, D, NT, kSinks>, p, k_map, v_map)) != cudaSuccess || !p.record) return e;
   cfg.gridDim = dim3((unsigned)p.records, p.group < 8 * NT ? p.group : 8 * NT);
   cfg.blockDim = dim3(2 * D);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, NT, kCache == kCacheBf16 || kCache == kCacheE4m3>, p);
 }
 
-template <int kCache>
+template <int kCache, bool kSinks>
 cudaError_t launch_cache(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map,
                          cudaStream_t stream) {
   const bool two = p.group > 8;
   switch (d) {
     case 64:
-      return two ? launch_instance<kCache, 64, 2>(p, k_map, v_map, stream)
-                 : launch_instance<kCache, 64, 1>(p, k_map, v_map, stream);
+      return two ? launch_instance<kCache, 64, 2, kSinks>(p, k_map, v_map, stream)
+                 : launch_instance<kCache, 64, 1, kSinks>(p, k_map, v_map, stream);
     case 128:
-      return two ? launch_instance<kCache, 128, 2>(p, k_map, v_map, stream)
-                 : launch_instance<kCache, 128, 1>(p, k_map, v_map, stream);
+      return two ? launch_instance<kCache, 128, 2, kSinks>(p, k_map, v_map, stream)
+                 : launch_instance<kCache, 128, 1, kSinks>(p, k_map, v_map, stream);
     default:
-      return two ? launch_instance<kCache, 256, 2>(p, k_map, v_map, stream)
-                 : launch_instance<kCache, 256, 1>(p, k_map, v_map, stream);
+      return two ? launch_instance<kCache, 256, 2, kSinks>(p, k_map, v_map, stream)
+                 : launch_instance<kCache, 256, 1, kSinks>(p, k_map, v_map, stream);
   }
 }
 

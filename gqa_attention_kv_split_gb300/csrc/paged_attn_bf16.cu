@@ -5,7 +5,7 @@ namespace gqa {
 namespace pa {
 
 cudaError_t launch_bf16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
-  return launch_cache<kCacheBf16>(p, d, k_map, v_map, stream);
+  return launch_cache<kCacheBf16, false>(p, d, k_map, v_map, stream);
 }
 
 cudaError_t read_errors_bf16(uint32_t* word) { return read_errors_here(word); }

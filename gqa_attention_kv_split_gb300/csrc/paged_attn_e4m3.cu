@@ -5,11 +5,11 @@ namespace gqa {
 namespace pa {
 
 cudaError_t launch_e4m3(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
-  return launch_cache<kCacheE4m3>(p, d, k_map, v_map, stream);
+  return launch_cache<kCacheE4m3, false>(p, d, k_map, v_map, stream);
 }
 
 cudaError_t launch_e4m3_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
-  return launch_cache<kCacheE4m3F16>(p, d, k_map, v_map, stream);
+  return launch_cache<kCacheE4m3F16, false>(p, d, k_map, v_map, stream);
 }
 
 cudaError_t read_errors_e4m3(uint32_t* word) { return read_errors_here(word); }

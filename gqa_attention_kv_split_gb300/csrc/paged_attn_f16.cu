@@ -5,7 +5,7 @@ namespace gqa {
 namespace pa {
 
 cudaError_t launch_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
-  return launch_cache<kCacheF16>(p, d, k_map, v_map, stream);
+  return launch_cache<kCacheF16, false>(p, d, k_map, v_map, stream);
 }
 
 cudaError_t read_errors_f16(uint32_t* word) { return read_errors_here(word); }

@@ -45,17 +45,26 @@ struct Params {
   float scale_log2;  // scores to the exp2 domain
   float cap_out, cap_inv;  // the cap of the scores in the exp2 domain (0: none), and its reciprocal
   float v_scale;
-  int window, starve;
+  int window, sinks, starve;
 };
 
-// The instances of one cache type, each in a translation unit of its own.
+// The instances of one cache type, each in a translation unit of its own, and those with
+// sinks in others.
+using Launch = cudaError_t (*)(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_bf16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_e4m3(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_e4m3_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_sinks_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_sinks_bf16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_sinks_e4m3(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_sinks_e4m3_f16(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t read_errors_f16(uint32_t* word);
 cudaError_t read_errors_bf16(uint32_t* word);
 cudaError_t read_errors_e4m3(uint32_t* word);
+cudaError_t read_errors_sinks_f16(uint32_t* word);
+cudaError_t read_errors_sinks_bf16(uint32_t* word);
+cudaError_t read_errors_sinks_e4m3(uint32_t* word);
 
 }  // namespace pa
 }  // namespace gqa

@@ -422,6 +422,38 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
                                 gqa_tensor* q_out, int interleaved, float q_scale, gqa_stream_t stream);
 
 /*
+ * gqa_paged_norm_append_t, nvfp4_paged_norm_append_t -- the two appends with a
+ * norm of each query and key head before the rotation, and with angles of given
+ * positions:
+ *   x <- x * w / sqrt(sum_i x_i^2 / d + norm_eps)   (w = q_norm for q's heads,
+ *        k_norm for k's; values are not normed), then rotated, everything in f32
+ *        and rounded once, to what is stored
+ *   token t is rotated with row positions[t] of the rope table instead of row pos
+ *
+ *   q_norm, k_norm  [d]  the inputs' type or f32, both of one type; either or
+ *                both may be NULL: those heads are not normed
+ *   positions    [total]  int32, or NULL.  For tokens whose place in the cache is
+ *                not their position: drafted tokens of a tree (gqa_tree_mask_t).
+ *                They choose the angles alone; page and slot are as above.  A
+ *                token whose position lies outside the rope table is skipped and
+ *                bit 1 of the error word is set.  Needs rope
+ *   norm_eps     finite, >= 0 (read where there is a norm); squares are summed in
+ *                f32, so that a head whose squares pass its range becomes zeros
+ * Everything else as gqa_paged_append_t and nvfp4_paged_append_t.  q_norm and
+ * k_norm overlap nothing that is written.
+ */
+gqa_status gqa_paged_norm_append_t(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, gqa_tensor* k_pages,
+                                   gqa_tensor* v_pages, const gqa_tensor* block_table, const gqa_tensor* kv_lens,
+                                   const gqa_tensor* qo_indptr, const gqa_tensor* rope, const gqa_tensor* positions,
+                                   const gqa_tensor* q_norm, const gqa_tensor* k_norm, gqa_tensor* q_out, int interleaved,
+                                   float norm_eps, float k_scale, float v_scale, gqa_stream_t stream);
+gqa_status nvfp4_paged_norm_append_t(const gqa_tensor* q, const gqa_tensor* k, const gqa_tensor* v, gqa_tensor* k_fp4,
+                                     gqa_tensor* k_sf, gqa_tensor* v_fp4, gqa_tensor* v_sf, const gqa_tensor* block_table,
+                                     const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens, const gqa_tensor* rope,
+                                     const gqa_tensor* positions, const gqa_tensor* q_norm, const gqa_tensor* k_norm,
+                                     gqa_tensor* q_out, int interleaved, float norm_eps, float q_scale, gqa_stream_t stream);
+
+/*
  * gqa_paged_attn_t -- attention of one new token per sequence over a paged K/V
  * cache, split over the cache's length and joined:
  *
@@ -477,6 +509,82 @@ gqa_status gqa_paged_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, cons
 /* Bytes of workspace that gqa_paged_attn_t needs for a head layout, whatever the
  * batch and the lengths (0 for one that it does not take). */
 int64_t gqa_paged_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t d);
+
+/*
+ * gqa_paged_window_attn_t -- gqa_paged_attn_t whose sliding window leaves the
+ * first `sinks` tokens of a sequence visible: the sum runs over
+ *   t < min(sinks, len_b)  and  max(0, len_b - window) <= t < len_b,
+ * each token once.  sinks >= 0; without a window (0) every token is visible and
+ * sinks means nothing.  Only the block table's entries of pages that hold a
+ * visible token are read: those between the sinks and the window may be given
+ * back.  Workspace, errors and everything else as gqa_paged_attn_t, which is
+ * this with sinks = 0.
+ */
+gqa_status gqa_paged_window_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, const gqa_tensor* v_pages,
+                                   const gqa_tensor* block_table, const gqa_tensor* seq_lens, gqa_tensor* out,
+                                   gqa_tensor* lse, float q_scale, float k_scale, float v_scale, int window, int sinks,
+                                   float softcap, void* workspace, int64_t workspace_bytes, gqa_stream_t stream);
+
+/*
+ * gqa_tree_mask_t -- positions and visibility of trees of drafted tokens, once for
+ * all layers of a step.  The drafted tokens of a batch lie one sequence after the
+ * other; token i of sequence b is row t = qo_indptr[b] + i and, in the cache,
+ * behind base_b = kv_lens[b] - (qo_indptr[b+1] - qo_indptr[b]) tokens.
+ *   depth_i        = 0 if parents[t] is -1 (it follows the last cached token), else
+ *                    depth of token parents[t] of its sequence, plus 1
+ *   positions[t]   = base_b + depth_i
+ *   mask[t], bit j = token j of the sequence is i or above it, and, under a window
+ *                    (> 0), depth_i - depth_j < window or base_b + depth_j < sinks
+ *
+ *   parents    [total]  int32, each -1 or less than its token's own number
+ *   qo_indptr  [batch + 1], kv_lens [batch]  int32; the drafted tokens included
+ *   mask       [total, words]  int32, bit j % 32 of word j / 32; written
+ *   positions  [total]  int32, written
+ *   words      1 .. 32: trees of up to 32 * words tokens; batch 1 .. 2^20
+ *   window, sinks  >= 0, those of the attention
+ *
+ * A parent out of range counts as -1 and sets bit 1 of the error word; tokens from
+ * the 32 * words-th of a tree on are left alone and set it too.  A sequence whose
+ * offsets do not lie in order within [0, total] is left alone and sets bit 2, as
+ * does qo_indptr[0] != 0.  Rows behind qo_indptr[batch] are left as they are.
+ * Device tensors only; no workspace; one kernel.
+ */
+gqa_status gqa_tree_mask_t(const gqa_tensor* parents, const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens, gqa_tensor* mask,
+                           gqa_tensor* positions, int window, int sinks, gqa_stream_t stream);
+
+/*
+ * gqa_paged_keep_t -- compaction of a paged cache after verification: of each
+ * sequence's drafted tokens the accepted ones move together, behind its cached
+ * tokens, and the others are given up.  Drafted token kept[b, i] of sequence b
+ * (place base_b + kept[b, i] in the cache, base_b as above) goes to place
+ * base_b + i for 0 <= i < num_kept[b], and new_lens[b] = base_b + num_kept[b].
+ * Rows behind the new length are not cleared.
+ *
+ *   pages        1 to 4 tensors [num_pages, heads, page_size, w] or, for the pages
+ *                of several layers at once, [layers, num_pages, heads, page_size,
+ *                w] of any type; rows of a multiple of 8 bytes, strides multiples
+ *                of 8 bytes with a dense last dimension; num_pages and page_size
+ *                are common to all.  K and V pages, or the codes and scales of
+ *                NVFP4 ones.  Written; they overlap neither themselves (checked)
+ *                nor one another
+ *   block_table  [batch, max_pages_per_seq], qo_indptr [batch + 1], kv_lens
+ *                [batch]  int32, as for the step's append
+ *   kept         [batch, max_kept]  int32, rising; entries from num_kept[b] on are
+ *                not read
+ *   num_kept     [batch]  int32
+ *   new_lens     [batch]  int32, written; another tensor than kv_lens
+ *   batch        1 .. 65535
+ *
+ * A sequence whose kept tokens do not rise, or do not lie in its draft, or which is
+ * shorter than its draft, is left as it is (new_lens[b] = kv_lens[b]; bit 1 of the
+ * error word, or bit 2 where its offsets fall).  A row whose old or new place lies
+ * outside the block table or the pages stays where it is and sets bit 1.  Sequences
+ * that share a page must not both move rows in it.  Device tensors only; no
+ * workspace; one kernel; the same bits whatever the order.
+ */
+gqa_status gqa_paged_keep_t(const gqa_tensor* const* pages, int num_tensors, const gqa_tensor* block_table,
+                            const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens, const gqa_tensor* kept,
+                            const gqa_tensor* num_kept, gqa_tensor* new_lens, gqa_stream_t stream);
 
 /*
  * gqa_check_device_errors -- synchronise `device` and return (then clear)
