@@ -22,6 +22,9 @@ missing or fails to load, every call raises.
     gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=None, q_scale=1.0,
                    k_scale=1.0, v_scale=1.0, window=0, softcap=0.0, workspace=None, sinks=0)
     gqa_tree_mask(parents, qo_indptr, kv_lens, *, max_tokens=None, window=0, sinks=0, mask=None, positions=None)
+    gqa_paged_tree_attn(q, k_pages, v_pages, block_table, qo_indptr, kv_lens, *, mask=None, positions=None,
+                        out=None, lse=None, q_scale=1.0, k_scale=1.0, v_scale=1.0, window=0, sinks=0, softcap=0.0,
+                        workspace=None)
     gqa_paged_keep(pages, block_table, qo_indptr, kv_lens, kept, num_kept, *, new_lens=None)
 """
 from __future__ import annotations
@@ -39,7 +42,7 @@ __all__ = [
     "GqaError", "lib", "gqa_decode", "nvfp4_paged_ctx_attn", "gqa_debug_dequant_pages",
     "gqa_check_device_errors", "gqa_release_workspace", "gqa_decode_plan", "gqa_ctx_plan", "gqa_decode_paged", "gqa_debug_wait_expiry", "gqa_decode_noalloc", "gqa_debug_starve_producers", "gqa_set_schedule", "gqa_set_ctx_grid", "LIB_PATH",
     "build", "gqa_paged_append", "nvfp4_paged_append", "gqa_paged_attn", "gqa_paged_attn_workspace",
-    "gqa_tree_mask", "gqa_paged_keep",
+    "gqa_tree_mask", "gqa_paged_tree_attn", "gqa_paged_tree_attn_workspace", "gqa_paged_keep",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -157,6 +160,10 @@ def lib() -> ctypes.CDLL:
             L.gqa_tree_mask_t.restype = c.c_int
             L.gqa_paged_keep_t.argtypes = [c.POINTER(tp), c.c_int] + [tp] * 6 + [vp]
             L.gqa_paged_keep_t.restype = c.c_int
+            L.gqa_paged_tree_attn_t.argtypes = [tp] * 10 + [f32, f32, f32, c.c_int, c.c_int, f32, vp, i64, vp]
+            L.gqa_paged_tree_attn_t.restype = c.c_int
+            L.gqa_paged_tree_attn_workspace.argtypes = [i64, i64, i64]
+            L.gqa_paged_tree_attn_workspace.restype = i64
             L.gqa_paged_attn_workspace.argtypes = [i64, i64, i64]
             L.gqa_paged_attn_workspace.restype = i64
             L.gqa_release_workspace.argtypes = []
@@ -282,7 +289,7 @@ def _binding():
                         tuple(ctypes.cast(f, ctypes.c_void_p).value
                               for f in (L.gqa_paged_append_t, L.nvfp4_paged_append_t, L.gqa_paged_window_attn_t,
                                         L.gqa_paged_norm_append_t, L.nvfp4_paged_norm_append_t, L.gqa_tree_mask_t,
-                                        L.gqa_paged_keep_t)))
+                                        L.gqa_paged_keep_t, L.gqa_paged_tree_attn_t)))
                 _binding_module = m
     return _binding_module
 
@@ -398,6 +405,40 @@ def gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=
         workspace = torch.empty(gqa_paged_attn_workspace(q.shape[1], k_pages.shape[1], q.shape[2]), dtype=torch.uint8,
                                 device=q.device)
         st = call(q, k_pages, v_pages, block_table, seq_lens, out, lse, workspace, *args)
+    if st:
+        _check(st)
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def gqa_paged_tree_attn_workspace(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace of a gqa_paged_tree_attn call, whatever its batch, tokens and lengths."""
+    return int(lib().gqa_paged_tree_attn_workspace(int(q_heads), int(kv_heads), int(head_dim)))
+
+
+def gqa_paged_tree_attn(q, k_pages, v_pages, block_table, qo_indptr, kv_lens, *, mask=None, positions=None, out=None, lse=None,
+                        q_scale: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0, window: int = 0, sinks: int = 0,
+                        softcap: float = 0.0, workspace=None):
+    """Attention of several new tokens per sequence over a paged cache that
+    holds them already (see include/gqa.h): drafted tokens in trees, whose
+    mask [T,words] and positions [T] int32 gqa_tree_mask makes, or, without a
+    mask, in chains.  q [T,Hq,D] f16 or bf16, k_pages / v_pages
+    [num_pages,Hkv,page_size,D] of q's type or E4M3, in any order in memory,
+    block_table [B,max_pages_per_seq], qo_indptr [B+1] and kv_lens [B] (the
+    new tokens included) int32.  Under a window the first `sinks` tokens stay
+    visible.  Writes `lse` [T,Hq] f32 if given.  The workspace is the
+    library's for the stream (in a captured call: one from the graph's memory
+    pool) unless one of at least gqa_paged_tree_attn_workspace(Hq, Hkv, D)
+    bytes (uint8) is given; calls that can run at the same time need one each."""
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    args = (q_scale, k_scale, v_scale, window, sinks, softcap)
+    call = _binding().tree_attn
+    st = call(q, k_pages, v_pages, block_table, qo_indptr, kv_lens, mask, positions, out, lse, workspace, *args)
+    if st == _ERR_WORKSPACE:  # being captured: one from the graph's memory pool
+        workspace = torch.empty(gqa_paged_tree_attn_workspace(q.shape[1], k_pages.shape[1], q.shape[2]), dtype=torch.uint8,
+                                device=q.device)
+        st = call(q, k_pages, v_pages, block_table, qo_indptr, kv_lens, mask, positions, out, lse, workspace, *args)
     if st:
         _check(st)
     return out

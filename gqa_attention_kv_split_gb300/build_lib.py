@@ -27,7 +27,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cpp", "api_paged.cpp", "decode.cu", "ctx_nvfp4.cu", "ctx_study.cu", "append.cu", "append_norm.cu", "drafts.cu",
            "paged_attn.cpp", "paged_attn_f16.cu", "paged_attn_bf16.cu", "paged_attn_e4m3.cu", "paged_attn_sinks_f16.cu",
-           "paged_attn_sinks_bf16.cu", "paged_attn_sinks_e4m3.cu"]
+           "paged_attn_sinks_bf16.cu", "paged_attn_sinks_e4m3.cu", "tree_attn.cpp", "tree_attn_f16.cu", "tree_attn_bf16.cu",
+           "tree_attn_e4m3.cu", "tree_attn_e4m3_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I", CSRC, "-I", INCLUDE]

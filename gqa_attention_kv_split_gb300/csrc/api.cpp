@@ -424,14 +424,15 @@ gqa_status gqa_check_device_errors(int device, uint32_t* word) {
   *word = 0;
   ScopedDevice sd(device);
   if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", device);
-  uint32_t a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0;
   GQA_CUDA_TRY(gqa::decode_read_errors(&a), "read decode error word");
   GQA_CUDA_TRY(gqa::ctx_read_errors(&b), "read ctx error word");
   GQA_CUDA_TRY(gqa::ctx_study_read_errors(&c), "read ctx study error word");
   GQA_CUDA_TRY(gqa::append_read_errors(&d), "read append error word");
   GQA_CUDA_TRY(gqa::paged_attn_read_errors(&f), "read paged attention error word");
   GQA_CUDA_TRY(gqa::drafts_read_errors(&g), "read drafted tokens' error word");
-  *word = a | b | c | d | f | g;
+  GQA_CUDA_TRY(gqa::tree_attn_read_errors(&h), "read tree attention error word");
+  *word = a | b | c | d | f | g | h;
   if (*word & 1u) return fail(GQA_ERR_TIMEOUT, "a kernel's bounded wait expired (error word 0x%x)", *word);
   if (*word)
     return fail(GQA_ERR_INVALID_ARG,
@@ -500,7 +501,7 @@ gqa_status gqa_release_workspace(void) {
   std::lock_guard<std::mutex> lk(g_ws_mu);
   int prev = -1;
   cudaGetDevice(&prev);
-  for (WorkspaceMap* map : {&g_ws, &g_paged_ws}) {
+  for (WorkspaceMap* map : {&g_ws, &g_paged_ws, &g_tree_ws}) {
     for (auto& kv : *map) {
       if (kv.second.ptr) {
         cudaSetDevice(std::get<0>(kv.first));

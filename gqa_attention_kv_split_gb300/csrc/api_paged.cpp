@@ -267,6 +267,78 @@ gqa_status nvfp4_append_impl(const gqa_tensor* q, const gqa_tensor* k, const gqa
   return run_append(a, ts, "nvfp4_paged_append", stream);
 }
 
+// The library's workspace of an attention for a stream, of the most that any call needs (so
+// that it never moves); refused for a call that is being captured, which needs `need`.
+gqa_status own_workspace(int device, cudaStream_t s, size_t most, int64_t need, WorkspaceMap& map, void** out) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  GQA_CUDA_TRY(cudaStreamIsCapturing(s, &capture), "cudaStreamIsCapturing");
+  if (capture != cudaStreamCaptureStatusNone)
+    return fail(GQA_ERR_WORKSPACE, "a captured call needs a workspace of its own (%lld bytes)", (long long)need);
+  if (s == cudaStreamPerThread) {
+    static thread_local ThreadEnd end;
+    end.thread = gqa::thread_number();
+  }
+  // (allocated without disturbing a capture of another thread)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  GQA_CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode), "cudaThreadExchangeStreamCaptureMode");
+  const gqa_status st = workspace(device, s, most, out, map);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return st;
+}
+
+// What the two attentions share: queries [rows, hq, d] over pages, the table of `batch` sequences.
+struct AttnSizes {
+  int64_t rows, hq, d, num_pages, hkv, page_size, max_pages;
+  bool e4m3;
+};
+gqa_status check_attn(const gqa_tensor* q, const gqa_tensor* k_pages, const gqa_tensor* v_pages, const gqa_tensor* block_table,
+                      int64_t batch, const gqa_tensor* out, const gqa_tensor* lse, AttnSizes* z) {
+  int64_t qs[3], ps[4], bs[2];
+  GQA_TRY(check_strided(q, "q", {GQA_F16, GQA_BF16}, {-1, -1, -1}, false, qs));
+  GQA_TRY(check_strided(k_pages, "k_pages", {q->dtype, GQA_E4M3, GQA_U8}, {-1, -1, -1, qs[2]}, true, ps));
+  const bool e4m3 = k_pages->dtype != q->dtype;
+  GQA_TRY(e4m3 ? check_strided(v_pages, "v_pages", {GQA_E4M3, GQA_U8}, {ps[0], ps[1], ps[2], qs[2]}, true)
+               : check_strided(v_pages, "v_pages", {q->dtype}, {ps[0], ps[1], ps[2], qs[2]}, true));
+  GQA_TRY(check_desc(block_table, "block_table", {GQA_I32}, {batch < 0 ? qs[0] : batch, -1}, bs));
+  gqa_tensor o = *out, l;
+  if (!o.data && qs[0] == 0) o.data = &o;  // (an empty tensor may have no data)
+  GQA_TRY(check_desc(&o, "out", {q->dtype}, {qs[0], qs[1], qs[2]}));
+  if (lse) {
+    l = *lse;
+    if (!l.data && qs[0] == 0) l.data = &l;
+    GQA_TRY(check_desc(&l, "lse", {GQA_F32}, {qs[0], qs[1]}));
+  }
+  *z = {qs[0], qs[1], qs[2], ps[0], ps[1], ps[2], bs[1], e4m3};
+  return GQA_OK;
+}
+gqa_status check_layout(const AttnSizes& z) {
+  if (z.d != 64 && z.d != 128 && z.d != 256)
+    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "head dim %lld is not 64, 128 or 256", (long long)z.d);
+  if (z.hkv < 1 || z.hq < 1 || z.hq > 1024 || z.hq % z.hkv != 0)
+    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld query heads over %lld KV heads: 1 to 1024, a multiple, are taken",
+                (long long)z.hq, (long long)z.hkv);
+  if (z.page_size != 16 && z.page_size != 32 && z.page_size != 64 && z.page_size != 128 && z.page_size != 256)
+    return fail(GQA_ERR_UNSUPPORTED_SHAPE, "page size %lld is not 16, 32, 64, 128 or 256", (long long)z.page_size);
+  if (z.num_pages < 1 || z.num_pages > 2147483647LL)
+    return fail(GQA_ERR_INVALID_ARG, "num_pages %lld out of range", (long long)z.num_pages);
+  if (z.max_pages < 1 || z.max_pages > (int64_t(1) << 30) / z.page_size)
+    return fail(GQA_ERR_INVALID_ARG, "max_pages_per_seq %lld out of range", (long long)z.max_pages);
+  return GQA_OK;
+}
+gqa_status check_numbers(float q_scale, float k_scale, float v_scale, int window, int sinks, float softcap) {
+  if (!std::isfinite(q_scale)) return fail(GQA_ERR_INVALID_ARG, "q_scale is not finite");
+  GQA_TRY(check_scale(k_scale, "k_scale"));
+  GQA_TRY(check_scale(v_scale, "v_scale"));
+  if (window < 0) return fail(GQA_ERR_INVALID_ARG, "window %d is negative", window);
+  if (sinks < 0) return fail(GQA_ERR_INVALID_ARG, "sinks %d is negative", sinks);
+  if (!std::isfinite(softcap) || softcap < 0.f) return fail(GQA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  return GQA_OK;
+}
+int cache_type(const gqa_tensor* q, bool e4m3) {
+  const bool bf16 = q->dtype == GQA_BF16;
+  return e4m3 ? (bf16 ? gqa::kCacheE4m3 : gqa::kCacheE4m3F16) : bf16 ? gqa::kCacheBf16 : gqa::kCacheF16;
+}
+
 }  // namespace
 
 extern "C" {
@@ -331,38 +403,18 @@ gqa_status gqa_paged_window_attn_t(const gqa_tensor* q, const gqa_tensor* k_page
                                    float q_scale, float k_scale, float v_scale, int window, int sinks, float softcap, void* workspace_,
                                    int64_t workspace_bytes, gqa_stream_t stream) {
   return guarded([&]() -> gqa_status {
-    int64_t qs[3], ps[4], bs[2];
-    GQA_TRY(check_strided(q, "q", {GQA_F16, GQA_BF16}, {-1, -1, -1}, false, qs));
-    GQA_TRY(check_strided(k_pages, "k_pages", {q->dtype, GQA_E4M3, GQA_U8}, {-1, -1, -1, qs[2]}, true, ps));
-    const bool e4m3 = k_pages->dtype != q->dtype;
-    GQA_TRY(e4m3 ? check_strided(v_pages, "v_pages", {GQA_E4M3, GQA_U8}, {ps[0], ps[1], ps[2], qs[2]}, true)
-                 : check_strided(v_pages, "v_pages", {q->dtype}, {ps[0], ps[1], ps[2], qs[2]}, true));
-    GQA_TRY(check_desc(seq_lens, "seq_lens", {GQA_I32}, {qs[0]}));
-    GQA_TRY(check_desc(block_table, "block_table", {GQA_I32}, {qs[0], -1}, bs));
-    GQA_TRY(check_desc(out, "out", {q->dtype}, {qs[0], qs[1], qs[2]}));
-    if (lse) GQA_TRY(check_desc(lse, "lse", {GQA_F32}, {qs[0], qs[1]}));
-    if (qs[0] < 1 || qs[0] > 65535) return fail(GQA_ERR_UNSUPPORTED, "batch %lld outside [1, 65535]", (long long)qs[0]);
-    if (qs[2] != 64 && qs[2] != 128 && qs[2] != 256)
-      return fail(GQA_ERR_UNSUPPORTED_SHAPE, "head dim %lld is not 64, 128 or 256", (long long)qs[2]);
-    if (ps[1] < 1 || qs[1] < 1 || qs[1] > 1024 || qs[1] % ps[1] != 0)
-      return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld query heads over %lld KV heads: 1 to 1024, a multiple, are taken",
-                  (long long)qs[1], (long long)ps[1]);
-    if (ps[2] != 16 && ps[2] != 32 && ps[2] != 64 && ps[2] != 128 && ps[2] != 256)
-      return fail(GQA_ERR_UNSUPPORTED_SHAPE, "page size %lld is not 16, 32, 64, 128 or 256", (long long)ps[2]);
-    if (ps[0] < 1 || ps[0] > 2147483647LL) return fail(GQA_ERR_INVALID_ARG, "num_pages %lld out of range", (long long)ps[0]);
-    if (bs[1] < 1 || bs[1] > (int64_t(1) << 30) / ps[2])
-      return fail(GQA_ERR_INVALID_ARG, "max_pages_per_seq %lld out of range", (long long)bs[1]);
+    AttnSizes z;
+    if (!q || !k_pages || !out) return fail(GQA_ERR_INVALID_ARG, "q, k_pages or out: null descriptor");
+    GQA_TRY(check_attn(q, k_pages, v_pages, block_table, -1, out, lse, &z));
+    GQA_TRY(check_desc(seq_lens, "seq_lens", {GQA_I32}, {z.rows}));
+    if (z.rows < 1 || z.rows > 65535) return fail(GQA_ERR_UNSUPPORTED, "batch %lld outside [1, 65535]", (long long)z.rows);
+    GQA_TRY(check_layout(z));
     // (a block of the kernel counts the work of its share, in tiles of 32 tokens at least, in 31 bits)
-    if (qs[0] * ps[1] * ((qs[1] / ps[1] + 7) / 8) > (int64_t(1) << 38) / (bs[1] * ps[2] / 32 + 16))
-      return fail(GQA_ERR_UNSUPPORTED, "batch %lld x %lld KV heads x %lld tokens of capacity are too many", (long long)qs[0],
-                  (long long)ps[1], (long long)(bs[1] * ps[2]));
-    if (!std::isfinite(q_scale)) return fail(GQA_ERR_INVALID_ARG, "q_scale is not finite");
-    GQA_TRY(check_scale(k_scale, "k_scale"));
-    GQA_TRY(check_scale(v_scale, "v_scale"));
-    if (window < 0) return fail(GQA_ERR_INVALID_ARG, "window %d is negative", window);
-    if (sinks < 0) return fail(GQA_ERR_INVALID_ARG, "sinks %d is negative", sinks);
-    if (!std::isfinite(softcap) || softcap < 0.f) return fail(GQA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
-    const int64_t need = gqa_paged_attn_workspace(qs[1], ps[1], qs[2]);
+    if (z.rows * z.hkv * ((z.hq / z.hkv + 7) / 8) > (int64_t(1) << 38) / (z.max_pages * z.page_size / 32 + 16))
+      return fail(GQA_ERR_UNSUPPORTED, "batch %lld x %lld KV heads x %lld tokens of capacity are too many", (long long)z.rows,
+                  (long long)z.hkv, (long long)(z.max_pages * z.page_size));
+    GQA_TRY(check_numbers(q_scale, k_scale, v_scale, window, sinks, softcap));
+    const int64_t need = gqa_paged_attn_workspace(z.hq, z.hkv, z.d);
     if (workspace_ && workspace_bytes < need)
       return fail(GQA_ERR_INVALID_ARG, "workspace of %lld bytes; %lld are needed", (long long)workspace_bytes, (long long)need);
     gqa_tensor ws = *q;  // the workspace's place is checked with the tensors'
@@ -394,16 +446,15 @@ gqa_status gqa_paged_window_attn_t(const gqa_tensor* q, const gqa_tensor* k_page
     a.vp_page = v_pages->strides[0];
     a.vp_head = v_pages->strides[1];
     a.vp_slot = v_pages->strides[2];
-    a.batch = qs[0];
-    a.num_pages = ps[0];
-    a.max_pages_per_seq = bs[1];
-    a.hq = (int)qs[1];
-    a.hkv = (int)ps[1];
-    a.d = (int)qs[2];
-    a.page_size = (int)ps[2];
-    const bool bf16 = q->dtype == GQA_BF16;
-    a.cache = e4m3 ? (bf16 ? gqa::kCacheE4m3 : gqa::kCacheE4m3F16) : bf16 ? gqa::kCacheBf16 : gqa::kCacheF16;
-    a.scale = (float)((double)q_scale * k_scale / std::sqrt((double)qs[2]));
+    a.batch = z.rows;
+    a.num_pages = z.num_pages;
+    a.max_pages_per_seq = z.max_pages;
+    a.hq = (int)z.hq;
+    a.hkv = (int)z.hkv;
+    a.d = (int)z.d;
+    a.page_size = (int)z.page_size;
+    a.cache = cache_type(q, z.e4m3);
+    a.scale = (float)((double)q_scale * k_scale / std::sqrt((double)z.d));
     a.v_scale = v_scale;
     a.softcap = softcap;
     a.window = window;
@@ -417,23 +468,7 @@ gqa_status gqa_paged_window_attn_t(const gqa_tensor* q, const gqa_tensor* k_page
     // A call's two kernels follow each other on the stream: another thread's call on the
     // same stream, and so with the same workspace, must not come between them.
     std::lock_guard<std::mutex> lk(g_paged_launch_mu);
-    if (!workspace_) {
-      cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-      GQA_CUDA_TRY(cudaStreamIsCapturing(s, &capture), "cudaStreamIsCapturing");
-      if (capture != cudaStreamCaptureStatusNone)
-        return fail(GQA_ERR_WORKSPACE, "a captured call needs a workspace of its own (%lld bytes)", (long long)need);
-      if (s == cudaStreamPerThread) {
-        static thread_local ThreadEnd end;
-        end.thread = gqa::thread_number();
-      }
-      // As much as the largest head layout needs, so that it never moves; and allocated
-      // without disturbing a capture of another thread.
-      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-      GQA_CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode), "cudaThreadExchangeStreamCaptureMode");
-      const gqa_status st = workspace(where.device, s, gqa::paged_attn_workspace_bytes(1024, 1, 256), &workspace_, g_paged_ws);
-      cudaThreadExchangeStreamCaptureMode(&mode);
-      GQA_TRY(st);
-    }
+    if (!workspace_) GQA_TRY(own_workspace(where.device, s, gqa::paged_attn_workspace_bytes(1024, 1, 256), need, g_paged_ws, &workspace_));
     GQA_CUDA_TRY(gqa::launch_paged_attn(a, workspace_, s), "paged attention launch");
     return GQA_OK;
   });
@@ -560,6 +595,113 @@ gqa_status gqa_paged_keep_t(const gqa_tensor* const* pages, int num_tensors, con
     ScopedDevice sd(where.device);
     if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", where.device);
     GQA_CUDA_TRY(gqa::launch_keep(a, reinterpret_cast<cudaStream_t>(stream)), "keep launch");
+    return GQA_OK;
+  });
+}
+
+int64_t gqa_paged_tree_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t d) {
+  if (kv_heads < 1 || q_heads < 1 || q_heads > 1024 || q_heads % kv_heads != 0 || (d != 64 && d != 128 && d != 256)) return 0;
+  return (int64_t)gqa::tree_attn_workspace_bytes((int)d);
+}
+
+gqa_status gqa_paged_tree_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, const gqa_tensor* v_pages,
+                                 const gqa_tensor* block_table, const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens,
+                                 const gqa_tensor* mask, const gqa_tensor* positions, gqa_tensor* out, gqa_tensor* lse,
+                                 float q_scale, float k_scale, float v_scale, int window, int sinks, float softcap,
+                                 void* workspace_, int64_t workspace_bytes, gqa_stream_t stream) {
+  return guarded([&]() -> gqa_status {
+    AttnSizes z;
+    int64_t ls[1], ms[2] = {0, 0};
+    if (!q || !k_pages || !out) return fail(GQA_ERR_INVALID_ARG, "q, k_pages or out: null descriptor");
+    GQA_TRY(check_desc(kv_lens, "kv_lens", {GQA_I32}, {-1}, ls));
+    if (ls[0] < 1 || ls[0] > 65535) return fail(GQA_ERR_UNSUPPORTED, "batch %lld outside [1, 65535]", (long long)ls[0]);
+    GQA_TRY(check_desc(qo_indptr, "qo_indptr", {GQA_I32}, {ls[0] + 1}));
+    GQA_TRY(check_attn(q, k_pages, v_pages, block_table, ls[0], out, lse, &z));
+    if (mask) {
+      gqa_tensor m = *mask;
+      if (!m.data && z.rows == 0) m.data = &m;
+      GQA_TRY(check_desc(&m, "mask", {GQA_I32}, {z.rows, -1}, ms));
+      if (ms[1] < 1 || ms[1] > gqa::kMaxTreeTokens / 32)
+        return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld words of bits: 1 to %d are taken", (long long)ms[1], gqa::kMaxTreeTokens / 32);
+      if (window > 0 && !positions) return fail(GQA_ERR_INVALID_ARG, "a window over a tree needs the tokens' positions");
+    }
+    if (positions) {
+      gqa_tensor x = *positions;
+      if (!x.data && z.rows == 0) x.data = &x;
+      GQA_TRY(check_desc(&x, "positions", {GQA_I32}, {z.rows}));
+    }
+    GQA_TRY(check_layout(z));
+    GQA_TRY(check_numbers(q_scale, k_scale, v_scale, window, sinks, softcap));
+    const int64_t group = z.hq / z.hkv, tiles = z.max_pages * z.page_size / 64 + 16;
+    if (z.rows * group > 2147483647LL) return fail(GQA_ERR_UNSUPPORTED, "%lld tokens of %lld heads are too many", (long long)z.rows, (long long)group);
+    // (a block of the kernel counts the work of its share, in tiles of 64 tokens at least, in 31 bits)
+    if (z.hkv * (ls[0] + z.rows * group / 128) > (int64_t(1) << 38) / tiles)
+      return fail(GQA_ERR_UNSUPPORTED, "%lld sequences, %lld tokens x %lld KV heads x %lld tokens of capacity are too many",
+                  (long long)ls[0], (long long)z.rows, (long long)z.hkv, (long long)(z.max_pages * z.page_size));
+    const float scale = (float)((double)q_scale * k_scale / std::sqrt((double)z.d));
+    if (!std::isfinite(scale) || (softcap > 0.f && !std::isfinite((float)(4.0 * scale / softcap))))
+      return fail(GQA_ERR_INVALID_ARG, "q_scale * k_scale (over softcap) is out of range");
+    const int64_t need = gqa_paged_tree_attn_workspace(z.hq, z.hkv, z.d);
+    if (workspace_ && workspace_bytes < need)
+      return fail(GQA_ERR_INVALID_ARG, "workspace of %lld bytes; %lld are needed", (long long)workspace_bytes, (long long)need);
+    if (z.rows == 0) return GQA_OK;
+    gqa_tensor ws = *q;  // the workspace's place is checked with the tensors'
+    ws.data = workspace_;
+    std::vector<Named> ts = {{q, "q"}, {k_pages, "k_pages"}, {v_pages, "v_pages"}, {block_table, "block_table"},
+                             {qo_indptr, "qo_indptr"}, {kv_lens, "kv_lens"}, {out, "out"}};
+    if (workspace_) ts.push_back({&ws, "workspace"});
+    if (mask) ts.push_back({mask, "mask"});
+    if (positions) ts.push_back({positions, "positions"});
+    gqa_tensor l;
+    if (lse) {
+      l = *lse;
+      l.dtype = GQA_I32;  // (4-byte alignment)
+      ts.push_back({&l, "lse"});
+    }
+    Where where;
+    GQA_TRY(locate_tensors(ts, "gqa_paged_tree_attn", &where));
+    gqa::TreeAttnArgs a{};
+    a.q = q->data;
+    a.out = out->data;
+    a.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+    a.k_pages = k_pages->data;
+    a.v_pages = v_pages->data;
+    a.block_table = static_cast<const int32_t*>(block_table->data);
+    a.indptr = static_cast<const int32_t*>(qo_indptr->data);
+    a.kv_lens = static_cast<const int32_t*>(kv_lens->data);
+    a.mask = mask ? static_cast<const int32_t*>(mask->data) : nullptr;
+    a.positions = positions ? static_cast<const int32_t*>(positions->data) : nullptr;
+    a.q_tok = stride_of(q, 0);
+    a.q_head = stride_of(q, 1);
+    a.kp_page = k_pages->strides[0];
+    a.kp_head = k_pages->strides[1];
+    a.kp_slot = k_pages->strides[2];
+    a.vp_page = v_pages->strides[0];
+    a.vp_head = v_pages->strides[1];
+    a.vp_slot = v_pages->strides[2];
+    a.total = z.rows;
+    a.batch = ls[0];
+    a.num_pages = z.num_pages;
+    a.max_pages_per_seq = z.max_pages;
+    a.hq = (int)z.hq;
+    a.hkv = (int)z.hkv;
+    a.d = (int)z.d;
+    a.page_size = (int)z.page_size;
+    a.words = (int)ms[1];
+    a.cache = cache_type(q, z.e4m3);
+    a.scale = scale;
+    a.v_scale = v_scale;
+    a.softcap = softcap;
+    a.window = window;
+    a.sinks = sinks;
+    a.starve = gqa::starve_producers();
+    ScopedDevice sd(where.device);
+    if (!sd.ok()) return fail(GQA_ERR_CUDA, "cannot switch to device %d", where.device);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // (two kernels that share a workspace, as the one-token attention's)
+    std::lock_guard<std::mutex> lk(g_paged_launch_mu);
+    if (!workspace_) GQA_TRY(own_workspace(where.device, s, gqa::tree_attn_workspace_bytes(256), need, g_tree_ws, &workspace_));
+    GQA_CUDA_TRY(gqa::launch_tree_attn(a, workspace_, s), "tree attention launch");
     return GQA_OK;
   });
 }

@@ -135,6 +135,8 @@ inline WorkspaceMap g_ws;
 // Of gqa_paged_attn_t's calls without a workspace (a map of their own: growing one
 // never moves the other, which a captured call may have been given).
 inline WorkspaceMap g_paged_ws;
+// Of gqa_paged_tree_attn_t's.
+inline WorkspaceMap g_tree_ws;
 inline std::mutex g_paged_launch_mu;
 
 inline gqa_status workspace(int dev, cudaStream_t stream, size_t bytes, void** out, WorkspaceMap& map = g_ws) {
@@ -170,7 +172,7 @@ inline gqa_status workspace(int dev, cudaStream_t stream, size_t bytes, void** o
   return GQA_OK;
 }
 
-// Gives back a thread's g_paged_ws buffers when it ends: its per-thread stream ends with it.
+// Gives back a thread's g_paged_ws and g_tree_ws buffers when it ends: its per-thread stream ends with it.
 // (g_ws's stay until gqa_release_workspace: a captured call may have been given one.)
 struct ThreadEnd {
   uint64_t thread = 0;
@@ -181,16 +183,17 @@ struct ThreadEnd {
     cudaGetDevice(&prev);
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // (leaves a capture of another thread alone)
     cudaThreadExchangeStreamCaptureMode(&mode);
-    for (auto it = g_paged_ws.begin(); it != g_paged_ws.end();) {
-      if (std::get<2>(it->first) != thread) {
-        ++it;
-        continue;
+    for (WorkspaceMap* map : {&g_paged_ws, &g_tree_ws})
+      for (auto it = map->begin(); it != map->end();) {
+        if (std::get<2>(it->first) != thread) {
+          ++it;
+          continue;
+        }
+        cudaSetDevice(std::get<0>(it->first));
+        cudaStreamSynchronize(cudaStreamPerThread);
+        cudaFree(it->second.ptr);
+        it = map->erase(it);
       }
-      cudaSetDevice(std::get<0>(it->first));
-      cudaStreamSynchronize(cudaStreamPerThread);
-      cudaFree(it->second.ptr);
-      it = g_paged_ws.erase(it);
-    }
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (prev >= 0) cudaSetDevice(prev);
   }

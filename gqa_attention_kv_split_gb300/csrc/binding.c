@@ -26,8 +26,10 @@ static __typeof__(&gqa_paged_norm_append_t) g_norm_append;
 static __typeof__(&nvfp4_paged_norm_append_t) g_nvfp4_norm_append;
 static __typeof__(&gqa_tree_mask_t) g_tree_mask;
 static __typeof__(&gqa_paged_keep_t) g_keep;
+static __typeof__(&gqa_paged_tree_attn_t) g_tree_attn;
 static void** const g_entries[] = {(void**)&g_append,           (void**)&g_nvfp4_append, (void**)&g_attn, (void**)&g_norm_append,
-                                   (void**)&g_nvfp4_norm_append, (void**)&g_tree_mask,    (void**)&g_keep};
+                                   (void**)&g_nvfp4_norm_append, (void**)&g_tree_mask,    (void**)&g_keep,
+                                   (void**)&g_tree_attn};
 enum { kEntries = sizeof(g_entries) / sizeof(g_entries[0]) };
 /* torch.Tensor's own descriptors, looked up once: methods and attributes */
 static PyObject *m_data_ptr, *m_get_device, *m_stride, *a_dtype, *a_shape;
@@ -236,6 +238,30 @@ static PyObject* py_tree_mask(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   return PyLong_FromLong(st);
 }
 
+/* tree_attn(q, k_pages, v_pages, block_table, qo_indptr, kv_lens, mask, positions, out, lse, workspace, q_scale, k_scale,
+ * v_scale, window, sinks, softcap) -> status */
+static PyObject* py_tree_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const char* const names[11] = {"q",    "k_pages",   "v_pages", "block_table", "qo_indptr", "kv_lens",
+                                        "mask", "positions", "out",     "lse",         "workspace"};
+  gqa_tensor d[11];
+  gqa_tensor* r[11];
+  float qs, ks, vs, cap;
+  int window, sinks;
+  gqa_stream_t stream;
+  void* ws;
+  int64_t bytes;
+  (void)self;
+  if (expect(n, 17) || fill_all(a, names, 11, d, r)) return NULL;
+  if (as_float(a[11], &qs) || as_float(a[12], &ks) || as_float(a[13], &vs) || as_int(a[14], &window) || as_int(a[15], &sinks) ||
+      as_float(a[16], &cap) || stream_of(r[0], &stream) || workspace_of(r[10], &ws, &bytes))
+    return NULL;
+  gqa_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_tree_attn(r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], qs, ks, vs, window, sinks, cap, ws, bytes, stream);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
 /* keep((pages, ...), block_table, qo_indptr, kv_lens, kept, num_kept, new_lens) -> status */
 static PyObject* py_keep(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   static const char* const names[6] = {"block_table", "qo_indptr", "kv_lens", "kept", "num_kept", "new_lens"};
@@ -308,6 +334,7 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"nvfp4_append", (PyCFunction)(void (*)(void))py_nvfp4_append, METH_FASTCALL, NULL},
                                 {"attn", (PyCFunction)(void (*)(void))py_attn, METH_FASTCALL, NULL},
                                 {"tree_mask", (PyCFunction)(void (*)(void))py_tree_mask, METH_FASTCALL, NULL},
+                                {"tree_attn", (PyCFunction)(void (*)(void))py_tree_attn, METH_FASTCALL, NULL},
                                 {"keep", (PyCFunction)(void (*)(void))py_keep, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 

@@ -110,4 +110,32 @@ size_t paged_attn_workspace_bytes(int hq, int hkv, int d);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t paged_attn_read_errors(uint32_t* word);
 
+// ---- attention of several new tokens per sequence over a paged cache ---------
+
+struct TreeAttnArgs {
+  const void* q;               // [total, hq, d] f16 or bf16
+  void* out;                   // [total, hq, d], q's type, dense
+  float* lse;                  // [total, hq] or null
+  const void *k_pages, *v_pages;
+  const int32_t* block_table;  // [batch, max_pages_per_seq]
+  const int32_t* indptr;       // [batch + 1]
+  const int32_t* kv_lens;      // [batch], the new tokens included
+  const int32_t* mask;         // [total, words], or null: chains
+  const int32_t* positions;    // [total], or null
+  int64_t q_tok, q_head;       // elements
+  int64_t kp_page, kp_head, kp_slot, vp_page, vp_head, vp_slot;  // elements
+  int64_t total, batch, num_pages, max_pages_per_seq;
+  int hq, hkv, d, page_size, words;
+  int cache;                   // a CacheType
+  float scale, v_scale;        // of the scores (q_scale * k_scale / sqrt(d)) and of the output
+  float softcap;               // 0: none
+  int window, sinks;           // 0: none
+  int starve;
+};
+
+// Bytes of scratch of a call (a bound that depends on the head dim alone).
+size_t tree_attn_workspace_bytes(int d);
+cudaError_t launch_tree_attn(const TreeAttnArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t tree_attn_read_errors(uint32_t* word);
+
 }  // namespace gqa

@@ -1,36 +1,22 @@
 // paged_attn.cpp -- host side of the one-token paged attention: tensor maps,
 // workspace layout, choice of the instance.
-#include <cuda.h>  // CUtensorMap and the cuTensorMapEncodeTiled prototype (resolved at run time)
-
 #include <algorithm>
 #include <cmath>
 #include <limits>
-#include <mutex>
 
+#include "page_map.h"
 #include "paged_attn_host.h"
 
 namespace gqa {
 namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-std::once_flag g_encode_once;
-EncodeTiledFn g_encode = nullptr;
 
 // Tensor map over pages [num_pages, hkv, page_size, d] of any order in memory: a row
 // of d elements is cut into chunks of at most 128 bytes, and a copy takes `box`
 // tokens of one head of one page, chunk after chunk, swizzled.
 cudaError_t make_map(const void* pages, const PagedAttnArgs& a, int64_t s_page, int64_t s_head, int64_t s_slot, int box,
                      CUtensorMap* map) {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
-        qr == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-  });
-  if (!g_encode) return cudaErrorNotSupported;
+  const EncodeTiledFn encode = encode_tiled();
+  if (!encode) return cudaErrorNotSupported;
   const int64_t esz = a.cache >= kCacheE4m3 ? 1 : 2;
   const int64_t row = a.d * esz, chunk = row < 128 ? row : 128;
   const cuuint64_t dims[5] = {(cuuint64_t)chunk, (cuuint64_t)a.page_size, (cuuint64_t)(row / chunk), (cuuint64_t)a.hkv,
@@ -40,8 +26,8 @@ cudaError_t make_map(const void* pages, const PagedAttnArgs& a, int64_t s_page, 
                                  (cuuint64_t)(a.hkv > 1 ? s_head * esz : row), (cuuint64_t)(a.num_pages > 1 ? s_page * esz : row)};
   const cuuint32_t boxes[5] = {(cuuint32_t)chunk, (cuuint32_t)box, (cuuint32_t)(row / chunk), 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(pages), dims, strides, boxes, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(pages), dims, strides, boxes, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
                               chunk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                               // (rows of one head apart: what lies behind 128 bytes may be another head's)
                               s_slot == a.d ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,

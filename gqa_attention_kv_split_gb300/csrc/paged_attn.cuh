@@ -56,6 +56,7 @@
 
 #include "common.cuh"
 #include "paged_attn_host.h"
+#include "softcap.cuh"
 
 namespace gqa {
 namespace pa {
@@ -289,22 +290,6 @@ struct Walk {
   }
   __device__ __forceinline__ bool whole() const { return t_beg == 0 && t_end == span.tiles; }
 };
-
-// cap * tanh(s / cap), to 2^-19 of itself.  With u = s / cap and |u| >= 1/4, tanh u = 1 - 2 /
-// (exp(2 u) + 1), whose error of up to 1.6 * 2^-22 (the exponential's and the reciprocal's) is
-// 2^-19 of it at 1/4 and would be any multiple of it nearer to 0.  There the series u - u^3 / 3
-// + 2 u^5 / 15 - 17 u^7 / 315 + 62 u^9 / 2835 is taken, 2^-26 off at 1/4, as s (1 + u^2 (...)):
-// under a cap far above the scores u may be denormal, and s stays as it is.  (Both are formed
-// and one is chosen: the window case with its cap 50 109.7 us, 48 x 16001 over E4M3 pages with
-// cap 30 128.7 us; 109.1 and 127.2 with the exponential alone, 115.5 and 134.5 with tanhf.)
-__device__ __forceinline__ float capped(const Params& p, float s) {
-  const float u = s * p.cap_inv, w = u * u;
-  const float series = fmaf(fmaf(fmaf(62.f / 2835.f, w, -17.f / 315.f), w, 2.f / 15.f), w, -1.f / 3.f);
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(u * 2.8853900817779268f) + 1.f));
-  const float far = fmaf(-2.f * p.cap_out, r, p.cap_out);
-  return fabsf(u) < 0.25f ? fmaf(s * w, series, s) : far;
-}
 
 // Elements d, d + 1 of a head's output from sums relative to exp2(mm), and its lse.
 template <int D, bool kQBf16>
@@ -726,7 +711,7 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
             for (int e = 0; e < 4; ++e) {
               float& v = s[j][t][e];
               v *= sc[t][e & 1];
-              if (p.cap_out != 0.f) v = capped(p, v);
+              if (p.cap_out != 0.f) v = capped(v, p.cap_out, p.cap_inv);
             }
             if (edge) {
               const int ka = key0 + 16 * j + g, kc = ka + 8;

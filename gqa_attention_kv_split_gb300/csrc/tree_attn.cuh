@@ -1,0 +1,1014 @@
+// tree_attn.cuh -- attention of several new tokens per sequence over a paged K/V cache
+// (f16, bf16 or E4M3 pages): drafted tokens in a tree or a chain, grouped queries, split
+// over the cache's length and joined, on tcgen05 with accumulators in TMEM, for sm_103a.
+//
+// Mathematics.  Sequence b has n new tokens whose keys and values are in the cache already,
+// behind base = len - n others.  Row (i, h), token i and query head h over KV head g, is
+//   s_t = cap( (q_ih . K_t) * scale ),  out = v_scale * sum_t w_t V_t / sum_t w_t,
+//   w_t = exp(s_t - m),  lse = ln sum_t exp(s_t)
+// over the cached tokens t < base within its window (or among the sinks) and the drafted ones
+// base + j whose bit j its mask has; without masks over t <= base + i.  A range of tokens is
+// summed as (m, l, o) and ranges join by rescaling to the larger m.
+//
+// What bounds it: a K/V byte serves n G / 2 products of 16 bits (G heads a KV head), so HBM does up to
+// about 256 rows n G, the tensor cores from there on.  The rows of a KV head are packed into
+// the MMA's M = 128 (row = token * G + head): S = Q K^T with the keys on N, O = P V with the
+// weights as TMEM operand.  With 128 rows or fewer a tile of 128 tokens (64 KB in bf16, head
+// dim 128: 1.5 us of an SM's share of HBM) keeps the tensor pipe busy for 0.8 us, however few
+// rows there are, and the softmax for less:
+//  * Replicas.  With 64 (32) rows or fewer each row stands in the M dimension twice (four times),
+//    and each copy weighs a half (a quarter) of a tile's tokens, with zeros in P for the
+//    others: four warps share the softmax evenly, as independent (m, l, o) that join at the end.
+//  * S in two TMEM buffers: S of the next tile is computed while the softmax works on this one;
+//    P overwrites the S it came from (32 tokens' weights: 16 columns of their first terms, 16
+//    of their second ones).
+//  * Weights enter the product with V as two terms of 16 bits (22 bits in f16, 16 in bf16).
+//  * The maximum is raised (and O rescaled in TMEM) only when a row's passes the one in use by
+//    more than 2^8: weights then stay within f16, whose terms keep 2^-31 of the largest.
+//
+//  * Grid: one block per SM, in gangs of up to 8 with equal shares of the sequences' tokens,
+//    counted on the device from the lengths, as the one-token attention's (paged_attn.cuh):
+//    the blocks of a gang read the same tokens for other heads or other row blocks.  Pieces of
+//    units that lie in several blocks go to the workspace and a second kernel joins them.
+//  * Warps: 0 and 3 copy K and V (tensor-map TMA, one 128-byte chunk of a head's row for a page
+//    or a tile at a time, into the 128-byte-swizzled layout that both products read), 1 issues S,
+//    2 issues O, 4-7 load the queries, do the softmax (one thread a TMEM lane) and write the
+//    results.  E4M3 pages: 8-11 and 12-15 widen K and V to f16, exactly.
+//  * Every wait is bounded; a block whose wait expires drains what it started and leaves.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "softcap.cuh"
+#include "tcgen05.cuh"
+#include "tree_attn_host.h"
+
+namespace gqa {
+namespace ta {
+
+namespace {
+
+__device__ uint32_t g_tree_attn_err;  // of this translation unit's kernels
+
+}  // namespace
+
+template <int kCache, int D>
+struct Shape {
+  static constexpr bool kFp8 = kCache >= kCacheE4m3;
+  static constexpr int kTile = tile_of(D);
+  static constexpr int kChunks = D / 64;              // 128-byte chunks of a 16-bit row
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kSlot = kTile * D * 2;         // a tile of K (or of V) as the products read it
+  static constexpr int kRaw = kTile * D;              // an E4M3 tile as it is copied
+  // Slots of K and V, and of tiles yet to be widened: what fits beside the queries.
+  static constexpr int kNK = kFp8 ? (D == 64 ? 3 : D == 128 ? 2 : 1) : (D == 64 ? 5 : 3);
+  static constexpr int kNV = kFp8 ? (D == 64 ? 3 : 2) : (D == 64 ? 5 : D == 128 ? 3 : 2);
+  static constexpr int kNR = kFp8 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int kThreads = kFp8 ? 512 : 256;
+  static constexpr int kData = kQBytes + (kNK + kNV) * kSlot + 2 * kNR * kRaw;
+  // What starting and ending a unit costs, in tiles.
+  static constexpr int kUnitWork = 2;
+};
+
+struct Bars {
+  uint64_t k_full[5], k_free[5], v_full[5], v_free[5];      // tiles as the products read them
+  uint64_t kr_full[4], kr_free[4], vr_full[4], vr_free[4];  // E4M3 tiles
+  uint64_t s_full[2], p_full[2], p_free[2];
+  uint64_t q_ready, drain[2];
+};
+
+template <int kThreads>
+struct Smem {
+  Bars bar;
+  float m[kRows], l[kRows];  // of the replicas, at a unit's end
+  float q_up[kRows];         // by what a row's queries were scaled down (bf16 queries as f16)
+  int64_t scan_work[kThreads / 32], scan_turns[kThreads / 32];
+  int most[kThreads / 32];
+  int64_t total, end, rem;
+  int n_gangs, b0;
+  uint32_t tmem;
+};
+
+__device__ __forceinline__ int64_t share_begin(int i, int64_t total, int n) { return total * i / n; }
+// The gang that has a piece of work: the last one whose share begins at or before it.
+__device__ __forceinline__ int share_of(int64_t at, int64_t total, int n) { return (int)(((at + 1) * n + total - 1) / total) - 1; }
+
+// A sequence: its new tokens, and its tiles in the order in which they are gone through
+// (those of the sinks, then those from the window's first on, `gap` further).
+template <int kTile>
+struct Seq {
+  int64_t row0;                  // of its first new token
+  int n, len, base;              // new tokens; cached ones in all, and before the new ones
+  int first, sinks;              // no row sees the tokens in [sinks, first)
+  int sink_tiles, gap, tiles;
+  int rows, blocks;              // rows of a KV head, and blocks of kRows of them
+  bool bad;
+  __device__ __forceinline__ Seq(const Params& p, int b) {
+    const int64_t lo = p.indptr[b], hi = p.indptr[b + 1];
+    bad = lo < 0 || hi < lo || hi > p.total;
+    row0 = lo;
+    n = bad ? 0 : (int)(hi - lo);
+    const int64_t cap = p.max_pages << p.page_shift, x = p.kv_lens[b];
+    len = (int)(x < 0 ? 0 : x > cap ? cap : x);  // (a capacity is at most 2^30)
+    base = len - n;
+    rows = n * p.group;
+    blocks = (rows + kRows - 1) / kRows;
+    first = p.window > 0 && base >= p.window ? base + 1 - p.window : 0;
+    sinks = p.sinks < first ? p.sinks : 0;
+    if (first > 0 && p.sinks >= first) first = 0;  // the sinks reach the window
+    sink_tiles = (sinks + kTile - 1) / kTile;
+    gap = max(0, first / kTile - sink_tiles);
+    tiles = n > 0 ? (len + kTile - 1) / kTile - gap : 0;
+  }
+  __device__ __forceinline__ int place(int tile) const { return tile < sink_tiles ? tile : tile + gap; }
+  __device__ __forceinline__ bool hidden(int key) const { return key >= len || (key < first && key >= sinks); }
+  // Is any of the tokens [key, key + count) in no row's sight?
+  __device__ __forceinline__ bool edge(int key, int count) const { return key + count > len || (key < first && key + count > sinks); }
+};
+
+// Walks the units of a block's share (paged_attn.cuh's walk, with units that depend on the
+// sequence): work is counted in a unit's tiles and kUnitWork before them, or, by_unit, in
+// whole units.  Unit u of a sequence is row block u % blocks of KV head u / blocks: a gang's
+// blocks, which have neighbouring units, share the tokens that several row blocks read.
+template <int kTile, int kUnitWork>
+struct Walk {
+  int left, b, unit, t_beg, t_end;
+  bool by_unit, chain;
+  Seq<kTile> seq;
+  __device__ __forceinline__ Walk(const Params& p, int share, int b_, int64_t rem, bool by_unit_)
+      : b(b_), by_unit(by_unit_), chain(!p.mask), seq(p, b_) {
+    if (by_unit) {
+      unit = (int)rem;
+      t_beg = 0;
+      t_end = seq.tiles;
+      left = share - 1;
+    } else {
+      const int work = seq.tiles + kUnitWork;
+      unit = (int)(rem / work);
+      const int at = (int)(rem - (int64_t)unit * work);
+      t_beg = max(0, at - kUnitWork);
+      left = share - max(0, kUnitWork - at);
+      t_end = min(seq.tiles, t_beg + left);
+    }
+    unit = (unit << p.gang_shift) + ((int)blockIdx.x & ((1 << p.gang_shift) - 1));
+  }
+  __device__ __forceinline__ bool valid() const { return by_unit || left > 0; }
+  __device__ __forceinline__ bool next(const Params& p) {
+    left -= by_unit ? 1 : t_end - t_beg + kUnitWork;
+    if (by_unit ? left < 0 : left <= 0) return false;
+    t_beg = 0;
+    unit += 1 << p.gang_shift;
+    if (unit >= p.hkv * seq.blocks) {
+      unit -= p.hkv * seq.blocks;
+      do {
+        if (++b >= p.batch) return false;
+        seq = Seq<kTile>(p, b);
+      } while (seq.tiles == 0);
+    }
+    t_end = by_unit ? seq.tiles : min(seq.tiles, left);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t_beg == 0 && t_end == seq.tiles; }
+  __device__ __forceinline__ int kv_head() const { return unit / seq.blocks; }
+  __device__ __forceinline__ int row_begin() const { return (unit - unit / seq.blocks * seq.blocks) * kRows; }
+  __device__ __forceinline__ int rows() const { return min(kRows, seq.rows - row_begin()); }
+  // Tiles of this piece that a row of it can see: in a chain none behind its last token's.
+  __device__ __forceinline__ int count(const Params& p) const {
+    int e = t_end;
+    if (chain) {
+      const int last = seq.base + (row_begin() + rows() - 1) / p.group;
+      if (last < 0) return 0;
+      const int tile = last / kTile;
+      e = min(e, (tile < seq.sink_tiles ? tile : tile - seq.gap) + 1);
+    }
+    return max(0, e - t_beg);
+  }
+};
+
+// ---- the products -------------------------------------------------------------
+
+// Instruction descriptor, kind::f16, f32 accumulators: the operands' type at bits 7 and 10
+// (0 f16, 1 bf16), B's major at 16 (1: MN), N >> 3 at 17, M >> 4 at 24.
+__host__ __device__ constexpr uint32_t idesc(bool bf16, int n, bool b_mn_major) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* map, int slot, int chunk, int head, int page, uint32_t bar,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(map), "r"(0), "r"(slot), "r"(chunk), "r"(head), "r"(page), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
+  return d;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if (kBf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <bool kBf16>
+__device__ __forceinline__ float2 unpack(uint32_t x) {
+  if (kBf16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Bits of the tokens key .. key + 31 that lie in [lo, hi).
+__device__ __forceinline__ uint32_t range_bits(int key, int lo, int hi) {
+  const int a = lo - key, z = hi - key;
+  if (z <= 0 || a >= 32) return 0u;
+  const uint32_t below = z >= 32 ? ~0u : (1u << z) - 1u;
+  return a <= 0 ? below : below & (~0u << a);
+}
+
+// What a row sees.
+struct Sight {
+  int lo, hi, sinks;          // cached tokens in [lo, hi) and [0, sinks)
+  int base, words, len;       // drafted token j, at base + j: bit j of mask
+  const int32_t* mask;        // null: none
+  __device__ __forceinline__ uint32_t bits(int key) const {
+    if (lo <= key && key + 32 <= hi) return ~0u;
+    uint32_t v = range_bits(key, lo, hi) | range_bits(key, 0, sinks);
+    if (mask && key + 32 > base) {
+      const int j = key - base, w = j >> 5;
+      const uint32_t a = w >= 0 && w < words ? (uint32_t)mask[w] : 0u;
+      const uint32_t z = w >= -1 && w + 1 < words ? (uint32_t)mask[w + 1] : 0u;
+      v |= __funnelshift_r(a, z, j & 31) & range_bits(key, base, len);
+    }
+    return v;
+  }
+};
+
+namespace {
+
+template <int kCache, int D>
+__global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
+  using S = Shape<kCache, D>;
+  constexpr bool kFp8 = S::kFp8, kBf16 = kCache == kCacheBf16;    // the pages; the products' type
+  constexpr bool kQBf16 = kBf16 || kCache == kCacheE4m3;          // q and out
+  constexpr int kTile = S::kTile, kThreads = S::kThreads;
+  constexpr int kTileShift = kTile == 64 ? 6 : 7;
+  constexpr uint32_t kTmemO = 0, kTmemS = D;                      // columns: O, then two buffers of S
+  constexpr float kRaise = 8.f, kShift = kBf16 ? 0.f : 6.f;       // weights are at most 2^(kRaise + kShift)
+  uint32_t* const err = &g_tree_attn_err;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* const sq = smem_raw;
+  uint8_t* const sk = sq + S::kQBytes;
+  uint8_t* const sv = sk + S::kNK * S::kSlot;
+  uint8_t* const skr = sv + S::kNV * S::kSlot;
+  uint8_t* const svr = skr + S::kNR * S::kRaw;
+  Smem<kThreads>& sm = *reinterpret_cast<Smem<kThreads>*>(smem_raw + S::kData);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gang = (int)blockIdx.x >> p.gang_shift, gangs = kGrid >> p.gang_shift;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(smem_u32(&sm.bar.k_full[i]), kFp8 ? 4 : 1);
+      mbar_init(smem_u32(&sm.bar.k_free[i]), 1);
+      mbar_init(smem_u32(&sm.bar.v_full[i]), kFp8 ? 4 : 1);
+      mbar_init(smem_u32(&sm.bar.v_free[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sm.bar.kr_full[i]), 1);
+      mbar_init(smem_u32(&sm.bar.kr_free[i]), 4);
+      mbar_init(smem_u32(&sm.bar.vr_full[i]), 1);
+      mbar_init(smem_u32(&sm.bar.vr_free[i]), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.bar.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.bar.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.bar.p_free[i]), 1);
+      mbar_init(smem_u32(&sm.bar.drain[i]), 1);
+    }
+    mbar_init(smem_u32(&sm.bar.q_ready), 4);
+    fence_mbar_init();
+  }
+  // Launched as a programmatic dependent: what went before on the stream (the append of
+  // this step) has ended and is visible from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0 && p.record) p.record[blockIdx.x].last = -1;
+
+  // ---- this block's share ------------------------------------------------------
+  // Each thread sums the work of a contiguous range of sequences; a scan over the threads
+  // gives the ranges' starts, and the range that holds the share's first piece of work is
+  // walked by its thread.
+  using SeqT = Seq<kTile>;
+  const int64_t per = (p.batch + kThreads - 1) / kThreads;
+  const int64_t s0 = threadIdx.x * per < p.batch ? threadIdx.x * per : p.batch;
+  const int64_t s1 = s0 + per < p.batch ? s0 + per : p.batch;
+  auto turns_of = [&](const SeqT& s) { return s.tiles == 0 ? 0 : (p.hkv * s.blocks) >> p.gang_shift; };
+  int64_t work = 0, turns = 0;
+  int most = 0;
+  for (int64_t b = s0; b < s1; ++b) {
+    const SeqT s(p, (int)b);
+    if (blockIdx.x == 0 && (s.bad || (b == 0 && s.row0 != 0))) atomicOr(err, kErrBadIndptr);
+    const int64_t t = turns_of(s);
+    turns += t;
+    work += t * (s.tiles + S::kUnitWork);
+    most = max(most, s.tiles);
+  }
+  int64_t iw = work, it = turns;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, iw, d), c = __shfl_up_sync(0xffffffffu, it, d);
+    if (lane >= d) {
+      iw += a;
+      it += c;
+    }
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    sm.scan_work[warp] = iw;
+    sm.scan_turns[warp] = it;
+    sm.most[warp] = most;
+  }
+  __syncthreads();
+  int64_t before_w = 0, before_t = 0, total_w = 0, total_t = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) {
+      before_w += sm.scan_work[w];
+      before_t += sm.scan_turns[w];
+    }
+    total_w += sm.scan_work[w];
+    total_t += sm.scan_turns[w];
+    most = max(most, sm.most[w]);
+  }
+  const bool by_unit = most <= kWholeTiles && total_t <= gangs;
+  const int64_t before = by_unit ? before_t + it - turns : before_w + iw - work;
+  const int64_t total = by_unit ? total_t : total_w, mine = by_unit ? turns : work;
+  const int n_gangs = total < gangs ? (int)total : gangs;  // gangs with a share: none is empty
+  const int64_t beg = gang < n_gangs ? share_begin(gang, total, n_gangs) : 0;
+  const int64_t end = gang < n_gangs ? share_begin(gang + 1, total, n_gangs) : 0;
+  if (threadIdx.x == 0) {
+    sm.total = total;
+    sm.n_gangs = n_gangs;
+    sm.end = end;
+  }
+  if (beg < end && beg >= before && beg < before + mine) {
+    int64_t rem = beg - before;
+    int64_t b = s0;
+    for (;; ++b) {
+      const SeqT s(p, (int)b);
+      const int64_t t = turns_of(s), w = by_unit ? t : t * (s.tiles + S::kUnitWork);
+      if (rem < w) break;
+      rem -= w;
+    }
+    sm.b0 = (int)b;
+    sm.rem = rem;
+  }
+  // Rows of sequences without a cached token: zeros.
+  for (int64_t b = blockIdx.x; b < p.batch; b += kGrid) {
+    const SeqT s(p, (int)b);
+    if (s.tiles > 0 || s.n == 0) continue;
+    const int64_t r0 = s.row0 * p.hq, rows = (int64_t)s.n * p.hq;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + r0 * D * 2);
+    for (int64_t i = threadIdx.x; i < rows * (D / 8); i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t i = threadIdx.x; p.lse && i < rows; i += kThreads) p.lse[r0 + i] = -INFINITY;
+  }
+  __syncthreads();
+  if (beg >= end) return;
+  Walk<kTile, S::kUnitWork> walk(p, (int)(end - beg), sm.b0, sm.rem, by_unit);
+  if (!walk.valid()) return;  // (a share that lies before a unit's first tile)
+
+  if (warp == 1) {
+    tc::tmem_alloc(smem_u32(&sm.tmem), 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  tc::fence_after_thread_sync();
+  const uint32_t tmem = sm.tmem;
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return (bool)__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, err));
+  };
+  bool failed = false;  // a wait of this thread's role expired
+  int issued = 0;       // producers: stages issued, up to all of them
+
+  if (warp == 0 || warp == 3) {
+    // ---------------------------------------------------------------- producers
+    const bool is_v = warp == 3;
+    constexpr int kStagesK = kFp8 ? S::kNR : S::kNK, kStagesV = kFp8 ? S::kNR : S::kNV;
+    const int stages = is_v ? kStagesV : kStagesK;
+    uint64_t* const full = kFp8 ? (is_v ? sm.bar.vr_full : sm.bar.kr_full) : (is_v ? sm.bar.v_full : sm.bar.k_full);
+    uint64_t* const free_ = kFp8 ? (is_v ? sm.bar.vr_free : sm.bar.kr_free) : (is_v ? sm.bar.v_free : sm.bar.k_free);
+    constexpr int kStage = kFp8 ? S::kRaw : S::kSlot;
+    constexpr int kParts = kFp8 ? 1 : S::kChunks;  // copies for one box: the chunks of its rows
+    const uint32_t base = smem_u32(kFp8 ? (is_v ? svr : skr) : (is_v ? sv : sk));
+    const CUtensorMap* const map = is_v ? &v_map : &k_map;
+    const int box_shift = p.box_shift, boxes = kTile >> box_shift, box_bytes = (kFp8 ? D : 128) << box_shift;
+    const int my_box = lane & (boxes - 1), my_part = lane >> (kTileShift - box_shift);
+    const uint32_t my_dst = base + my_part * (kTile * 128) + my_box * box_bytes;
+    int st = 0, ph = 1;
+    do {
+      const SeqT& s = walk.seq;
+      const int n = p.starve ? 0 : walk.count(p), head = walk.kv_head();
+      // (row blocks that read the same tokens find them in L2)
+      const uint64_t pol = s.blocks > 1 ? policy_evict_last() : policy_evict_first();
+      const int32_t* row = p.block_table + (int64_t)walk.b * p.max_pages;
+      // Copies are counted along the unit's tiles; place() says where in the sequence one lies.
+      auto place = [&](int c) { return (s.place(c >> (kTileShift - box_shift)) << (kTileShift - box_shift)) + (c & (boxes - 1)); };
+      auto wanted = [&](int c) {
+        const int64_t key = (int64_t)c << box_shift;
+        return key < s.len && (key + (1 << box_shift) > s.first || key < s.sinks);
+      };
+      auto page_of = [&](int c) {
+        c = place(c);
+        if (!wanted(c)) return 0;
+        int g = row[c >> (p.page_shift - box_shift)];
+        if (g < 0 || g >= p.num_pages) {
+          atomicOr(err, kErrBadIndex);
+          g = 0;
+        }
+        return g;
+      };
+      // Page numbers, 32 copies' worth at a time and one such group ahead (lane l has those of copy l).
+      int c = walk.t_beg << (kTileShift - box_shift);
+      int cur = n > 0 ? page_of(c + lane) : 0, nxt = n > 0 ? page_of(c + 32 + lane) : 0, at = 0;
+      for (int j = 0; j < n; ++j) {
+        if (!wait_all(&free_[st], ph)) {
+          failed = true;
+          break;
+        }
+        const int pg = __shfl_sync(0xffffffffu, cur, at + my_box);
+        const int mine_at = place(c + my_box);
+        const bool live = my_part < kParts && wanted(mine_at);
+        const uint32_t bar = smem_u32(&full[st]);
+        const uint32_t bytes = box_bytes * __popc(__ballot_sync(0xffffffffu, live));
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        if (live) tma_5d(my_dst + st * kStage, map, (mine_at << box_shift) & ((1 << p.page_shift) - 1), my_part, head, pg, bar, pol);
+        c += boxes;
+        at += boxes;
+        if (at == 32) {
+          at = 0;
+          cur = nxt;
+          nxt = page_of(c + 32 + lane);
+        }
+        issued = min(issued + 1, stages);
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    } while (!failed && walk.next(p));
+    // No copy may land after the block has gone (the stages before st were filled in the present
+    // round, the others in the one before).
+    if (lane == 0)
+      for (int i = 0; i < issued; ++i)
+        if (!mbar_wait(smem_u32(&full[i]), i < st ? ph ^ 1 : ph, err)) break;
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- S issuer
+    constexpr uint32_t id = idesc(kBf16, kTile, false);
+    const uint64_t dq = tc::sw128_desc(smem_u32(sq)), dk0 = tc::sw128_desc(smem_u32(sk));
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + kTmemS;
+    int st = 0, ph = 0, j = 0, units = 0;  // slot and its parity; tiles and units so far
+    do {
+      const int n = walk.count(p);
+      if (n == 0) continue;
+      if (!wait_all(&sm.bar.q_ready, units & 1)) {
+        failed = true;
+        break;
+      }
+      ++units;
+      for (int i = 0; i < n; ++i, ++j) {
+        if (!wait_all(&sm.bar.k_full[st], ph) || (j >= 2 && !wait_all(&sm.bar.p_free[j & 1], ((j >> 1) - 1) & 1))) {
+          failed = true;
+          break;
+        }
+        tc::fence_after_thread_sync();
+        const uint64_t dk = dk0 + (uint64_t)(st * (S::kSlot >> 4));
+        const uint32_t ts = tm + (uint32_t)(j & 1) * kTile;
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc::mma_f16(ts, dq + (k / 4) * (kRows * 128 >> 4) + 2 * (k % 4), dk + (k / 4) * (kTile * 128 >> 4) + 2 * (k % 4), id, k > 0);
+          tc::commit(smem_u32(&sm.bar.s_full[j & 1]));
+          tc::commit(smem_u32(&sm.bar.k_free[st]));
+        }
+        __syncwarp();
+        if (++st == S::kNK) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    } while (!failed && walk.next(p));
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- O issuer
+    constexpr uint32_t id = idesc(kBf16, D, true);
+    const uint64_t dv0 = tc::sw128_desc_lbo(smem_u32(sv), kTile * 128);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int st = 0, ph = 0, j = 0;
+    do {
+      const int n = walk.count(p);
+      for (int i = 0; i < n; ++i, ++j) {
+        if (!wait_all(&sm.bar.v_full[st], ph)) {
+          failed = true;
+          break;
+        }
+        if (!kFp8) {
+          // Rows that nothing sees may hold anything; 0 * NaN is NaN, so they are zeroed.
+          const int key0 = walk.seq.place(walk.t_beg + i) * kTile;
+          if (walk.seq.edge(key0, kTile)) {
+            for (int x = lane; x < kTile * 8; x += 32) {
+              if (!walk.seq.hidden(key0 + (x >> 3))) continue;
+#pragma unroll
+              for (int ch = 0; ch < S::kChunks; ++ch)
+                *reinterpret_cast<uint4*>(sv + st * S::kSlot + ch * (kTile * 128) + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (!wait_all(&sm.bar.p_full[j & 1], (j >> 1) & 1)) {
+          failed = true;
+          break;
+        }
+        tc::fence_after_thread_sync();
+        const uint64_t dv = dv0 + (uint64_t)(st * (S::kSlot >> 4));
+        const uint32_t tp = tm + kTmemS + (uint32_t)(j & 1) * kTile;
+        if (tc::elect_one()) {
+          // K = 16 tokens a product: 8 columns of P (first terms, then second ones), 2048 bytes of V
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) {
+            const uint32_t a = tp + 32 * (k / 2) + 8 * (k % 2);
+            tc::mma_f16_tmem_a(tm + kTmemO, a, dv + 128 * k, id, (i > 0 || k > 0) ? 1u : 0u);
+            tc::mma_f16_tmem_a(tm + kTmemO, a + 16, dv + 128 * k, id, 1u);
+          }
+          tc::commit(smem_u32(&sm.bar.p_free[j & 1]));
+          tc::commit(smem_u32(&sm.bar.v_free[st]));
+        }
+        __syncwarp();
+        if (++st == S::kNV) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    } while (!failed && walk.next(p));
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int quad = warp - 4, L = 32 * quad + lane;  // TMEM lane
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
+    const float neg = p.scale_log2 < 0.f ? -1.f : 1.f;
+    int j = 0, seg = 0;  // tiles so far; pieces begun
+    // Once a wait has expired (failed) nothing more is waited for, computed or written, but the
+    // four warps go on meeting at the units' ends.
+    do {
+      const SeqT& s = walk.seq;
+      const int n = walk.count(p), kvh = walk.kv_head(), r0 = walk.row_begin(), rows = walk.rows();
+      // Copies of each row, a power of two, of `span` rows each
+      const int rep_shift = rows > 64 ? 0 : rows > 32 || kTile == 64 ? 1 : 2;
+      const int span = kRows >> rep_shift, rep = L / span, row = L - rep * span;
+      const bool live = row < rows;
+      const int token = (r0 + (live ? row : 0)) / p.group, head = kvh * p.group + (r0 + (live ? row : 0)) - token * p.group;
+      ++seg;
+      if (n > 0 && !failed) {
+        // ---- queries: a row is read by D / 8 lanes
+        constexpr int kPer = D / 8, kAt = 32 / kPer;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kAt) {
+          const int x = 32 * quad + i + lane / kPer, e = lane % kPer, y = x & (span - 1);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (y < rows) {
+            const int t = (r0 + y) / p.group, h = kvh * p.group + (r0 + y) - t * p.group;
+            v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) + ((s.row0 + t) * p.q_tok + h * p.q_head + 8 * e) * 2);
+          }
+          if (kFp8 && kQBf16) {
+            // bf16 rows enter the f16 product scaled by a power of two that brings their largest
+            // element into [2^15, 2^16): exact but for elements below 2^-29 of it, whose
+            // rounding is at most 2^-40 of the largest.
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+            uint32_t mx = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = 1; o < kPer; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int ex = min(max((int)(mx >> 7), 16), 254);  // biased exponent
+            const float down = __uint_as_float((uint32_t)(269 - ex) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = unpack<true>(w[k]);
+              w[k] = pack<false>(f.x * down, f.y * down);
+            }
+            if (e == 0) sm.q_up[x] = __uint_as_float((uint32_t)(ex - 15) << 23);
+          }
+          *reinterpret_cast<uint4*>(sq + (e / 8) * (kRows * 128) + x * 128 + (((e % 8) ^ (x & 7)) << 4)) = v;
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.bar.q_ready));
+      }
+      const float up = kFp8 && kQBf16 && n > 0 ? sm.q_up[L] : 1.f;
+      const float scale = p.scale_log2 * up;
+      // ---- what this row sees
+      Sight see;
+      see.base = s.base;
+      see.len = s.len;
+      see.words = p.words;
+      see.mask = nullptr;
+      const int at = s.base + token;  // its place in the cache
+      int pos = at;
+      see.hi = p.mask ? s.base : at + 1;
+      if (p.mask && live) {
+        see.mask = p.mask + (s.row0 + token) * p.words;
+        if (p.window > 0) pos = max(s.base, p.positions[s.row0 + token]);
+      }
+      see.lo = p.window > 0 && pos >= p.window ? pos + 1 - p.window : 0;
+      see.sinks = p.window > 0 ? min(p.sinks, see.hi) : 0;
+      if (!live) see.lo = see.hi = see.sinks = 0;
+      // This copy's 32-token parts of a tile
+      const int part0 = (rep * kTile) >> (rep_shift + 5), part1 = ((rep + 1) * kTile) >> (rep_shift + 5);
+
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < n && !failed; ++i, ++j) {
+        if (!wait_all(&sm.bar.s_full[j & 1], (j >> 1) & 1)) {
+          failed = true;
+          break;
+        }
+        tc::fence_after_thread_sync();
+        const uint32_t ts = t_lane + kTmemS + (uint32_t)(j & 1) * kTile;
+        const int key0 = s.place(walk.t_beg + i) * kTile;
+        // ---- the tile's maximum
+        float mx = -INFINITY;  // of neg * s: the scale's sign aside
+        for (int c = part0; c < part1; ++c) {
+          uint32_t v[32];
+          tc::ld32(ts + 32 * c, v);
+          const uint32_t vis = see.bits(key0 + 32 * c);
+          tc::ld_wait();
+          if (neg < 0.f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] ^= 0x80000000u;
+          }
+          if (__all_sync(0xffffffffu, vis == ~0u)) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (vis >> e & 1u) mx = fmaxf(mx, __uint_as_float(v[e]));
+          }
+        }
+        mx = mx == -INFINITY ? mx : mx * neg * scale;
+        if (p.cap_out != 0.f && mx != -INFINITY) mx = capped(mx, p.cap_out, p.cap_inv);
+        const bool raise = mx > m + kRaise || (m == -INFINITY && mx > m);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float alpha = raise ? fast_exp2(m - mx) : 1.f;  // 0 where m was -inf
+          if (i > 0) {
+            // O holds the products of the tiles before this one
+            if (!wait_all(&sm.bar.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) {
+              failed = true;
+              break;
+            }
+            tc::fence_after_thread_sync();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tc::ld32(t_lane + kTmemO + c, o);
+              tc::ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc::st32(t_lane + kTmemO + c, o);
+            }
+          }
+          if (raise) {
+            l *= alpha;
+            m = mx;
+          }
+        }
+        // ---- weights, in two terms, over the scores that they came from
+        const float sub = m == -INFINITY ? 0.f : m - kShift;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < kTile / 32; ++c) {
+          uint32_t w[32];
+          if (c < part0 || c >= part1) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = 0u;
+            tc::st32(ts + 32 * c, w);
+            continue;
+          }
+          uint32_t v[32];
+          tc::ld32(ts + 32 * c, v);
+          const uint32_t vis = see.bits(key0 + 32 * c);
+          const bool all = __all_sync(0xffffffffu, vis == ~0u);
+          tc::ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 x = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+            if (p.cap_out != 0.f) {
+              x.x = capped(x.x * scale, p.cap_out, p.cap_inv) - sub;
+              x.y = capped(x.y * scale, p.cap_out, p.cap_inv) - sub;
+            } else {
+              x = __ffma2_rn(x, make_float2(scale, scale), make_float2(-sub, -sub));
+            }
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+            if (!all) {
+              if (!(vis >> (2 * e) & 1u)) x.x = 0.f;
+              if (!(vis >> (2 * e + 1) & 1u)) x.y = 0.f;
+            }
+            w[e] = pack<kBf16>(x.x, x.y);
+            const float2 h = unpack<kBf16>(w[e]);
+            w[16 + e] = pack<kBf16>(x.x - h.x, x.y - h.y);
+            sum = __fadd2_rn(sum, x);
+          }
+          tc::st32(ts + 32 * c, w);
+        }
+        l += sum.x + sum.y;
+        tc::st_wait();
+        tc::fence_before_thread_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.bar.p_full[j & 1]));
+      }
+      // ---- the unit's (or its piece's) end
+      if (n > 0 && !failed) {
+        if (!wait_all(&sm.bar.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) failed = true;
+        tc::fence_after_thread_sync();
+      }
+      // The copies of a row: their maxima and sums
+      float f = 1.f;  // what this copy's sums are multiplied by
+      if (rep_shift > 0) {
+        sm.m[L] = m;
+        sm.l[L] = l;
+        named_bar_sync(1, 128);
+        float mm = -INFINITY, ll = 0.f;
+        for (int x = row; x < kRows; x += span) mm = fmaxf(mm, sm.m[x]);
+        for (int x = row; x < kRows; x += span) ll = fmaf(sm.l[x], sm.m[x] == -INFINITY ? 0.f : fast_exp2(sm.m[x] - mm), ll);
+        f = m == -INFINITY ? 0.f : fast_exp2(m - mm);
+        m = mm;
+        l = ll;
+      }
+      const bool summed = n > 0 && !failed;  // there is something in O
+      if (!summed) f = 0.f;
+      const bool whole = walk.whole(), writes = live && rep == 0 && !failed;
+      if (whole) f = l == 0.f ? 0.f : f * (p.v_scale / l);
+      const int64_t out_row = (s.row0 + token) * p.hq + head;
+      const int64_t piece = ((int64_t)blockIdx.x * 2 + (seg == 1 ? 0 : 1)) * kRows + row;
+      float* const stage = reinterpret_cast<float*>(sq) + L * 20;  // (the queries are no longer needed; 16 columns, spread over the banks)
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        if (summed) {
+          tc::ld16(t_lane + kTmemO + c, o);
+          tc::ld_wait();
+        }
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = f == 0.f ? 0.f : __uint_as_float(o[e]) * f;
+        if (rep_shift > 0) {
+          if (rep > 0)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(stage + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          named_bar_sync(1, 128);
+          if (rep == 0)
+            for (int y = row + span; y < kRows; y += span)
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 z = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(sq) + y * 20 + e);
+                x[e] += z.x;
+                x[e + 1] += z.y;
+                x[e + 2] += z.z;
+                x[e + 3] += z.w;
+              }
+          named_bar_sync(1, 128);
+        }
+        if (!writes) continue;
+        if (whole) {
+          uint4 u[2];
+          uint32_t* w = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = pack<kQBf16>(x[2 * e], x[2 * e + 1]);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (out_row * D + c) * 2);
+          dst[0] = u[0];
+          dst[1] = u[1];
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + piece * D + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        }
+      }
+      if (writes) {
+        if (!whole)
+          p.part_ml[piece] = make_float2(m - kShift, l);
+        else if (p.lse)
+          p.lse[out_row] = l == 0.f ? -INFINITY : (m - kShift) * 0.6931471805599453f + logf(l);
+      }
+      if (p.record && L == 0 && walk.t_beg == 0 && !whole && !failed) {
+        // The unit begins here; it ends in the gang that has its last tile.
+        const int64_t last = sm.end - walk.left + s.tiles - 1;
+        p.record[blockIdx.x] = Record{walk.b, walk.unit, gang, share_of(last, sm.total, sm.n_gangs), seg == 1 ? 0 : 1};
+      }
+    } while (walk.next(p));
+  } else {
+    // ---------------------------------------------------------------- E4M3 -> f16
+    if constexpr (kFp8) {
+      const bool is_v = warp >= 12;
+      uint64_t* const raw_full = is_v ? sm.bar.vr_full : sm.bar.kr_full;
+      uint64_t* const raw_free = is_v ? sm.bar.vr_free : sm.bar.kr_free;
+      uint64_t* const full = is_v ? sm.bar.v_full : sm.bar.k_full;
+      uint64_t* const free_ = is_v ? sm.bar.v_free : sm.bar.k_free;
+      const uint8_t* const raw = is_v ? svr : skr;
+      uint8_t* const slots = is_v ? sv : sk;
+      const int n_slots = is_v ? S::kNV : S::kNK, t = threadIdx.x & 127;
+      int rs = 0, rph = 0, st = 0, ph = 1;
+      do {
+        const int n = walk.count(p);
+        for (int i = 0; i < n; ++i) {
+          if (!wait_all(&raw_full[rs], rph) || !wait_all(&free_[st], ph)) {
+            failed = true;
+            break;
+          }
+          const int key0 = walk.seq.place(walk.t_beg + i) * kTile;
+          const bool edge = is_v && walk.seq.edge(key0, kTile);
+          const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw);
+          uint8_t* dst = slots + st * S::kSlot;
+          constexpr int kPer = D / 16;  // 16-byte pieces of a row
+#pragma unroll 4
+          for (int x = t; x < kTile * kPer; x += 128) {
+            const int key = x / kPer, e = x % kPer;
+            uint4 v = src[x];
+            // Rows that nothing sees may hold anything; 0 * NaN is NaN, so they are zeroed.
+            if (edge && walk.seq.hidden(key0 + key)) v = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint4 h[2];
+            uint32_t* hw = reinterpret_cast<uint32_t*>(h);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              hw[2 * k] = e4m3_to_f16x2(w[k] & 0xffffu);
+              hw[2 * k + 1] = e4m3_to_f16x2(w[k] >> 16);
+            }
+            // (the pieces of odd chunks in the other order: eight lanes then fill all banks)
+            const int flip = (e / 4) & 1;
+            uint8_t* d = dst + (e / 4) * (kTile * 128) + key * 128;
+            const int c0 = 2 * (e % 4) + flip, c1 = 2 * (e % 4) + 1 - flip;
+            *reinterpret_cast<uint4*>(d + ((c0 ^ (key & 7)) << 4)) = flip ? h[1] : h[0];
+            *reinterpret_cast<uint4*>(d + ((c1 ^ (key & 7)) << 4)) = flip ? h[0] : h[1];
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&full[st]));
+            mbar_arrive(smem_u32(&raw_free[rs]));
+          }
+          if (++rs == S::kNR) {
+            rs = 0;
+            rph ^= 1;
+          }
+          if (++st == n_slots) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      } while (!failed && walk.next(p));
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc::fence_before_thread_sync();
+  if (__syncthreads_or(failed)) {
+    // A wait expired: let the products that the issuers started complete before TMEM is freed.
+    if (warp == 1 || warp == 2) {
+      if (tc::elect_one()) tc::commit(smem_u32(&sm.bar.drain[warp - 1]));
+      __syncwarp();
+      mbar_wait(smem_u32(&sm.bar.drain[warp - 1]), 0, err);
+    }
+    tc::fence_before_thread_sync();
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc::fence_after_thread_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// (volatile: the compiler would otherwise put each load next to its use)
+template <int kN>
+__device__ __forceinline__ void load_l2(const float* p, float (&v)[kN]) {
+  if constexpr (kN == 2)
+    asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p));
+  else
+#pragma unroll
+    for (int i = 0; i < kN; i += 4)
+      asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]) : "l"(p + i));
+}
+
+// Joins the pieces of the units that lie in several blocks' shares, in the order of their
+// tiles: a warp per row, a few pieces' loads in flight.
+template <int kTile, int D, bool kQBf16>
+__global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ Params p) {
+  constexpr int kN = D / 32, kBatch = 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Record u = p.record[blockIdx.x];
+  if (u.last < 0) return;
+  const Seq<kTile> s(p, u.b);
+  const int lane = threadIdx.x & 31, row = (int)blockIdx.y * 8 + ((int)threadIdx.x >> 5);
+  const int kvh = u.unit / s.blocks, r = (u.unit - kvh * s.blocks) * kRows + row;
+  if (row >= kRows || r >= s.rows) return;
+  const int in_gang = u.unit & ((1 << p.gang_shift) - 1);
+  float m = -INFINITY, l = 0.f, x[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) x[i] = 0.f;
+  for (int c0 = u.first; c0 <= u.last; c0 += kBatch) {
+    float ml[kBatch][2], v[kBatch][kN];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int c = min(c0 + e, u.last);
+      const int64_t at = (int64_t)(2 * ((c << p.gang_shift) + in_gang) + (c == u.first ? u.first_slot : 0)) * kRows + row;
+      load_l2<2>(reinterpret_cast<const float*>(p.part_ml + at), ml[e]);
+      load_l2<kN>(p.part_o + at * D + lane * kN, v[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      if (c0 + e > u.last) break;
+      const float mn = fmaxf(m, ml[e][0]);
+      const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn), g = ml[e][0] == -INFINITY ? 0.f : fast_exp2(ml[e][0] - mn);
+      m = mn;
+      l = fmaf(l, f, ml[e][1] * g);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) x[i] = fmaf(x[i], f, v[e][i] * g);
+    }
+  }
+  const int token = r / p.group, head = kvh * p.group + r - token * p.group;
+  const int64_t out_row = (s.row0 + token) * p.hq + head;
+  const float inv = l == 0.f ? 0.f : p.v_scale / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (out_row * D + lane * kN) * 2);
+#pragma unroll
+  for (int i = 0; i < kN; i += 2) dst[i / 2] = pack<kQBf16>(x[i] * inv, x[i + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+}
+
+template <int kCache, int D>
+cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
+  using S = Shape<kCache, D>;
+  constexpr size_t smem = S::kData + sizeof(Smem<S::kThreads>);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static_assert(S::kNK <= 5 && S::kNV <= 5 && S::kNR <= 4, "barrier arrays");
+  static_assert(kRows * 20 * sizeof(float) <= S::kQBytes, "the copies' sums lie where the queries were");
+  static_assert(D + 2 * S::kTile <= 512, "TMEM columns");
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(tree_attn_kernel<kCache, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kGrid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<kCache, D>, p, k_map, v_map)) != cudaSuccess || !p.record) return e;
+  cfg.gridDim = dim3(kGrid, p.row_groups);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<S::kTile, D, kCache == kCacheBf16 || kCache == kCacheE4m3>, p);
+}
+
+template <int kCache>
+cudaError_t launch_cache(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
+  switch (d) {
+    case 64: return launch_instance<kCache, 64>(p, k_map, v_map, stream);
+    case 128: return launch_instance<kCache, 128>(p, k_map, v_map, stream);
+    default: return launch_instance<kCache, 256>(p, k_map, v_map, stream);
+  }
+}
+
+cudaError_t read_errors_here(uint32_t* word) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_tree_attn_err, sizeof(uint32_t));
+  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_tree_attn_err, &zero, sizeof(uint32_t));
+}
+
+}  // namespace
+
+}  // namespace ta
+}  // namespace gqa

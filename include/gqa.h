@@ -553,6 +553,61 @@ gqa_status gqa_tree_mask_t(const gqa_tensor* parents, const gqa_tensor* qo_indpt
                            gqa_tensor* positions, int window, int sinks, gqa_stream_t stream);
 
 /*
+ * gqa_paged_tree_attn_t -- attention of several new tokens per sequence over a paged
+ * K/V cache: the drafted tokens of a tree, or of a chain, whose keys and values have
+ * been appended.  Token i of sequence b (row t = qo_indptr[b] + i of q and out) lies at
+ * place base_b + i of the cache, base_b as above, and sees
+ *   with a mask (a tree): the cached tokens j < base_b that its window leaves, j >
+ *     positions[t] - window or j < sinks (all of them without a window), and the
+ *     drafted tokens at places base_b + j >= 0 whose bit j mask[t] has
+ *   without: the tokens j <= base_b + i with j > base_b + i - window or j < sinks
+ *   s_j = (q[t,h,:] . K_j) * q_scale * k_scale / sqrt(d), capped as gqa_paged_attn_t's
+ *   out[t,h,:] = v_scale * sum_j softmax_j(s) V_j,  lse[t,h] = ln sum_j exp(s_j)
+ *
+ *   q            [total, q_heads, d]  f16 or bf16; strides multiples of 16 bytes,
+ *                last dimension dense
+ *   k_pages, v_pages, block_table  as gqa_paged_attn_t's
+ *   qo_indptr    [batch + 1], kv_lens [batch]  int32, read on the device; kv_lens
+ *                counts the new tokens and is clamped to the block table's capacity
+ *   mask         [total, words]  int32, words 1 .. 32, as gqa_tree_mask_t writes it
+ *                (its own bit is a token's sight of itself); a drafted token behind
+ *                the 32 * words-th is seen by none.  Or NULL: chains
+ *   positions    [total]  int32; read with a mask and a window only (then needed),
+ *                values below base_b count as base_b; or NULL
+ *   out          [total, q_heads, d]  q's type, dense, written
+ *   lse          [total, q_heads]  f32, dense, written; or NULL
+ *   workspace    as gqa_paged_attn_t's, of gqa_paged_tree_attn_workspace(q_heads,
+ *                kv_heads, d) bytes
+ *   batch 1 .. 65535; total >= 0; window, sinks >= 0; head layouts, page sizes, the
+ *   other numbers and the limit on their product as gqa_paged_attn_t's
+ *
+ * Scores, maxima, sums and accumulators are f32.  A softmax weight meets V as two
+ * 16-bit terms of the pages' type (f16 for E4M3 ones), 22 bits in f16 and 16 in bf16;
+ * f16 terms are exact to 2^-31 of the largest weight at best.  A bf16 query over E4M3
+ * pages is exact to 2^-40 of its row's largest element.
+ *
+ * A row that sees nothing (a sequence of length 0, an empty mask) becomes zeros, with
+ * lse = -infinity; rows behind qo_indptr[batch] are left as they are.  Slots that no
+ * row of their sequence can see -- behind its length, or between the sinks and the
+ * window of its first new token -- may hold anything, NaN too; an infinity or NaN in a
+ * row of V that some row of the sequence sees may make its element NaN in the others,
+ * whether they see it or not.  A page outside [0, num_pages) is not read: page 0 is
+ * used instead and bit 1 of the error word is set.  A sequence whose offsets do not lie
+ * in order within [0, total] is left out (its rows are not written) and sets bit 2, as
+ * does qo_indptr[0] != 0.  out and lse overlap no other argument.  The split is chosen
+ * on the device from the lengths.  One kernel, or two; host tensors are refused.
+ */
+gqa_status gqa_paged_tree_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, const gqa_tensor* v_pages,
+                                 const gqa_tensor* block_table, const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens,
+                                 const gqa_tensor* mask, const gqa_tensor* positions, gqa_tensor* out, gqa_tensor* lse,
+                                 float q_scale, float k_scale, float v_scale, int window, int sinks, float softcap,
+                                 void* workspace, int64_t workspace_bytes, gqa_stream_t stream);
+
+/* Bytes of workspace that gqa_paged_tree_attn_t needs for a head layout, whatever the
+ * batch, the tokens and the lengths (0 for one that it does not take). */
+int64_t gqa_paged_tree_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t d);
+
+/*
  * gqa_paged_keep_t -- compaction of a paged cache after verification: of each
  * sequence's drafted tokens the accepted ones move together, behind its cached
  * tokens, and the others are given up.  Drafted token kept[b, i] of sequence b

@@ -95,6 +95,56 @@ def test_tree_mask_of_nothing_is_accepted():
     assert mask.shape == (0, 2) and positions.shape == (0,)
 
 
+def tree_args(B=2, T=5, hq=4, hkv=2, d=64, page=16, dtype=torch.float16, cache=None, P=5, mp=2):
+    return dict(q=fake((T, hq, d), dtype), k_pages=fake((P, hkv, page, d), cache or dtype), v_pages=fake((P, hkv, page, d), cache or dtype),
+                block_table=fake((B, mp), I32), qo_indptr=fake((B + 1,), I32), kv_lens=fake((B,), I32), mask=fake((T, 1), I32),
+                workspace=torch.zeros(64 << 20, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("change,match", [
+    (dict(q=torch.zeros(5, 4, 64)), "q has dtype f32; expected f16 or bf16"),
+    (dict(q=fake((5, 5, 64), torch.float16)), "5 query heads over 2 KV heads"),
+    (dict(q=fake((5, 4, 32), torch.float16)), "k_pages has extent 64 in dimension 3; expected 32"),
+    (dict(q=fake((5, 4, 68), torch.float16)[..., :64]), "q: stride 68 in dimension 1"),
+    (dict(k_pages=fake((5, 2, 24, 64), torch.float16), v_pages=fake((5, 2, 24, 64), torch.float16)), "page size 24 is not"),
+    (dict(v_pages=fake((5, 2, 16, 64), torch.uint8)), "v_pages has dtype u8; expected f16"),
+    (dict(qo_indptr=fake((2,), I32)), "qo_indptr has extent 2 in dimension 0; expected 3"),
+    (dict(block_table=fake((3, 2), I32)), "block_table has extent 3 in dimension 0; expected 2"),
+    (dict(mask=fake((4, 1), I32)), "mask has extent 4 in dimension 0; expected 5"),
+    (dict(mask=fake((5, 33), I32)), "33 words of bits"),
+    (dict(mask=fake((5, 1), torch.uint8)), "mask has dtype u8; expected i32"),
+    (dict(window=4), "a window over a tree needs the tokens' positions"),
+    (dict(positions=fake((4,), I32)), "positions has extent 4"),
+    (dict(out=fake((5, 4, 64))), "out has dtype bf16; expected f16"),
+    (dict(lse=torch.zeros(5, 2)), "lse has extent 2 in dimension 1; expected 4"),
+    (dict(mask=None, window=-1), "window -1 is negative"),
+    (dict(sinks=-1), "sinks -1 is negative"),
+    (dict(softcap=math.nan), "softcap must be finite and >= 0"),
+    (dict(q_scale=math.inf), "q_scale is not finite"),
+    (dict(v_scale=0.0), "v_scale must be finite and > 0"),
+    (dict(workspace=torch.zeros(64, dtype=torch.uint8)), "workspace of 64 bytes"),
+    (dict(), "gqa_paged_tree_attn takes device tensors only"),
+    (dict(workspace=None, mask=None), "gqa_paged_tree_attn takes device tensors only"),
+])
+def test_tree_attention_refusals(change, match):
+    with pytest.raises(gqa.GqaError, match=match):
+        gqa.gqa_paged_tree_attn(**{**tree_args(), **change})
+
+
+def test_tree_attention_over_too_much_is_refused():
+    """Its blocks count the work of their shares in 31 bits."""
+    a = tree_args(B=60000, mp=1, page=256)
+    a["block_table"] = torch.zeros(1, dtype=I32).expand(60000 * 70000).as_strided((60000, 70000), (0, 0))
+    with pytest.raises(gqa.GqaError, match="not dense"):
+        gqa.gqa_paged_tree_attn(**a)
+
+
+def test_tree_attention_workspace():
+    need = gqa.gqa_paged_tree_attn_workspace(32, 8, 128)
+    assert 152 * 2 * 128 * 520 <= need <= 152 * 2 * 128 * 520 + 65536
+    assert gqa.gqa_paged_tree_attn_workspace(32, 5, 128) == 0 and gqa.gqa_paged_tree_attn_workspace(32, 8, 96) == 0
+
+
 def keep_args(B=2, P=5, h=2, page=16, d=64, dtype=torch.bfloat16):
     return dict(pages=(fake((P, h, page, d), dtype), fake((P, h, page, d), dtype)), block_table=fake((B, 2), I32),
                 qo_indptr=fake((B + 1,), I32), kv_lens=fake((B,), I32), kept=fake((B, 3), I32), num_kept=fake((B,), I32))
