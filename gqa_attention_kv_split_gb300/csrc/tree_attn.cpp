@@ -82,6 +82,7 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a, void* workspace, cudaStream_
   p.row_groups = (int)((std::min<int64_t>(rows, ta::kRows) + 7) / 8);
   const double log2e = 1.4426950408889634;
   p.scale_log2 = (float)(a.scale * log2e);
+  if (p.scale_log2 == 0.f) p.scale_log2 = std::numeric_limits<float>::min();  // (0 times a hidden score's infinity)
   // (a cap at the end of f32's range stays finite, twice itself too)
   const double cap = a.softcap * log2e, most = std::numeric_limits<float>::max() / 2;
   p.cap_out = a.softcap > 0.f ? (float)std::min(cap, most) : 0.f;

@@ -16,9 +16,9 @@
 // weights as TMEM operand.  With 128 rows or fewer a tile of 128 tokens (64 KB in bf16, head
 // dim 128: 1.5 us of an SM's share of HBM) keeps the tensor pipe busy for 0.8 us, however few
 // rows there are, and the softmax for less:
-//  * Replicas.  With 64 (32) rows or fewer each row stands in the M dimension twice (four times),
+//  * Copies.  With 64 (32) rows or fewer each row stands in the M dimension twice (four times),
 //    and each copy weighs a half (a quarter) of a tile's tokens, with zeros in P for the
-//    others: four warps share the softmax evenly, as independent (m, l, o) that join at the end.
+//    others: the warps share the softmax evenly, as independent (m, l, o) that join at the end.
 //  * S in two TMEM buffers: S of the next tile is computed while the softmax works on this one;
 //    P overwrites the S it came from (32 tokens' weights: 16 columns of their first terms, 16
 //    of their second ones).
@@ -31,9 +31,10 @@
 //    the blocks of a gang read the same tokens for other heads or other row blocks.  Pieces of
 //    units that lie in several blocks go to the workspace and a second kernel joins them.
 //  * Warps: 0 and 3 copy K and V (tensor-map TMA, one 128-byte chunk of a head's row for a page
-//    or a tile at a time, into the 128-byte-swizzled layout that both products read), 1 issues S,
-//    2 issues O, 4-7 load the queries, do the softmax (one thread a TMEM lane) and write the
-//    results.  E4M3 pages: 8-11 and 12-15 widen K and V to f16, exactly.
+//    or a tile at a time, into the 128-byte-swizzled layout that both products read), 1 issues the
+//    products (S with the queries as TMEM operand), 4-11 load the queries, do the softmax (one
+//    thread a TMEM lane, two groups in turn) and write the results.  E4M3 pages: 12-15 widen K and V to f16,
+//    exactly.
 //  * Every wait is bounded; a block whose wait expires drains what it started and leaves.
 #pragma once
 #include <cuda.h>
@@ -61,15 +62,16 @@ struct Shape {
   static constexpr bool kFp8 = kCache >= kCacheE4m3;
   static constexpr int kTile = tile_of(D);
   static constexpr int kChunks = D / 64;              // 128-byte chunks of a 16-bit row
-  static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kSlot = kTile * D * 2;         // a tile of K (or of V) as the products read it
   static constexpr int kRaw = kTile * D;              // an E4M3 tile as it is copied
-  // Slots of K and V, and of tiles yet to be widened: what fits beside the queries.
-  static constexpr int kNK = kFp8 ? (D == 64 ? 3 : D == 128 ? 2 : 1) : (D == 64 ? 5 : 3);
-  static constexpr int kNV = kFp8 ? (D == 64 ? 3 : 2) : (D == 64 ? 5 : D == 128 ? 3 : 2);
+  // Slots of K and V, and of tiles yet to be widened.
+  static constexpr int kNK = kFp8 ? (D == 64 ? 3 : 2) : (D == 64 ? 5 : 3);
+  static constexpr int kNV = kNK;  // (the widening warps count both with one number)
   static constexpr int kNR = kFp8 ? (D == 64 ? 4 : 2) : 0;
-  static constexpr int kThreads = kFp8 ? 512 : 256;
-  static constexpr int kData = kQBytes + (kNK + kNV) * kSlot + 2 * kNR * kRaw;
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kData = (kNK + kNV) * kSlot + 2 * kNR * kRaw;
+  // TMEM columns: O, two buffers of S, the queries (two elements a column).
+  static constexpr uint32_t kO = 0, kS = D, kQ = D + 2 * kTile;
   // What starting and ending a unit costs, in tiles.
   static constexpr int kUnitWork = 2;
 };
@@ -77,15 +79,16 @@ struct Shape {
 struct Bars {
   uint64_t k_full[5], k_free[5], v_full[5], v_free[5];      // tiles as the products read them
   uint64_t kr_full[4], kr_free[4], vr_full[4], vr_free[4];  // E4M3 tiles
-  uint64_t s_full[2], p_full[2], p_free[2];
-  uint64_t q_ready, drain[2];
+  uint64_t s_full[2], p_full[2][2], p_free[2];              // buffers of S and P; P by halves of a tile
+  uint64_t q_ready, drain;
 };
 
 template <int kThreads>
 struct Smem {
   Bars bar;
-  float m[kRows], l[kRows];  // of the replicas, at a unit's end
-  float q_up[kRows];         // by what a row's queries were scaled down (bf16 queries as f16)
+  alignas(16) float stage[2][kRows][20];  // 16 columns of the copies' sums, for each half of the columns
+  float m_used[kRows];                 // the maximum that the last tile's weights are relative to
+  float m[2][kRows], l[2][kRows];      // of the groups' copies, at a unit's end (and their queries' largest elements)
   int64_t scan_work[kThreads / 32], scan_turns[kThreads / 32];
   int most[kThreads / 32];
   int64_t total, end, rem;
@@ -232,6 +235,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Arrives at a named barrier that other threads wait at.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // Bits of the tokens key .. key + 31 that lie in [lo, hi).
 __device__ __forceinline__ uint32_t range_bits(int key, int lo, int hi) {
   const int a = lo - key, z = hi - key;
@@ -260,7 +268,7 @@ struct Sight {
 
 namespace {
 
-template <int kCache, int D>
+template <int kCache, int D, bool kCap>
 __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
@@ -269,12 +277,10 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   constexpr bool kQBf16 = kBf16 || kCache == kCacheE4m3;          // q and out
   constexpr int kTile = S::kTile, kThreads = S::kThreads;
   constexpr int kTileShift = kTile == 64 ? 6 : 7;
-  constexpr uint32_t kTmemO = 0, kTmemS = D;                      // columns: O, then two buffers of S
   constexpr float kRaise = 8.f, kShift = kBf16 ? 0.f : 6.f;       // weights are at most 2^(kRaise + kShift)
   uint32_t* const err = &g_tree_attn_err;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* const sq = smem_raw;
-  uint8_t* const sk = sq + S::kQBytes;
+  uint8_t* const sk = smem_raw;
   uint8_t* const sv = sk + S::kNK * S::kSlot;
   uint8_t* const skr = sv + S::kNV * S::kSlot;
   uint8_t* const svr = skr + S::kNR * S::kRaw;
@@ -297,11 +303,12 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.bar.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.bar.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.bar.p_full[i][0]), 4);
+      mbar_init(smem_u32(&sm.bar.p_full[i][1]), 4);
       mbar_init(smem_u32(&sm.bar.p_free[i]), 1);
-      mbar_init(smem_u32(&sm.bar.drain[i]), 1);
     }
-    mbar_init(smem_u32(&sm.bar.q_ready), 4);
+    mbar_init(smem_u32(&sm.bar.drain), 1);
+    mbar_init(smem_u32(&sm.bar.q_ready), 8);
     fence_mbar_init();
   }
   // Launched as a programmatic dependent: what went before on the stream (the append of
@@ -402,6 +409,9 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, err));
   };
+  // The softmax holds a tile's scores of a row in registers (128 of them); the others need few.
+  // (Shares of what the block was launched with: 384 x 168 = 128 x 56 + 256 x 224, or 512 x 128 =
+  // 128 x 64 + 256 x 184 + 128 x 80.)
   bool failed = false;  // a wait of this thread's role expired
   int issued = 0;       // producers: stages issued, up to all of them
 
@@ -479,11 +489,35 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         if (!mbar_wait(smem_u32(&full[i]), i < st ? ph ^ 1 : ph, err)) break;
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- S issuer
-    constexpr uint32_t id = idesc(kBf16, kTile, false);
-    const uint64_t dq = tc::sw128_desc(smem_u32(sq)), dk0 = tc::sw128_desc(smem_u32(sk));
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + kTmemS;
-    int st = 0, ph = 0, j = 0, units = 0;  // slot and its parity; tiles and units so far
+    // ---------------------------------------------------------------- products
+    // S of two tiles ahead, and then O of each tile followed by the S that goes into the buffer
+    // which that O has read: the tensor pipe takes them in this order, so that nothing waits
+    // for a product's end but the softmax.
+    constexpr uint32_t id_s = idesc(kBf16, kTile, false), id_o = idesc(kBf16, D, true);
+    const uint64_t dk0 = tc::sw128_desc(smem_u32(sk)), dv0 = tc::sw128_desc_lbo(smem_u32(sv), kTile * 128);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int ks = 0, kph = 0, vs = 0, vph = 0, units = 0;  // slots of K and V and their parities; units so far
+    int js = 0, j = 0;                                // tiles of S and of O so far
+    auto issue_s = [&] {
+      if (!wait_all(&sm.bar.k_full[ks], kph)) return false;
+      tc::fence_after_thread_sync();
+      const uint64_t dk = dk0 + (uint64_t)(ks * (S::kSlot >> 4));
+      const uint32_t ts = tm + S::kS + (uint32_t)(js & 1) * kTile;
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_f16_tmem_a(ts, tm + S::kQ + 8 * k, dk + (k / 4) * (kTile * 128 >> 4) + 2 * (k % 4), id_s, k > 0);
+        tc::commit(smem_u32(&sm.bar.s_full[js & 1]));
+        tc::commit(smem_u32(&sm.bar.k_free[ks]));
+      }
+      __syncwarp();
+      ++js;
+      if (++ks == S::kNK) {
+        ks = 0;
+        kph ^= 1;
+      }
+      return true;
+    };
     do {
       const int n = walk.count(p);
       if (n == 0) continue;
@@ -492,38 +526,12 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         break;
       }
       ++units;
-      for (int i = 0; i < n; ++i, ++j) {
-        if (!wait_all(&sm.bar.k_full[st], ph) || (j >= 2 && !wait_all(&sm.bar.p_free[j & 1], ((j >> 1) - 1) & 1))) {
-          failed = true;
-          break;
-        }
-        tc::fence_after_thread_sync();
-        const uint64_t dk = dk0 + (uint64_t)(st * (S::kSlot >> 4));
-        const uint32_t ts = tm + (uint32_t)(j & 1) * kTile;
-        if (tc::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc::mma_f16(ts, dq + (k / 4) * (kRows * 128 >> 4) + 2 * (k % 4), dk + (k / 4) * (kTile * 128 >> 4) + 2 * (k % 4), id, k > 0);
-          tc::commit(smem_u32(&sm.bar.s_full[j & 1]));
-          tc::commit(smem_u32(&sm.bar.k_free[st]));
-        }
-        __syncwarp();
-        if (++st == S::kNK) {
-          st = 0;
-          ph ^= 1;
-        }
+      if (!issue_s() || (n > 1 && !issue_s())) {
+        failed = true;
+        break;
       }
-    } while (!failed && walk.next(p));
-  } else if (warp == 2) {
-    // ---------------------------------------------------------------- O issuer
-    constexpr uint32_t id = idesc(kBf16, D, true);
-    const uint64_t dv0 = tc::sw128_desc_lbo(smem_u32(sv), kTile * 128);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    int st = 0, ph = 0, j = 0;
-    do {
-      const int n = walk.count(p);
       for (int i = 0; i < n; ++i, ++j) {
-        if (!wait_all(&sm.bar.v_full[st], ph)) {
+        if (!wait_all(&sm.bar.v_full[vs], vph)) {
           failed = true;
           break;
         }
@@ -535,92 +543,115 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
               if (!walk.seq.hidden(key0 + (x >> 3))) continue;
 #pragma unroll
               for (int ch = 0; ch < S::kChunks; ++ch)
-                *reinterpret_cast<uint4*>(sv + st * S::kSlot + ch * (kTile * 128) + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(sv + vs * S::kSlot + ch * (kTile * 128) + x * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
           }
         }
-        if (!wait_all(&sm.bar.p_full[j & 1], (j >> 1) & 1)) {
+        const uint64_t dv = dv0 + (uint64_t)(vs * (S::kSlot >> 4));
+        const uint32_t tp = tm + S::kS + (uint32_t)(j & 1) * kTile;
+        bool ok = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && wait_all(&sm.bar.p_full[j & 1][h], (j >> 1) & 1);
+          if (!ok) break;
+          tc::fence_after_thread_sync();
+          if (tc::elect_one()) {
+            // K = 16 tokens a product: 8 columns of P (first terms, then second ones), 2048 bytes of V
+#pragma unroll
+            for (int k = h * (kTile / 32); k < (h + 1) * (kTile / 32); ++k) {
+              const uint32_t a = tp + 32 * (k / 2) + 8 * (k % 2);
+              tc::mma_f16_tmem_a(tm + S::kO, a, dv + 128 * k, id_o, (i > 0 || k > 0) ? 1u : 0u);
+              tc::mma_f16_tmem_a(tm + S::kO, a + 16, dv + 128 * k, id_o, 1u);
+            }
+            if (h == 1) {
+              tc::commit(smem_u32(&sm.bar.p_free[j & 1]));
+              tc::commit(smem_u32(&sm.bar.v_free[vs]));
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok || (i + 2 < n && !issue_s())) {
           failed = true;
           break;
         }
-        tc::fence_after_thread_sync();
-        const uint64_t dv = dv0 + (uint64_t)(st * (S::kSlot >> 4));
-        const uint32_t tp = tm + kTmemS + (uint32_t)(j & 1) * kTile;
-        if (tc::elect_one()) {
-          // K = 16 tokens a product: 8 columns of P (first terms, then second ones), 2048 bytes of V
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) {
-            const uint32_t a = tp + 32 * (k / 2) + 8 * (k % 2);
-            tc::mma_f16_tmem_a(tm + kTmemO, a, dv + 128 * k, id, (i > 0 || k > 0) ? 1u : 0u);
-            tc::mma_f16_tmem_a(tm + kTmemO, a + 16, dv + 128 * k, id, 1u);
-          }
-          tc::commit(smem_u32(&sm.bar.p_free[j & 1]));
-          tc::commit(smem_u32(&sm.bar.v_free[st]));
-        }
-        __syncwarp();
-        if (++st == S::kNV) {
-          st = 0;
-          ph ^= 1;
+        if (++vs == S::kNV) {
+          vs = 0;
+          vph ^= 1;
         }
       }
     } while (!failed && walk.next(p));
-  } else if (warp < 8) {
+  } else if (warp == 2) {
+    // (holds its place: groups of four warps read TMEM by their numbers)
+  } else if (warp < 12) {
     // ---------------------------------------------------------------- softmax
-    const int quad = warp - 4, L = 32 * quad + lane;  // TMEM lane
+    // Two groups of four warps take the tiles in turn (and a half of the columns of O and of the
+    // queries each); a thread is a TMEM lane.  A tile's group hands the maximum that it used to
+    // the next one's, so that O has one reference: the groups' phases drift apart, and one loads
+    // scores or waits while the other computes (256 rows of 65536 f16 tokens, 8 sequences: 660 us with
+    // both groups on one tile, half the tokens each; 565 so).
+    const int group = (warp - 4) >> 2, quad = warp & 3, L = 32 * quad + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
-    const float neg = p.scale_log2 < 0.f ? -1.f : 1.f;
+    constexpr int kParts = kTile / 32;
     int j = 0, seg = 0;  // tiles so far; pieces begun
     // Once a wait has expired (failed) nothing more is waited for, computed or written, but the
-    // four warps go on meeting at the units' ends.
+    // warps go on meeting.
     do {
       const SeqT& s = walk.seq;
       const int n = walk.count(p), kvh = walk.kv_head(), r0 = walk.row_begin(), rows = walk.rows();
-      // Copies of each row, a power of two, of `span` rows each
+      // Copies of each row, a power of two, of `span` rows each; copy `rep` weighs the 32-token
+      // parts of a tile that are rep modulo their number.
       const int rep_shift = rows > 64 ? 0 : rows > 32 || kTile == 64 ? 1 : 2;
-      const int span = kRows >> rep_shift, rep = L / span, row = L - rep * span;
+      const int copies = 1 << rep_shift, span = kRows >> rep_shift, rep = L / span, row = L - rep * span;
       const bool live = row < rows;
       const int token = (r0 + (live ? row : 0)) / p.group, head = kvh * p.group + (r0 + (live ? row : 0)) - token * p.group;
       ++seg;
+      float scale = fabsf(p.scale_log2);  // (its sign goes into the queries)
       if (n > 0 && !failed) {
-        // ---- queries: a row is read by D / 8 lanes
-        constexpr int kPer = D / 8, kAt = 32 / kPer;
-#pragma unroll 4
-        for (int i = 0; i < 32; i += kAt) {
-          const int x = 32 * quad + i + lane / kPer, e = lane % kPer, y = x & (span - 1);
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (y < rows) {
-            const int t = (r0 + y) / p.group, h = kvh * p.group + (r0 + y) - t * p.group;
-            v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) + ((s.row0 + t) * p.q_tok + h * p.q_head + 8 * e) * 2);
+        // ---- queries: half a row a thread
+        constexpr int kVec = D / 16;  // 16-byte pieces
+        uint4 v[kVec];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
+                                                          ((s.row0 + token) * p.q_tok + head * p.q_head + group * (D / 2)) * 2);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) v[k] = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t* w = reinterpret_cast<uint32_t*>(v);
+        if (kFp8 && kQBf16) {
+          // bf16 rows enter the f16 product scaled by a power of two that brings their largest
+          // element into [2^15, 2^16): exact but for elements below 2^-29 of it, whose
+          // rounding is at most 2^-40 of the largest.
+          uint32_t mx = 0;
+#pragma unroll
+          for (int k = 0; k < 4 * kVec; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          sm.m[group][L] = __uint_as_float(mx);
+          named_bar_sync(12 + quad, 64);
+          mx = max(mx, __float_as_uint(sm.m[1 - group][L]));
+          named_bar_sync(12 + quad, 64);
+          const int ex = min(max((int)(mx >> 7), 16), 254);  // biased exponent
+          const float down = __uint_as_float((uint32_t)(269 - ex) << 23);
+#pragma unroll
+          for (int k = 0; k < 4 * kVec; ++k) {
+            const float2 f = unpack<true>(w[k]);
+            w[k] = pack<false>(f.x * down, f.y * down);
           }
-          if (kFp8 && kQBf16) {
-            // bf16 rows enter the f16 product scaled by a power of two that brings their largest
-            // element into [2^15, 2^16): exact but for elements below 2^-29 of it, whose
-            // rounding is at most 2^-40 of the largest.
-            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-            uint32_t mx = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = 1; o < kPer; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int ex = min(max((int)(mx >> 7), 16), 254);  // biased exponent
-            const float down = __uint_as_float((uint32_t)(269 - ex) << 23);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = unpack<true>(w[k]);
-              w[k] = pack<false>(f.x * down, f.y * down);
-            }
-            if (e == 0) sm.q_up[x] = __uint_as_float((uint32_t)(ex - 15) << 23);
-          }
-          *reinterpret_cast<uint4*>(sq + (e / 8) * (kRows * 128) + x * 128 + (((e % 8) ^ (x & 7)) << 4)) = v;
+          scale *= __uint_as_float((uint32_t)(ex - 15) << 23);
         }
-        tc::fence_proxy_async_smem();
+        if (p.scale_log2 < 0.f) {
+#pragma unroll
+          for (int k = 0; k < 4 * kVec; ++k) w[k] ^= 0x80008000u;
+        }
+#pragma unroll
+        for (int c = 0; c < 4 * kVec; c += 16)
+          tc::st16(t_lane + S::kQ + group * (D / 4) + c, *reinterpret_cast<uint32_t(*)[16]>(w + c));
+        tc::st_wait();
+        tc::fence_before_thread_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.bar.q_ready));
+      } else if (n > 0 && kFp8 && kQBf16) {
+        named_bar_sync(12 + quad, 64);
+        named_bar_sync(12 + quad, 64);
       }
-      const float up = kFp8 && kQBf16 && n > 0 ? sm.q_up[L] : 1.f;
-      const float scale = p.scale_log2 * up;
       // ---- what this row sees
       Sight see;
       see.base = s.base;
@@ -636,141 +667,143 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
       }
       see.lo = p.window > 0 && pos >= p.window ? pos + 1 - p.window : 0;
       see.sinks = p.window > 0 ? min(p.sinks, see.hi) : 0;
-      if (!live) see.lo = see.hi = see.sinks = 0;
-      // This copy's 32-token parts of a tile
-      const int part0 = (rep * kTile) >> (rep_shift + 5), part1 = ((rep + 1) * kTile) >> (rep_shift + 5);
+      if (!live) {  // a row that is not there: its sums (of zero queries) go nowhere
+        see.lo = 0;
+        see.hi = 0x7fffffff;
+      }
 
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < n && !failed; ++i, ++j) {
-        if (!wait_all(&sm.bar.s_full[j & 1], (j >> 1) & 1)) {
-          failed = true;
-          break;
-        }
+      for (int i = 0; i < n; ++i, ++j) {
+        if ((j & 1) != group) continue;
+        if (!failed && !wait_all(&sm.bar.s_full[group], (j >> 1) & 1)) failed = true;
         tc::fence_after_thread_sync();
-        const uint32_t ts = t_lane + kTmemS + (uint32_t)(j & 1) * kTile;
+        const uint32_t ts = t_lane + S::kS + (uint32_t)group * kTile;
         const int key0 = s.place(walk.t_beg + i) * kTile;
-        // ---- the tile's maximum
-        float mx = -INFINITY;  // of neg * s: the scale's sign aside
-        for (int c = part0; c < part1; ++c) {
-          uint32_t v[32];
-          tc::ld32(ts + 32 * c, v);
+        const bool plain = __all_sync(0xffffffffu, see.lo <= key0 && key0 + kTile <= see.hi);  // nothing is hidden
+        auto hide = [&](uint32_t (&x)[32], int c) {
           const uint32_t vis = see.bits(key0 + 32 * c);
-          tc::ld_wait();
-          if (neg < 0.f) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] ^= 0x80000000u;
-          }
-          if (__all_sync(0xffffffffu, vis == ~0u)) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (vis >> e & 1u) mx = fmaxf(mx, __uint_as_float(v[e]));
-          }
-        }
-        mx = mx == -INFINITY ? mx : mx * neg * scale;
-        if (p.cap_out != 0.f && mx != -INFINITY) mx = capped(mx, p.cap_out, p.cap_inv);
-        const bool raise = mx > m + kRaise || (m == -INFINITY && mx > m);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float alpha = raise ? fast_exp2(m - mx) : 1.f;  // 0 where m was -inf
-          if (i > 0) {
-            // O holds the products of the tiles before this one
-            if (!wait_all(&sm.bar.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) {
-              failed = true;
-              break;
-            }
-            tc::fence_after_thread_sync();
+          for (int e = 0; e < 32; ++e) x[e] = vis >> e & 1u ? x[e] : 0xff800000u;  // -infinity
+        };
+        // ---- the tile's maximum
+        float mx = -INFINITY;
+        if (!failed) {
+          float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (four chains)
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tc::ld32(t_lane + kTmemO + c, o);
-              tc::ld_wait();
+          for (int c = rep; c < kParts; c += copies) {
+            uint32_t v[32];
+            tc::ld32(ts + 32 * c, v);
+            tc::ld_wait();
+            if (!plain) hide(v, c);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc::st32(t_lane + kTmemO + c, o);
-            }
+            for (int e = 0; e < 32; e += 2) y[e / 2 % 4] = max3(y[e / 2 % 4], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
           }
-          if (raise) {
-            l *= alpha;
-            m = mx;
+          mx = max3(fmaxf(y[0], y[1]), y[2], y[3]);
+          if (mx != -INFINITY) mx = kCap ? capped(mx * scale, p.cap_out, p.cap_inv) : mx * scale;
+        }
+        // ---- the maximum in use: what the tile before this one left, raised if it is passed by far
+        if (i > 0) {
+          named_bar_sync(2 + 2 * quad + (j & 1), 64);
+          const float last = sm.m_used[L];
+          l *= m == -INFINITY ? 0.f : fast_exp2(m - last);
+          m = last;
+        }
+        const bool raise = mx > m + kRaise || (m == -INFINITY && mx > m);
+        const float alpha = raise ? fast_exp2(m - mx) : 1.f;  // 0 where m was -inf
+        if (raise) {
+          l *= alpha;
+          m = mx;
+        }
+        if (i + 1 < n) {
+          sm.m_used[L] = m;
+          named_bar_arrive(2 + 2 * quad + ((j + 1) & 1), 64);
+        }
+        if (i > 0 && !failed && __any_sync(0xffffffffu, raise)) {
+          // O holds the products of the tiles before this one
+          if (!wait_all(&sm.bar.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) failed = true;
+          tc::fence_after_thread_sync();
+#pragma unroll 1
+          for (int c = 0; c < D && !failed; c += 16) {  // (16 columns at a time: the tile's scores are live)
+            uint32_t o[16];
+            tc::ld16(t_lane + S::kO + c, o);
+            tc::ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::st16(t_lane + S::kO + c, o);
           }
         }
+        if (failed) continue;
         // ---- weights, in two terms, over the scores that they came from
         const float sub = m == -INFINITY ? 0.f : m - kShift;
         float2 sum = make_float2(0.f, 0.f);
+        const float2 ss = make_float2(kCap ? 1.f : scale, kCap ? 1.f : scale), nn = make_float2(-sub, -sub);
+        // (A loop that is not unrolled: with 64 or 128 tokens in one piece of code the instructions no
+        // longer come fast enough, 608 and 748 us for 565 of the same case.)
 #pragma unroll 1
-        for (int c = 0; c < kTile / 32; ++c) {
+        for (int c = 0; c < kParts; ++c) {
           uint32_t w[32];
-          if (c < part0 || c >= part1) {
+          if ((c & (copies - 1)) == rep) {
+            uint32_t v[32];
+            tc::ld32(ts + 32 * c, v);
+            tc::ld_wait();
+            if (kCap) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(capped(__uint_as_float(v[e]) * scale, p.cap_out, p.cap_inv));
+            }
+            if (!plain) hide(v, c);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 z = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), ss, nn);
+              z.x = fast_exp2(z.x);
+              z.y = fast_exp2(z.y);
+              w[e] = pack<kBf16>(z.x, z.y);
+              const float2 low = __ffma2_rn(unpack<kBf16>(w[e]), make_float2(-1.f, -1.f), z);
+              w[16 + e] = pack<kBf16>(low.x, low.y);
+              sum = __fadd2_rn(sum, z);
+            }
+          } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) w[e] = 0u;
-            tc::st32(ts + 32 * c, w);
-            continue;
-          }
-          uint32_t v[32];
-          tc::ld32(ts + 32 * c, v);
-          const uint32_t vis = see.bits(key0 + 32 * c);
-          const bool all = __all_sync(0xffffffffu, vis == ~0u);
-          tc::ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 x = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-            if (p.cap_out != 0.f) {
-              x.x = capped(x.x * scale, p.cap_out, p.cap_inv) - sub;
-              x.y = capped(x.y * scale, p.cap_out, p.cap_inv) - sub;
-            } else {
-              x = __ffma2_rn(x, make_float2(scale, scale), make_float2(-sub, -sub));
-            }
-            x.x = fast_exp2(x.x);
-            x.y = fast_exp2(x.y);
-            if (!all) {
-              if (!(vis >> (2 * e) & 1u)) x.x = 0.f;
-              if (!(vis >> (2 * e + 1) & 1u)) x.y = 0.f;
-            }
-            w[e] = pack<kBf16>(x.x, x.y);
-            const float2 h = unpack<kBf16>(w[e]);
-            w[16 + e] = pack<kBf16>(x.x - h.x, x.y - h.y);
-            sum = __fadd2_rn(sum, x);
           }
           tc::st32(ts + 32 * c, w);
+          if (c % (kParts / 2) == kParts / 2 - 1) {  // a half of the tile: its product may begin
+            tc::st_wait();
+            tc::fence_before_thread_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.bar.p_full[group][c / (kParts / 2)]));
+          }
         }
         l += sum.x + sum.y;
-        tc::st_wait();
-        tc::fence_before_thread_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.bar.p_full[j & 1]));
       }
       // ---- the unit's (or its piece's) end
       if (n > 0 && !failed) {
         if (!wait_all(&sm.bar.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) failed = true;
         tc::fence_after_thread_sync();
       }
-      // The copies of a row: their maxima and sums
-      float f = 1.f;  // what this copy's sums are multiplied by
-      if (rep_shift > 0) {
-        sm.m[L] = m;
-        sm.l[L] = l;
-        named_bar_sync(1, 128);
-        float mm = -INFINITY, ll = 0.f;
-        for (int x = row; x < kRows; x += span) mm = fmaxf(mm, sm.m[x]);
-        for (int x = row; x < kRows; x += span) ll = fmaf(sm.l[x], sm.m[x] == -INFINITY ? 0.f : fast_exp2(sm.m[x] - mm), ll);
-        f = m == -INFINITY ? 0.f : fast_exp2(m - mm);
-        m = mm;
-        l = ll;
-      }
+      // The copies of a row, and the groups' sums: O is relative to the later group's maximum
+      sm.m[group][L] = m;
+      sm.l[group][L] = l;
+      named_bar_sync(1, 256);
+      const float own = fmaxf(sm.m[0][L], sm.m[1][L]);
+      float mm = -INFINITY, ll = 0.f;
+      for (int x = row; x < kRows; x += span) mm = max3(mm, sm.m[0][x], sm.m[1][x]);
+      for (int x = row; x < kRows; x += span)
+        for (int g = 0; g < 2; ++g) ll = fmaf(sm.l[g][x], sm.m[g][x] == -INFINITY ? 0.f : fast_exp2(sm.m[g][x] - mm), ll);
+      float f = own == -INFINITY ? 0.f : fast_exp2(own - mm);  // what this copy's sums are multiplied by
+      m = mm;
+      l = ll;
+      named_bar_sync(1, 256);  // (they are written again at the next unit's end)
       const bool summed = n > 0 && !failed;  // there is something in O
       if (!summed) f = 0.f;
       const bool whole = walk.whole(), writes = live && rep == 0 && !failed;
       if (whole) f = l == 0.f ? 0.f : f * (p.v_scale / l);
       const int64_t out_row = (s.row0 + token) * p.hq + head;
       const int64_t piece = ((int64_t)blockIdx.x * 2 + (seg == 1 ? 0 : 1)) * kRows + row;
-      float* const stage = reinterpret_cast<float*>(sq) + L * 20;  // (the queries are no longer needed; 16 columns, spread over the banks)
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
+      for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 16) {
         uint32_t o[16];
         if (summed) {
-          tc::ld16(t_lane + kTmemO + c, o);
+          tc::ld16(t_lane + S::kO + c, o);
           tc::ld_wait();
         }
         float x[16];
@@ -779,19 +812,20 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         if (rep_shift > 0) {
           if (rep > 0)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(stage + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-          named_bar_sync(1, 128);
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(&sm.stage[group][L][e]) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          named_bar_sync(10 + group, 128);
           if (rep == 0)
             for (int y = row + span; y < kRows; y += span)
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
-                const float4 z = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(sq) + y * 20 + e);
+                const float4 z = *reinterpret_cast<const float4*>(&sm.stage[group][y][e]);
                 x[e] += z.x;
                 x[e + 1] += z.y;
                 x[e + 2] += z.z;
                 x[e + 3] += z.w;
               }
-          named_bar_sync(1, 128);
+          named_bar_sync(10 + group, 128);
         }
         if (!writes) continue;
         if (whole) {
@@ -808,74 +842,74 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
           for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
       }
-      if (writes) {
+      if (writes && group == 0) {
         if (!whole)
           p.part_ml[piece] = make_float2(m - kShift, l);
         else if (p.lse)
           p.lse[out_row] = l == 0.f ? -INFINITY : (m - kShift) * 0.6931471805599453f + logf(l);
       }
-      if (p.record && L == 0 && walk.t_beg == 0 && !whole && !failed) {
+      if (p.record && L == 0 && group == 0 && walk.t_beg == 0 && !whole && !failed) {
         // The unit begins here; it ends in the gang that has its last tile.
         const int64_t last = sm.end - walk.left + s.tiles - 1;
         p.record[blockIdx.x] = Record{walk.b, walk.unit, gang, share_of(last, sm.total, sm.n_gangs), seg == 1 ? 0 : 1};
       }
+      tc::fence_before_thread_sync();  // (O has been read before the next unit's first weights are there)
     } while (walk.next(p));
   } else {
     // ---------------------------------------------------------------- E4M3 -> f16
+    // K and then V of each tile.
     if constexpr (kFp8) {
-      const bool is_v = warp >= 12;
-      uint64_t* const raw_full = is_v ? sm.bar.vr_full : sm.bar.kr_full;
-      uint64_t* const raw_free = is_v ? sm.bar.vr_free : sm.bar.kr_free;
-      uint64_t* const full = is_v ? sm.bar.v_full : sm.bar.k_full;
-      uint64_t* const free_ = is_v ? sm.bar.v_free : sm.bar.k_free;
-      const uint8_t* const raw = is_v ? svr : skr;
-      uint8_t* const slots = is_v ? sv : sk;
-      const int n_slots = is_v ? S::kNV : S::kNK, t = threadIdx.x & 127;
+      const int t = threadIdx.x & 127;
       int rs = 0, rph = 0, st = 0, ph = 1;
       do {
         const int n = walk.count(p);
-        for (int i = 0; i < n; ++i) {
-          if (!wait_all(&raw_full[rs], rph) || !wait_all(&free_[st], ph)) {
-            failed = true;
-            break;
-          }
+        for (int i = 0; i < n && !failed; ++i) {
           const int key0 = walk.seq.place(walk.t_beg + i) * kTile;
-          const bool edge = is_v && walk.seq.edge(key0, kTile);
-          const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw);
-          uint8_t* dst = slots + st * S::kSlot;
-          constexpr int kPer = D / 16;  // 16-byte pieces of a row
-#pragma unroll 4
-          for (int x = t; x < kTile * kPer; x += 128) {
-            const int key = x / kPer, e = x % kPer;
-            uint4 v = src[x];
-            // Rows that nothing sees may hold anything; 0 * NaN is NaN, so they are zeroed.
-            if (edge && walk.seq.hidden(key0 + key)) v = make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint4 h[2];
-            uint32_t* hw = reinterpret_cast<uint32_t*>(h);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              hw[2 * k] = e4m3_to_f16x2(w[k] & 0xffffu);
-              hw[2 * k + 1] = e4m3_to_f16x2(w[k] >> 16);
+          const bool edge = walk.seq.edge(key0, kTile);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            uint64_t* const raw_full = (kv ? sm.bar.vr_full : sm.bar.kr_full) + rs;
+            uint64_t* const free_ = (kv ? sm.bar.v_free : sm.bar.k_free) + st;
+            if (!wait_all(raw_full, rph) || !wait_all(free_, ph)) {
+              failed = true;
+              break;
             }
-            // (the pieces of odd chunks in the other order: eight lanes then fill all banks)
-            const int flip = (e / 4) & 1;
-            uint8_t* d = dst + (e / 4) * (kTile * 128) + key * 128;
-            const int c0 = 2 * (e % 4) + flip, c1 = 2 * (e % 4) + 1 - flip;
-            *reinterpret_cast<uint4*>(d + ((c0 ^ (key & 7)) << 4)) = flip ? h[1] : h[0];
-            *reinterpret_cast<uint4*>(d + ((c1 ^ (key & 7)) << 4)) = flip ? h[0] : h[1];
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&full[st]));
-            mbar_arrive(smem_u32(&raw_free[rs]));
+            const uint4* src = reinterpret_cast<const uint4*>((kv ? svr : skr) + rs * S::kRaw);
+            uint8_t* dst = (kv ? sv : sk) + st * S::kSlot;
+            constexpr int kPer = D / 16;  // 16-byte pieces of a row
+#pragma unroll 8
+            for (int x = t; x < kTile * kPer; x += 128) {
+              const int key = x / kPer, e = x % kPer;
+              uint4 v = src[x];
+              // Rows of V that nothing sees may hold anything; 0 * NaN is NaN, so they are zeroed.
+              if (edge && kv && walk.seq.hidden(key0 + key)) v = make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              uint4 h[2];
+              uint32_t* hw = reinterpret_cast<uint32_t*>(h);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                hw[2 * k] = e4m3_to_f16x2(w[k] & 0xffffu);
+                hw[2 * k + 1] = e4m3_to_f16x2(w[k] >> 16);
+              }
+              // (the pieces of odd chunks in the other order: eight lanes then fill all banks)
+              const int flip = (e / 4) & 1;
+              uint8_t* d = dst + (e / 4) * (kTile * 128) + key * 128;
+              const int c0 = 2 * (e % 4) + flip, c1 = 2 * (e % 4) + 1 - flip;
+              *reinterpret_cast<uint4*>(d + ((c0 ^ (key & 7)) << 4)) = flip ? h[1] : h[0];
+              *reinterpret_cast<uint4*>(d + ((c1 ^ (key & 7)) << 4)) = flip ? h[0] : h[1];
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_u32((kv ? sm.bar.v_full : sm.bar.k_full) + st));
+              mbar_arrive(smem_u32((kv ? sm.bar.vr_free : sm.bar.kr_free) + rs));
+            }
           }
           if (++rs == S::kNR) {
             rs = 0;
             rph ^= 1;
           }
-          if (++st == n_slots) {
+          if (++st == S::kNK) {
             st = 0;
             ph ^= 1;
           }
@@ -887,11 +921,11 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   // ---------------------------------------------------------------- teardown
   tc::fence_before_thread_sync();
   if (__syncthreads_or(failed)) {
-    // A wait expired: let the products that the issuers started complete before TMEM is freed.
-    if (warp == 1 || warp == 2) {
-      if (tc::elect_one()) tc::commit(smem_u32(&sm.bar.drain[warp - 1]));
+    // A wait expired: let the products that the issuer started complete before TMEM is freed.
+    if (warp == 1) {
+      if (tc::elect_one()) tc::commit(smem_u32(&sm.bar.drain));
       __syncwarp();
-      mbar_wait(smem_u32(&sm.bar.drain[warp - 1]), 0, err);
+      mbar_wait(smem_u32(&sm.bar.drain), 0, err);
     }
     tc::fence_before_thread_sync();
     __syncthreads();
@@ -958,21 +992,20 @@ __global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_consta
   if (lane == 0 && p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
-template <int kCache, int D>
+template <int kCache, int D, bool kCap>
 cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
   using S = Shape<kCache, D>;
   constexpr size_t smem = S::kData + sizeof(Smem<S::kThreads>);
   static_assert(smem <= 227 * 1024, "shared memory");
   static_assert(S::kNK <= 5 && S::kNV <= 5 && S::kNR <= 4, "barrier arrays");
-  static_assert(kRows * 20 * sizeof(float) <= S::kQBytes, "the copies' sums lie where the queries were");
-  static_assert(D + 2 * S::kTile <= 512, "TMEM columns");
+  static_assert(S::kQ + D / 2 <= 512, "TMEM columns");
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(tree_attn_kernel<kCache, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(tree_attn_kernel<kCache, D, kCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
@@ -986,7 +1019,7 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUt
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<kCache, D>, p, k_map, v_map)) != cudaSuccess || !p.record) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<kCache, D, kCap>, p, k_map, v_map)) != cudaSuccess || !p.record) return e;
   cfg.gridDim = dim3(kGrid, p.row_groups);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
@@ -995,10 +1028,11 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUt
 
 template <int kCache>
 cudaError_t launch_cache(const Params& p, int d, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
+  const bool cap = p.cap_out != 0.f;
   switch (d) {
-    case 64: return launch_instance<kCache, 64>(p, k_map, v_map, stream);
-    case 128: return launch_instance<kCache, 128>(p, k_map, v_map, stream);
-    default: return launch_instance<kCache, 256>(p, k_map, v_map, stream);
+    case 64: return cap ? launch_instance<kCache, 64, true>(p, k_map, v_map, stream) : launch_instance<kCache, 64, false>(p, k_map, v_map, stream);
+    case 128: return cap ? launch_instance<kCache, 128, true>(p, k_map, v_map, stream) : launch_instance<kCache, 128, false>(p, k_map, v_map, stream);
+    default: return cap ? launch_instance<kCache, 256, true>(p, k_map, v_map, stream) : launch_instance<kCache, 256, false>(p, k_map, v_map, stream);
   }
 }
 
