@@ -21,7 +21,9 @@ constexpr int tile_of(int d) { return d > 128 ? 64 : 128; }
 
 // For the joining kernel: a unit that begins in one block's share and ends in another's.
 struct Record {
-  int b, unit;      // sequence, unit within it
+  int64_t row0;     // the sequence's first new token
+  int kv_head, row; // the unit: rows [row, row + rows) of a KV head's
+  int rows, lane;   // and its block's place in a gang
   int first, last;  // gangs that have a piece of it; last < 0: no such unit
   int first_slot;   // which of the first gang's two pieces it is (it is the first one of the others)
 };
