@@ -70,8 +70,10 @@ struct Shape {
   static constexpr int kNR = kFp8 ? (D == 64 ? 4 : 2) : 0;
   static constexpr int kThreads = kFp8 ? 512 : 384;
   static constexpr int kData = (kNK + kNV) * kSlot + 2 * kNR * kRaw;
-  // TMEM columns: O, two buffers of S, the queries (two elements a column).
-  static constexpr uint32_t kO = 0, kS = D, kQ = D + 2 * kTile;
+  // TMEM columns: O, the buffers of S (where they fit three, so that a group's next scores are there when
+  // it has done with a tile), and the queries (two elements a column).
+  static constexpr int kBufs = D == 64 ? 3 : 2;
+  static constexpr uint32_t kO = 0, kS = D, kQ = D + kBufs * kTile;
   // What starting and ending a unit costs, in tiles.  (48 sequences of up to 16001 E4M3 tokens with up to 16
   // drafts: 265 us with 2, 254 with 6; 33 of 6007 in bf16 under a window 120.8, 119.1 with 4.)
   static constexpr int kUnitWork = kFp8 ? 6 : 4;
@@ -80,7 +82,7 @@ struct Shape {
 struct Bars {
   uint64_t k_full[5], k_free[5], v_full[5], v_free[5];      // tiles as the products read them
   uint64_t kr_full[4], kr_free[4], vr_full[4], vr_free[4];  // E4M3 tiles
-  uint64_t s_full[2], p_full[2][2], p_free[2];              // buffers of S and P; P by halves of a tile
+  uint64_t s_full[3], p_full[3][2], p_free[3];              // buffers of S and P; P by halves of a tile
   uint64_t q_ready, drain;
 };
 
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
       mbar_init(smem_u32(&sm.bar.vr_full[i]), 1);
       mbar_init(smem_u32(&sm.bar.vr_free[i]), 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(smem_u32(&sm.bar.s_full[i]), 1);
       mbar_init(smem_u32(&sm.bar.p_full[i][0]), 4);
       mbar_init(smem_u32(&sm.bar.p_full[i][1]), 4);
@@ -498,28 +500,28 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
-    // S of two tiles ahead, and then O of each tile followed by the S that goes into the buffer
+    // S of kBufs tiles ahead, and then O of each tile followed by the S that goes into the buffer
     // which that O has read: the tensor pipe takes them in this order, so that nothing waits
     // for a product's end but the softmax.
     constexpr uint32_t id_s = idesc(kBf16, kTile, false), id_o = idesc(kBf16, D, true);
     const uint64_t dk0 = tc::sw128_desc(smem_u32(sk)), dv0 = tc::sw128_desc_lbo(smem_u32(sv), kTile * 128);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     int ks = 0, kph = 0, vs = 0, vph = 0, units = 0;  // slots of K and V and their parities; units so far
-    int js = 0, j = 0;                                // tiles of S and of O so far
+    int sb = 0, pb = 0, pph = 0;                      // buffers of the next S and of the next P, and its parity
     auto issue_s = [&] {
       if (!wait_all(&sm.bar.k_full[ks], kph)) return false;
       tc::fence_after_thread_sync();
       const uint64_t dk = dk0 + (uint64_t)(ks * (S::kSlot >> 4));
-      const uint32_t ts = tm + S::kS + (uint32_t)(js & 1) * kTile;
+      const uint32_t ts = tm + S::kS + (uint32_t)sb * kTile;
       if (tc::elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           tc::mma_f16_tmem_a(ts, tm + S::kQ + 8 * k, dk + (k / 4) * (kTile * 128 >> 4) + 2 * (k % 4), id_s, k > 0);
-        tc::commit(smem_u32(&sm.bar.s_full[js & 1]));
+        tc::commit(smem_u32(&sm.bar.s_full[sb]));
         tc::commit(smem_u32(&sm.bar.k_free[ks]));
       }
       __syncwarp();
-      ++js;
+      if (++sb == S::kBufs) sb = 0;
       if (++ks == S::kNK) {
         ks = 0;
         kph ^= 1;
@@ -534,11 +536,8 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         break;
       }
       ++units;
-      if (!issue_s() || (n > 1 && !issue_s())) {
-        failed = true;
-        break;
-      }
-      for (int i = 0; i < n; ++i, ++j) {
+      for (int i = 0; i < S::kBufs && i < n && !failed; ++i) failed = !issue_s();
+      for (int i = 0; i < n && !failed; ++i) {
         if (!wait_all(&sm.bar.v_full[vs], vph)) {
           failed = true;
           break;
@@ -558,11 +557,11 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
           }
         }
         const uint64_t dv = dv0 + (uint64_t)(vs * (S::kSlot >> 4));
-        const uint32_t tp = tm + S::kS + (uint32_t)(j & 1) * kTile;
+        const uint32_t tp = tm + S::kS + (uint32_t)pb * kTile;
         bool ok = true;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          ok = ok && wait_all(&sm.bar.p_full[j & 1][h], (j >> 1) & 1);
+          ok = ok && wait_all(&sm.bar.p_full[pb][h], pph);
           if (!ok) break;
           tc::fence_after_thread_sync();
           if (tc::elect_one()) {
@@ -574,15 +573,19 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
               tc::mma_f16_tmem_a(tm + S::kO, a + 16, dv + 128 * k, id_o, 1u);
             }
             if (h == 1) {
-              tc::commit(smem_u32(&sm.bar.p_free[j & 1]));
+              tc::commit(smem_u32(&sm.bar.p_free[pb]));
               tc::commit(smem_u32(&sm.bar.v_free[vs]));
             }
           }
           __syncwarp();
         }
-        if (!ok || (i + 2 < n && !issue_s())) {
+        if (!ok || (i + S::kBufs < n && !issue_s())) {
           failed = true;
           break;
+        }
+        if (++pb == S::kBufs) {
+          pb = 0;
+          pph ^= 1;
         }
         if (++vs == S::kNV) {
           vs = 0;
@@ -602,7 +605,10 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
     const int group = (warp - 4) >> 2, quad = warp & 3, L = 32 * quad + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
     constexpr int kParts = kTile / 32;
-    int j = 0, seg = 0;  // tiles so far; pieces begun
+    int j = 0, seg = 0;     // tiles so far; pieces begun
+    int buf = 0, bph = 0;   // the next tile's buffer and its parity
+    auto last_buf = [&] { return buf == 0 ? S::kBufs - 1 : buf - 1; };  // the buffer before it
+    auto last_ph = [&] { return buf == 0 ? bph ^ 1 : bph; };
     // Once a wait has expired (failed) nothing more is waited for, computed or written, but the
     // warps go on meeting.
     do {
@@ -681,11 +687,18 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
       }
 
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < n; ++i, ++j) {
+      auto advance = [&] {
+        ++j;
+        if (++buf == S::kBufs) {
+          buf = 0;
+          bph ^= 1;
+        }
+      };
+      for (int i = 0; i < n; ++i, advance()) {
         if ((j & 1) != group) continue;
-        if (!failed && !wait_all(&sm.bar.s_full[group], (j >> 1) & 1)) failed = true;
+        if (!failed && !wait_all(&sm.bar.s_full[buf], bph)) failed = true;
         tc::fence_after_thread_sync();
-        const uint32_t ts = t_lane + S::kS + (uint32_t)group * kTile;
+        const uint32_t ts = t_lane + S::kS + (uint32_t)buf * kTile;
         const int key0 = s.place(walk.t_beg + i) * kTile;
         const bool plain = __all_sync(0xffffffffu, see.lo <= key0 && key0 + kTile <= see.hi);  // nothing is hidden
         auto hide = [&](uint32_t (&x)[32], int c) {
@@ -728,7 +741,7 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         }
         if (i > 0 && !failed && __any_sync(0xffffffffu, raise)) {
           // O holds the products of the tiles before this one
-          if (!wait_all(&sm.bar.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) failed = true;
+          if (!wait_all(&sm.bar.p_free[last_buf()], last_ph())) failed = true;
           tc::fence_after_thread_sync();
 #pragma unroll 1
           for (int c = 0; c < D && !failed; c += 16) {  // (16 columns at a time: the tile's scores are live)
@@ -778,14 +791,14 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
             tc::st_wait();
             tc::fence_before_thread_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.bar.p_full[group][c / (kParts / 2)]));
+            if (lane == 0) mbar_arrive(smem_u32(&sm.bar.p_full[buf][c / (kParts / 2)]));
           }
         }
         l += sum.x + sum.y;
       }
       // ---- the unit's (or its piece's) end
       if (n > 0 && !failed) {
-        if (!wait_all(&sm.bar.p_free[(j - 1) & 1], ((j - 1) >> 1) & 1)) failed = true;
+        if (!wait_all(&sm.bar.p_free[last_buf()], last_ph())) failed = true;
         tc::fence_after_thread_sync();
       }
       // The copies of a row, and the groups' sums: O is relative to the later group's maximum
