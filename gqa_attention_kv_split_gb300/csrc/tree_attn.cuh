@@ -217,9 +217,11 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
-__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
+// Four E4M3 bytes -> four f16, exactly.
+__device__ __forceinline__ uint2 widen(uint32_t four) {
+  uint2 d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d.x) : "h"((uint16_t)(four & 0xffffu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d.y) : "h"((uint16_t)(four >> 16)));
   return d;
 }
 template <bool kBf16>
@@ -892,7 +894,13 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
     // ---------------------------------------------------------------- E4M3 -> f16
     // K and then V of each tile.
     if constexpr (kFp8) {
-      const int t = threadIdx.x & 127;
+      // A thread's 16-byte pieces of a tile: one column of them, every 128 / kPer-th row (a multiple of 8, so
+      // that its place in a swizzled row is the same), each two pieces of f16.  Those of odd chunks go in
+      // the other order: eight lanes then fill all banks.
+      constexpr int kPer = D / 16, kRowStep = 128 / kPer, kMine = kTile / kRowStep;
+      const int t = threadIdx.x & 127, e = t % kPer, row0 = t / kPer;
+      const bool flip = (e / 4) & 1;
+      const uint32_t first = (uint32_t)((e / 4) * (kTile * 128) + row0 * 128 + (((2 * (e % 4) + (flip ? 1 : 0)) ^ (row0 & 7)) << 4));
       int rs = 0, rph = 0, st = 0, ph = 1;
       do {
         const int n = walk.count(p);
@@ -903,44 +911,39 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
           for (int kv = 0; kv < 2; ++kv) {
             uint64_t* const raw_full = (kv ? sm.bar.vr_full : sm.bar.kr_full) + rs;
             uint64_t* const free_ = (kv ? sm.bar.v_free : sm.bar.k_free) + st;
-            if (!wait_all(raw_full, rph) || !wait_all(free_, ph)) {
+            if (!wait_all(raw_full, rph)) {
               failed = true;
               break;
             }
             const uint4* src = reinterpret_cast<const uint4*>((kv ? svr : skr) + rs * S::kRaw);
             uint8_t* dst = (kv ? sv : sk) + st * S::kSlot;
-            constexpr int kPer = D / 16;  // 16-byte pieces of a row
-            constexpr int kMine = kTile * kPer / 128;
             // (all loads before the first store: the compiler cannot know that they are of other bytes)
             uint4 v[kMine];
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) v[i] = src[t + 128 * i];
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-              const int x = t + 128 * i, key = x / kPer, e = x % kPer;
+            for (int k = 0; k < kMine; ++k) v[k] = src[t + 128 * k];
+            if (!wait_all(free_, ph)) {
+              failed = true;
+              break;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32((kv ? sm.bar.vr_free : sm.bar.kr_free) + rs));  // (it is in registers)
+            if (edge && kv) {
               // Rows of V that nothing sees may hold anything; 0 * NaN is NaN, so they are zeroed.
-              if (edge && kv && walk.seq.hidden(key0 + key)) v[i] = make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-              uint4 h[2];
-              uint32_t* hw = reinterpret_cast<uint32_t*>(h);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                hw[2 * k] = e4m3_to_f16x2(w[k] & 0xffffu);
-                hw[2 * k + 1] = e4m3_to_f16x2(w[k] >> 16);
-              }
-              // (the pieces of odd chunks in the other order: eight lanes then fill all banks)
-              const int flip = (e / 4) & 1;
-              uint8_t* d = dst + (e / 4) * (kTile * 128) + key * 128;
-              const int c0 = 2 * (e % 4) + flip, c1 = 2 * (e % 4) + 1 - flip;
-              *reinterpret_cast<uint4*>(d + ((c0 ^ (key & 7)) << 4)) = flip ? h[1] : h[0];
-              *reinterpret_cast<uint4*>(d + ((c1 ^ (key & 7)) << 4)) = flip ? h[0] : h[1];
+              for (int k = 0; k < kMine; ++k)
+                if (walk.seq.hidden(key0 + row0 + kRowStep * k)) v[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) {
+              const uint2 a = widen(flip ? v[k].z : v[k].x), b = widen(flip ? v[k].w : v[k].y);
+              const uint2 c = widen(flip ? v[k].x : v[k].z), d = widen(flip ? v[k].y : v[k].w);
+              uint8_t* to = dst + k * (kRowStep * 128);
+              *reinterpret_cast<uint4*>(to + first) = make_uint4(a.x, a.y, b.x, b.y);
+              *reinterpret_cast<uint4*>(to + (first ^ 16)) = make_uint4(c.x, c.y, d.x, d.y);
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_u32((kv ? sm.bar.v_full : sm.bar.k_full) + st));
-              mbar_arrive(smem_u32((kv ? sm.bar.vr_free : sm.bar.kr_free) + rs));
-            }
+            if (lane == 0) mbar_arrive(smem_u32((kv ? sm.bar.v_full : sm.bar.k_full) + st));
           }
           if (++rs == S::kNR) {
             rs = 0;
