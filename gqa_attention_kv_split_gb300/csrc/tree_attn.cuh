@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
             const float2 f = unpack<true>(w[k]);
             w[k] = pack<false>(f.x * down, f.y * down);
           }
-          scale *= __uint_as_float((uint32_t)(ex - 15) << 23);
+          scale = fmaxf(scale * __uint_as_float((uint32_t)(ex - 15) << 23), 1.17549435e-38f);  // (not 0: hidden scores are infinities)
         }
         if (p.scale_log2 < 0.f) {
 #pragma unroll

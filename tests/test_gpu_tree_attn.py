@@ -127,6 +127,14 @@ def test_scales_caps_and_signs():
     Batch([9, 30], [300, 40], d=128, dtype=F16, cache=E4M3, seed=2).check(k_scale=0.06, v_scale=0.03, softcap=30.0)
 
 
+def test_scales_next_to_nothing():
+    """Rows of zeros and scales whose product with a row's own power of two would be 0: every token weighs the same."""
+    for scale in (1e-30, 1e-38, 0.0):
+        b = Batch([9, 3], [300, 40], d=64, dtype=BF16, cache=E4M3, seed=22)
+        b.q[:5] = 0
+        b.check(k_scale=1e-7, q_scale=scale)
+
+
 def test_maxima_that_grow():
     """Keys whose scores rise along the sequence: the maximum in use is passed again and again, by a little and by a lot."""
     for dtype, cache in TYPES:
