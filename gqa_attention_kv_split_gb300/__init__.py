@@ -392,8 +392,9 @@ def gqa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, *, out=None, lse=
     include/gqa.h): q [B,Hq,D] f16 or bf16, k_pages / v_pages
     [num_pages,Hkv,page_size,D] of q's type or E4M3, in any order in memory,
     block_table [B,max_pages_per_seq] and seq_lens [B] int32.  Under a window
-    the first `sinks` tokens stay visible.  Writes `lse` [B,Hq] f32 if given.  The workspace is the library's for the stream (in
-    a captured call: one from the graph's memory pool) unless one of at least
+    the first `sinks` tokens stay visible.  Writes `lse` [B,Hq] f32 if given.
+    The workspace is the library's for the stream (in a captured call: one
+    from the graph's memory pool) unless one of at least
     gqa_paged_attn_workspace(Hq, Hkv, D) bytes (uint8) is given; calls that
     can run at the same time need one each."""
     if out is None:

@@ -1,5 +1,6 @@
-// api.cpp -- the C ABI of libgqa (include/gqa.h): argument validation,
-// device scoping, workspace ownership, host-buffer staging and launch.
+// api.cpp -- the C ABI of libgqa (include/gqa.h): argument validation, device
+// scoping, workspace ownership, host-buffer staging and launch of the decodes and the
+// context attention (the entry points of paged caches: api_paged.cpp).
 //
 // Launcher conventions follow "FlashInfer NVFP4 QKV GEMM 최적화: SM103a
 // Epilogue 통합 및 CUDA 런처 개선", section 2: every tensor must sit on one
@@ -7,7 +8,6 @@
 // restores the caller's (no current-device check), and a launch grid must be
 // positive.  Nothing here computes attention; every step of the path runs in
 // the kernels of decode.cu and ctx_nvfp4.cu.
-
 #include "api_util.h"
 #include "kernels.h"
 #include "paged.h"
@@ -33,7 +33,7 @@ extern "C" {
 
 const char* gqa_last_error(void) { return t_last_error.c_str(); }
 
-int gqa_version(void) { return 401; }  // 0.4.1: caps of any size, workspaces of per-thread streams, every offset checked
+int gqa_version(void) { return 500; }  // 0.5.0: drafted tokens over paged caches, head norms, sinks
 
 namespace {
 gqa_status decode_impl(const void* q, const void* kv, const int32_t* seq_lens, void* out, int64_t batch,

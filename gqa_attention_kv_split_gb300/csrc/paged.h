@@ -1,6 +1,6 @@
-// paged.h -- interface between the C-ABI host layer (api.cpp) and the kernels that fill
-// and read paged caches of any layout: the append (append.cu) and the one-token
-// attention (paged_attn.cpp).
+// paged.h -- interface between the C-ABI host layer (api_paged.cpp) and the kernels that
+// fill and read paged caches of any layout: the append (append.cuh), the one-token
+// attention (paged_attn.cpp), and masks and compaction of drafted tokens (drafts.cu).
 #pragma once
 #include <cuda_runtime.h>
 

@@ -36,6 +36,10 @@
 //    thread a TMEM lane, two groups in turn) and write the results.  E4M3 pages: 12-15 widen K and V to f16,
 //    exactly.
 //  * Every wait is bounded; a block whose wait expires drains what it started and leaves.
+//
+// Measured on GB300 (time in a graph): 16 sequences of 16384 tokens, 32/8 heads of 128, bf16, 8 drafts: 169 us,
+// 6.38 TB/s; 64 drafts: 298 us, 919 TFLOP/s; 8 of 65536, f16, 64 drafts: 566 us, 970 TFLOP/s; 48 of up to 16001, 64/8
+// heads, E4M3, up to 16 drafts: 244 us, 3.3 TB/s; one of 2048 tokens, 8 drafts: 21 us.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -421,9 +425,6 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, err));
   };
-  // The softmax holds a tile's scores of a row in registers (128 of them); the others need few.
-  // (Shares of what the block was launched with: 384 x 168 = 128 x 56 + 256 x 224, or 512 x 128 =
-  // 128 x 64 + 256 x 184 + 128 x 80.)
   bool failed = false;  // a wait of this thread's role expired
   int issued = 0;       // producers: stages issued, up to all of them
 

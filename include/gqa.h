@@ -1,16 +1,19 @@
 /*
  * gqa.h -- C ABI of libgqa: grouped-query attention kernels for NVIDIA GB300
  * (sm_103a), head_dim 128, 32 query heads over 8 KV heads (4 query heads per
- * KV head); for paged caches of other layouts the append and the attention of
- * one token, whose descriptors give the sizes.
+ * KV head); for paged caches of other layouts the append, the attention of one
+ * token and what a step with drafted tokens needs (their masks, their attention
+ * and the compaction of the accepted ones), whose descriptors give the sizes.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Pointers.  Every tensor argument is a plain pointer to a dense, row-major
  * (C-contiguous) array with the shape stated below; the entry points of other
- * cache layouts (gqa_paged_append_t, nvfp4_paged_append_t, gqa_paged_attn_t)
- * also take strided ones, and device memory only.  All tensor pointers of one
- * call must be either
+ * cache layouts (gqa_paged_append_t, gqa_paged_norm_append_t,
+ * nvfp4_paged_append_t, nvfp4_paged_norm_append_t, gqa_paged_attn_t,
+ * gqa_paged_window_attn_t, gqa_paged_tree_attn_t, gqa_paged_keep_t) also take
+ * strided ones, and they and gqa_tree_mask_t device memory only.  All tensor
+ * pointers of one call must be either
  *   - device memory of one and the same CUDA device (cudaMalloc'd, managed,
  *     or a PyTorch CUDA tensor's data pointer): the call enqueues its kernels
  *     on `stream` and returns without synchronising; or
@@ -34,7 +37,8 @@
  * gqa_release_workspace().  Two calls on the same stream are ordered by the
  * stream; calls on different streams use different workspaces.
  * cudaStreamPerThread counts as one stream of each host thread;
- * gqa_paged_attn_t's workspace for it is released when the thread ends.
+ * the workspaces of gqa_paged_attn_t, gqa_paged_window_attn_t and
+ * gqa_paged_tree_attn_t for it are released when the thread ends.
  *
  * Errors.  Every entry point returns a gqa_status; GQA_OK means the work was
  * validated and enqueued (device pointers) or completed (host pointers).  On
@@ -63,7 +67,7 @@ typedef enum gqa_status {
   GQA_ERR_CUDA = 4,               /* a CUDA runtime call failed */
   GQA_ERR_OOM = 5,                /* workspace allocation failed */
   GQA_ERR_TIMEOUT = 6,            /* a kernel's bounded wait expired (see gqa_check_device_errors) */
-  GQA_ERR_WORKSPACE = 7           /* a captured call without a workspace (see gqa_paged_attn_t) */
+  GQA_ERR_WORKSPACE = 7           /* a captured call without a workspace (see gqa_paged_attn_t, gqa_paged_tree_attn_t) */
 } gqa_status;
 
 /*
@@ -632,7 +636,7 @@ int64_t gqa_paged_tree_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t
  *
  * A sequence whose kept tokens do not rise, or do not lie in its draft, or which is
  * shorter than its draft, is left as it is (new_lens[b] = kv_lens[b]; bit 1 of the
- * error word, or bit 2 where its offsets fall).  A row whose old or new place lies
+ * error word unless it keeps nothing, or bit 2 where its offsets fall).  A row whose old or new place lies
  * outside the block table or the pages stays where it is and sets bit 1.  Sequences
  * that share a page must not both move rows in it.  Device tensors only; no
  * workspace; one kernel; the same bits whatever the order.
@@ -644,8 +648,9 @@ gqa_status gqa_paged_keep_t(const gqa_tensor* const* pages, int num_tensors, con
 /*
  * gqa_check_device_errors -- synchronise `device` and return (then clear)
  * the kernels' device error word in *word: bit 0 = a bounded wait expired,
- * bit 1 = an out-of-range page index (or an appended position) was skipped, bit 2 = qo_indptr was not
- * non-decreasing from 0 to total_q, bit 3 = the dequantisation export's
+ * bit 1 = an out-of-range page index, position of a token, parent of a tree or list of
+ * kept tokens was skipped, bit 2 = qo_indptr was not non-decreasing from 0 to total_q
+ * (to at most total where rows behind it are allowed), bit 3 = the dequantisation export's
  * self-check failed.  Returns GQA_ERR_TIMEOUT when bit 0 is set,
  * GQA_ERR_INVALID_ARG when another bit is set, GQA_OK when the word is 0.
  * After a timeout the outputs of the affected call are unspecified; every
