@@ -334,74 +334,108 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   if (threadIdx.x == 0 && p.record) p.record[blockIdx.x].last = -1;
 
   // ---- this block's share ------------------------------------------------------
-  // Each thread sums the work of a contiguous range of sequences; a scan over the threads
-  // gives the ranges' starts, and the range that holds the share's first piece of work is
-  // walked by its thread.
+  // Work is counted and scanned over the sequences; the share's first piece of work lies in the sequence
+  // whose work covers it.
   using SeqT = Seq<kTile>;
-  const int64_t per = (p.batch + kThreads - 1) / kThreads;
-  const int64_t s0 = threadIdx.x * per < p.batch ? threadIdx.x * per : p.batch;
-  const int64_t s1 = s0 + per < p.batch ? s0 + per : p.batch;
   auto turns_of = [&](const SeqT& s) { return s.tiles == 0 ? 0 : (p.hkv * s.blocks) >> p.gang_shift; };
-  int64_t work = 0, turns = 0;
-  int most = 0;
-  bool bare = false;  // a sequence without a cached token?
-  for (int64_t b = s0; b < s1; ++b) {
-    const SeqT s(p, (int)b);
+  auto flag = [&](const SeqT& s, int64_t b) {
     if (blockIdx.x == 0 && (s.bad || (b == 0 && s.row0 != 0))) atomicOr(err, kErrBadIndptr);
-    const int64_t t = turns_of(s);
-    turns += t;
-    work += t * (s.tiles + S::kUnitWork);
-    most = max(most, s.tiles);
-    bare |= s.n > 0 && s.tiles == 0;
-  }
-  int64_t iw = work, it = turns;
+  };
+  bool by_unit, bare = false;  // in whole units; a sequence without a cached token?
+  int n_gangs, b0 = 0;         // gangs with a share: none is empty; the share's first sequence
+  int64_t total, beg, end, rem = 0;
+  auto shares = [&](int most, int64_t total_w, int64_t total_t) {
+    by_unit = most <= kWholeTiles && total_t <= gangs;
+    total = by_unit ? total_t : total_w;
+    n_gangs = total < gangs ? (int)total : gangs;
+    beg = gang < n_gangs ? share_begin(gang, total, n_gangs) : 0;
+    end = gang < n_gangs ? share_begin(gang + 1, total, n_gangs) : 0;
+  };
+  if (p.few) {
+    // Up to 32 sequences, less than 2^31 of work: a lane each, and each warp for itself (nothing to meet for:
+    // one sequence of 2048 tokens 1 us sooner).
+    const bool in = lane < p.batch;
+    const SeqT s(p, in ? lane : 0);
+    if (in && warp == 0) flag(s, lane);
+    const int t = in ? turns_of(s) : 0, w = t * (s.tiles + S::kUnitWork);
+    int it = t, iw = w;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t a = __shfl_up_sync(0xffffffffu, iw, d), c = __shfl_up_sync(0xffffffffu, it, d);
-    if (lane >= d) {
-      iw += a;
-      it += c;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, it, d), c = __shfl_up_sync(0xffffffffu, iw, d);
+      if (lane >= d) {
+        it += a;
+        iw += c;
+      }
+    }
+    bare = __any_sync(0xffffffffu, in && s.n > 0 && s.tiles == 0);
+    shares(__reduce_max_sync(0xffffffffu, in ? s.tiles : 0), __shfl_sync(0xffffffffu, iw, 31), __shfl_sync(0xffffffffu, it, 31));
+    const int mine = by_unit ? t : w, before = (by_unit ? it : iw) - mine;
+    const uint32_t who = __ballot_sync(0xffffffffu, beg < end && beg >= before && beg < before + mine);
+    if (who) b0 = __ffs(who) - 1;
+    rem = beg - __shfl_sync(0xffffffffu, before, b0);
+  } else {
+    // Each thread sums the work of a contiguous range of sequences; a scan over the threads
+    // gives the ranges' starts, and the range that holds the share's first piece of work is
+    // walked by its thread.
+    const int64_t per = (p.batch + kThreads - 1) / kThreads;
+    const int64_t s0 = threadIdx.x * per < p.batch ? threadIdx.x * per : p.batch;
+    const int64_t s1 = s0 + per < p.batch ? s0 + per : p.batch;
+    int64_t work = 0, turns = 0;
+    int most = 0;
+    for (int64_t b = s0; b < s1; ++b) {
+      const SeqT s(p, (int)b);
+      flag(s, b);
+      const int64_t t = turns_of(s);
+      turns += t;
+      work += t * (s.tiles + S::kUnitWork);
+      most = max(most, s.tiles);
+      bare |= s.n > 0 && s.tiles == 0;
+    }
+    int64_t iw = work, it = turns;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, iw, d), c = __shfl_up_sync(0xffffffffu, it, d);
+      if (lane >= d) {
+        iw += a;
+        it += c;
+      }
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) {
+      sm.scan_work[warp] = iw;
+      sm.scan_turns[warp] = it;
+      sm.most[warp] = most;
+    }
+    bare = __syncthreads_or(bare);
+    int64_t before_w = 0, before_t = 0, total_w = 0, total_t = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) {
+        before_w += sm.scan_work[w];
+        before_t += sm.scan_turns[w];
+      }
+      total_w += sm.scan_work[w];
+      total_t += sm.scan_turns[w];
+      most = max(most, sm.most[w]);
+    }
+    shares(most, total_w, total_t);
+    const int64_t before = by_unit ? before_t + it - turns : before_w + iw - work, mine = by_unit ? turns : work;
+    if (beg < end && beg >= before && beg < before + mine) {
+      int64_t left = beg - before;
+      int64_t b = s0;
+      for (;; ++b) {
+        const SeqT s(p, (int)b);
+        const int64_t t = turns_of(s), w = by_unit ? t : t * (s.tiles + S::kUnitWork);
+        if (left < w) break;
+        left -= w;
+      }
+      sm.b0 = (int)b;
+      sm.rem = left;
     }
   }
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 31) {
-    sm.scan_work[warp] = iw;
-    sm.scan_turns[warp] = it;
-    sm.most[warp] = most;
-  }
-  bare = __syncthreads_or(bare);
-  int64_t before_w = 0, before_t = 0, total_w = 0, total_t = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) {
-      before_w += sm.scan_work[w];
-      before_t += sm.scan_turns[w];
-    }
-    total_w += sm.scan_work[w];
-    total_t += sm.scan_turns[w];
-    most = max(most, sm.most[w]);
-  }
-  const bool by_unit = most <= kWholeTiles && total_t <= gangs;
-  const int64_t before = by_unit ? before_t + it - turns : before_w + iw - work;
-  const int64_t total = by_unit ? total_t : total_w, mine = by_unit ? turns : work;
-  const int n_gangs = total < gangs ? (int)total : gangs;  // gangs with a share: none is empty
-  const int64_t beg = gang < n_gangs ? share_begin(gang, total, n_gangs) : 0;
-  const int64_t end = gang < n_gangs ? share_begin(gang + 1, total, n_gangs) : 0;
   if (threadIdx.x == 0) {
     sm.total = total;
     sm.n_gangs = n_gangs;
     sm.end = end;
-  }
-  if (beg < end && beg >= before && beg < before + mine) {
-    int64_t rem = beg - before;
-    int64_t b = s0;
-    for (;; ++b) {
-      const SeqT s(p, (int)b);
-      const int64_t t = turns_of(s), w = by_unit ? t : t * (s.tiles + S::kUnitWork);
-      if (rem < w) break;
-      rem -= w;
-    }
-    sm.b0 = (int)b;
-    sm.rem = rem;
   }
   // Rows of sequences without a cached token: zeros.
   for (int64_t b = blockIdx.x; bare && b < p.batch; b += kGrid) {
@@ -417,7 +451,11 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   tc::fence_after_thread_sync();
   const uint32_t tmem = sm.tmem;
   const bool has_share = beg < end;
-  Walk<kTile, S::kUnitWork> walk(p, has_share ? (int)(end - beg) : 0, has_share ? sm.b0 : 0, has_share ? sm.rem : 0, by_unit);
+  if (!p.few && has_share) {
+    b0 = sm.b0;
+    rem = sm.rem;
+  }
+  Walk<kTile, S::kUnitWork> walk(p, has_share ? (int)(end - beg) : 0, b0, has_share ? rem : 0, by_unit);
   if (!has_share || !walk.valid()) {  // (or a share that lies before a unit's first tile)
     if (warp == 1) tc::tmem_dealloc(tmem, 512);
     return;
@@ -842,13 +880,14 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
           }
           named_bar_sync(10 + group, 128);
           for (int y = L >> 2; y < rows && !failed; y += 32) {
-            float4 u = *reinterpret_cast<const float4*>(&sm.stage[group][y][4 * (L & 3)]);
-            for (int z = y + span; z < kRows; z += span) {
-              const float4 w = *reinterpret_cast<const float4*>(&sm.stage[group][z][4 * (L & 3)]);
-              u.x += w.x;
-              u.y += w.y;
-              u.z += w.z;
-              u.w += w.w;
+            const float* const from = &sm.stage[group][y][4 * (L & 3)];
+            auto copy = [&](int n) { return *reinterpret_cast<const float4*>(from + n * span * 20); };
+            float4 u = copy(0);
+            const float4 w = copy(1);
+            u = make_float4(u.x + w.x, u.y + w.y, u.z + w.z, u.w + w.w);
+            if (rep_shift > 1) {
+              const float4 a = copy(2), b = copy(3);
+              u = make_float4(u.x + (a.x + b.x), u.y + (a.y + b.y), u.z + (a.z + b.z), u.w + (a.w + b.w));
             }
             const int d = c + 4 * (L & 3);
             if (whole) {
@@ -989,35 +1028,50 @@ __device__ __forceinline__ void load_l2(const float* p, float (&v)[kN]) {
 }
 
 // Joins the pieces of the units that lie in several blocks' shares, in the order of their
-// tiles: a warp per row, a few pieces' loads in flight.
+// tiles: a warp per row.  Up to 32 pieces' maxima and sums come at once, a lane each, and their
+// outputs kBatch at a time, none of which waits for another: one sequence's 20 pieces are two trips to L2.
 template <int D, bool kQBf16>
 __global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ Params p) {
-  constexpr int kN = D / 32, kBatch = D > 128 ? 6 : 8;
+  constexpr int kN = D / 32, kBatch = 32 / kN;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Record u = p.record[blockIdx.x];
   const int lane = threadIdx.x & 31, row = (int)blockIdx.y * 8 + ((int)threadIdx.x >> 5);
   if (u.last < 0 || row >= u.rows) return;
+  auto piece = [&](int c) { return (int64_t)(2 * ((c << p.gang_shift) + u.lane) + (c == u.first ? u.first_slot : 0)) * kRows + row; };
   float m = -INFINITY, l = 0.f, x[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) x[i] = 0.f;
-  for (int c0 = u.first; c0 <= u.last; c0 += kBatch) {
-    float ml[kBatch][2], v[kBatch][kN];
+  for (int c1 = u.first; c1 <= u.last; c1 += 32) {
+    const int count = min(32, u.last + 1 - c1);
+    float ml[2] = {-INFINITY, 0.f};
+    if (lane < count) load_l2<2>(reinterpret_cast<const float*>(p.part_ml + piece(c1 + lane)), ml);
+    float f = 1.f, g = 0.f;  // what the sums so far, and this lane's piece, are multiplied by
+    for (int c0 = 0; c0 < count; c0 += kBatch) {
+      float v[kBatch][kN];
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int c = min(c0 + e, u.last);
-      const int64_t at = (int64_t)(2 * ((c << p.gang_shift) + u.lane) + (c == u.first ? u.first_slot : 0)) * kRows + row;
-      load_l2<2>(reinterpret_cast<const float*>(p.part_ml + at), ml[e]);
-      load_l2<kN>(p.part_o + at * D + lane * kN, v[e]);
-    }
+      for (int e = 0; e < kBatch; ++e)
+        if (c0 + e < count) load_l2<kN>(p.part_o + piece(c1 + c0 + e) * D + lane * kN, v[e]);
+      if (c0 == 0) {
+        float mn = fmaxf(m, ml[0]);
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      if (c0 + e > u.last) break;
-      const float mn = fmaxf(m, ml[e][0]);
-      const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn), g = ml[e][0] == -INFINITY ? 0.f : fast_exp2(ml[e][0] - mn);
-      m = mn;
-      l = fmaf(l, f, ml[e][1] * g);
+        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+        g = ml[0] == -INFINITY ? 0.f : fast_exp2(ml[0] - mn);
+        m = mn;
+        float sum = ml[1] * g;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) x[i] = fmaf(x[i], f, v[e][i] * g);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = fmaf(l, f, sum);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] *= f;
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        if (c0 + e >= count) break;
+        const float w = __shfl_sync(0xffffffffu, g, c0 + e);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] = fmaf(v[e][i], w, x[i]);
+      }
     }
   }
   const int r = u.row + row, token = r / p.group, head = u.kv_head * p.group + r - token * p.group;
