@@ -79,6 +79,7 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a, void* workspace, cudaStream_
   const bool whole = units <= (ta::kGrid >> p.gang_shift << p.gang_shift) &&
                      a.max_pages_per_seq * a.page_size <= (int64_t)ta::kWholeTiles * tile;
   p.record = whole ? nullptr : reinterpret_cast<ta::Record*>(p.part_ml + n);
+  p.long_lists = units * 8 < ta::kGrid;
   const int64_t tiles = a.max_pages_per_seq * a.page_size / tile + 16;  // (of a unit, and what its ends count as)
   p.few = a.batch <= 32 && a.hkv * (rows / ta::kRows + 1) <= (int64_t(1) << 25) / tiles;
   p.row_groups = (int)((std::min<int64_t>(rows, ta::kRows) + 7) / 8);

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   };
   if (p.few) {
     // Up to 32 sequences, less than 2^31 of work: a lane each, and each warp for itself (nothing to meet for:
-    // one sequence of 2048 tokens 1 us sooner).
+    // one sequence of 2048 tokens 18.5 -> 17.8 us).
     const bool in = lane < p.batch;
     const SeqT s(p, in ? lane : 0);
     if (in && warp == 0) flag(s, lane);
@@ -1029,10 +1029,12 @@ __device__ __forceinline__ void load_l2(const float* p, float (&v)[kN]) {
 
 // Joins the pieces of the units that lie in several blocks' shares, in the order of their
 // tiles: a warp per row.  Up to 32 pieces' maxima and sums come at once, a lane each, and their
-// outputs kBatch at a time, none of which waits for another: one sequence's 20 pieces are two trips to L2.
-template <int D, bool kQBf16>
+// outputs kBatch at a time, none of which waits for another.  Two at a time where units have few pieces (16
+// sequences of 16384 tokens, 32 drafts, head dim 64: 133.5 us; 135 with 8, 141 with 16), eight for long
+// lists (one of 2048 tokens, 20 pieces a unit: 16.6 us; 18.7 with 2).
+template <int D, bool kQBf16, int kBatch>
 __global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ Params p) {
-  constexpr int kN = D / 32, kBatch = 32 / kN;
+  constexpr int kN = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Record u = p.record[blockIdx.x];
   const int lane = threadIdx.x & 31, row = (int)blockIdx.y * 8 + ((int)threadIdx.x >> 5);
@@ -1114,7 +1116,8 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& k_map, const CUt
   cfg.gridDim = dim3(kGrid, p.row_groups);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, kCache == kCacheBf16 || kCache == kCacheE4m3>, p);
+  constexpr bool kQBf16 = kCache == kCacheBf16 || kCache == kCacheE4m3;
+  return cudaLaunchKernelEx(&cfg, p.long_lists ? tree_attn_join_kernel<D, kQBf16, D == 256 ? 4 : 8> : tree_attn_join_kernel<D, kQBf16, 2>, p);
 }
 
 template <int kCache>

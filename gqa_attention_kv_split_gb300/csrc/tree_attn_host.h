@@ -49,6 +49,7 @@ struct Params {
   float cap_out, cap_inv;    // the cap of the scores in the exp2 domain (0: none), and its reciprocal
   float v_scale;
   int window, sinks, starve;
+  int long_lists;            // so few units that one has more than about 8 pieces
   int few;                   // up to 32 sequences, and less than 2^31 of work whatever their offsets and lengths
 };
 
