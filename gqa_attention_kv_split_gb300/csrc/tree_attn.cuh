@@ -16,7 +16,7 @@
 // weights as TMEM operand.  With 128 rows or fewer a tile of 128 tokens (64 KB in bf16, head
 // dim 128: 1.5 us of an SM's share of HBM) keeps the tensor pipe busy for 0.8 us, however few
 // rows there are, and the softmax for less:
-//  * Copies.  With 64 (32) rows or fewer each row stands in the M dimension twice (four times),
+//  * Copies.  With 64 (32) rows or fewer each row stands in the M dimension twice (four times), if there are tiles enough,
 //    and each copy weighs a half (a quarter) of a tile's tokens, with zeros in P for the
 //    others: the warps share the softmax evenly, as independent (m, l, o) that join at the end.
 //  * S in two TMEM buffers: S of the next tile is computed while the softmax works on this one;
@@ -657,7 +657,8 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
       const int n = walk.count(p), kvh = walk.kv_head(), r0 = walk.row_begin(), rows = walk.rows();
       // Copies of each row, a power of two, of `span` rows each; copy `rep` weighs the 32-token
       // parts of a tile that are rep modulo their number.
-      const int rep_shift = rows > 64 ? 0 : rows > 32 || kTile == 64 ? 1 : 2;
+      // (None for one tile: adding them up would take longer than they save, 12.4 against 11.5 us for 100 tokens.)
+      const int rep_shift = rows > 64 || n < 2 ? 0 : rows > 32 || kTile == 64 ? 1 : 2;
       const int copies = 1 << rep_shift, span = kRows >> rep_shift, rep = L / span, row = L - rep * span;
       const bool live = row < rows;
       const int token = (r0 + (live ? row : 0)) / p.group, head = kvh * p.group + (r0 + (live ? row : 0)) - token * p.group;
