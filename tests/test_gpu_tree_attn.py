@@ -178,6 +178,45 @@ def test_many_sequences():
     Batch(drafts, [n + rng.randint(0, 60) for n in drafts], hq=8, hkv=4, d=64, dtype=BF16, seed=11).check()
 
 
+@pytest.mark.parametrize("batch", [2, 31, 32, 33, 65])
+def test_batches_of_every_size(batch):
+    """Around the 32 sequences that a warp looks over at once: empty drafts, empty caches, short and split ones."""
+    rng = random.Random(23 + batch)
+    drafts = [rng.choice([0, 1, 5, 9]) for _ in range(batch)]
+    lens = [rng.choice([0, n, n + 20, n + rng.randint(100, 900)]) for n in drafts]
+    lens[batch // 2] = drafts[batch // 2] + 3000
+    Batch(drafts, lens, hq=8, hkv=2, d=64, dtype=BF16, pad=2, seed=23).check()
+    Batch(drafts, lens, tree=False, window=300, sinks=10, hq=6, hkv=3, d=64, dtype=F16, cache=E4M3, seed=24).check()
+
+
+@pytest.mark.parametrize("batch", [5, 40])
+def test_offsets_that_fall_leave_the_others(batch):
+    b = Batch([3] * batch, [50 + i for i in range(batch)], hq=4, hkv=2, d=64, seed=25)
+    want, _ = b.check()
+    a = b.args()
+    indptr = list(b.indptr)
+    indptr[2] = b.n + 7  # the second sequence's end and the third one's start
+    a["qo_indptr"] = i32(indptr)
+    out = torch.full_like(b.q, 5.0)
+    gqa.gqa_paged_tree_attn(**a, out=out)
+    assert gqa.gqa_check_device_errors(0) == 4
+    assert torch.equal(out[:3], want[:3]) and torch.equal(out[9:], want[9:]) and (out[3:9] == 5.0).all()
+
+
+def test_capacities_up_to_the_limit():
+    """Block tables for 2^30 tokens, of which a few pages are there."""
+    b = Batch([6, 3], [700, 40], hq=16, hkv=8, d=64, page=256, seed=26)
+    want, _ = b.check()
+    a = b.args()
+    wide = torch.full((2, 1 << 22), -1, dtype=torch.int32, device=DEV)
+    wide[:, :b.table.shape[1]] = b.table
+    a["block_table"] = wide
+    got = gqa.gqa_paged_tree_attn(**a)
+    # (the shares may be others: both are the same sums in another order)
+    assert (got.double() - want.double()).abs().max() <= 2 * torch.finfo(F16).eps * max(1.0, want.double().abs().max().item())
+    assert gqa.gqa_check_device_errors(0) == 0
+
+
 @pytest.mark.parametrize("hkv", [1, 3, 8])
 @pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (F16, E4M3)])
 def test_long_sequences_split_over_blocks(hkv, dtype, cache):
@@ -193,6 +232,7 @@ def test_long_chains():
 
 
 def test_trees_of_many_words():
+    Batch([1024], [1300], hq=2, hkv=1, d=64, dtype=F16, shape="chain", seed=27).check()
     Batch([200, 64], [200, 500], hq=4, hkv=2, d=64, dtype=BF16, seed=17).check()
 
 
