@@ -935,13 +935,14 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
     // ---------------------------------------------------------------- E4M3 -> f16
     // K and then V of each tile.
     if constexpr (kFp8) {
-      // A thread's 16-byte pieces of a tile: one column of them, every 128 / kPer-th row (a multiple of 8, so
-      // that its place in a swizzled row is the same), each two pieces of f16.  Those of odd chunks go in
-      // the other order: eight lanes then fill all banks.
-      constexpr int kPer = D / 16, kRowStep = 128 / kPer, kMine = kTile / kRowStep;
-      const int t = threadIdx.x & 127, e = t % kPer, row0 = t / kPer;
-      const bool flip = (e / 4) & 1;
-      const uint32_t first = (uint32_t)((e / 4) * (kTile * 128) + row0 * 128 + (((2 * (e % 4) + (flip ? 1 : 0)) ^ (row0 & 7)) << 4));
+      // A thread's 16-byte pieces of a tile: one column of them, every kRowStep-th row (a multiple of 8, so
+      // that its place in a swizzled row is the same), each two pieces of f16.  Eight lanes have four pieces of a
+      // row's chunk and four of the next row's other chunk: they fill all banks when they load, and, as the swizzle
+      // puts an odd row's first halves where an even one's second ones lie, when they store either half.
+      constexpr int kRowStep = 128 / (D / 16), kMine = kTile / kRowStep;
+      const int t = threadIdx.x & 127, odd = (t >> 2) & 1, chunk = (t >> 3) % S::kChunks ^ (S::kChunks > 1 ? odd : 0);
+      const int row0 = 2 * ((t >> 3) / S::kChunks) + odd, piece0 = row0 * (D / 16) + chunk * 4 + (t & 3);
+      const uint32_t first = (uint32_t)(chunk * (kTile * 128) + row0 * 128 + ((2 * (t & 3) ^ (row0 & 7)) << 4));
       int rs = 0, rph = 0, st = 0, ph = 1;
       do {
         const int n = walk.count(p);
@@ -961,7 +962,7 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
             // (all loads before the first store: the compiler cannot know that they are of other bytes)
             uint4 v[kMine];
 #pragma unroll
-            for (int k = 0; k < kMine; ++k) v[k] = src[t + 128 * k];
+            for (int k = 0; k < kMine; ++k) v[k] = src[piece0 + 128 * k];
             if (!wait_all(free_, ph)) {
               failed = true;
               break;
@@ -976,8 +977,7 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
             }
 #pragma unroll
             for (int k = 0; k < kMine; ++k) {
-              const uint2 a = widen(flip ? v[k].z : v[k].x), b = widen(flip ? v[k].w : v[k].y);
-              const uint2 c = widen(flip ? v[k].x : v[k].z), d = widen(flip ? v[k].y : v[k].w);
+              const uint2 a = widen(v[k].x), b = widen(v[k].y), c = widen(v[k].z), d = widen(v[k].w);
               uint8_t* to = dst + k * (kRowStep * 128);
               *reinterpret_cast<uint4*>(to + first) = make_uint4(a.x, a.y, b.x, b.y);
               *reinterpret_cast<uint4*>(to + (first ^ 16)) = make_uint4(c.x, c.y, d.x, d.y);
