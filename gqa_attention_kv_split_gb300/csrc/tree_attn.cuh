@@ -39,7 +39,7 @@
 //
 // Measured on GB300 (time in a graph): 16 sequences of 16384 tokens, 32/8 heads of 128, bf16, 8 drafts: 169 us,
 // 6.37 TB/s; 64 drafts: 291 us, 940 TFLOP/s; 8 of 65536, f16, 64 drafts: 555 us, 990 TFLOP/s; 48 of up to 16001, 64/8
-// heads, E4M3, up to 16 drafts: 238 us, 3.4 TB/s; one of 2048 tokens, 8 drafts: 17 us.
+// heads, E4M3, up to 16 drafts: 237 us, 3.4 TB/s; one of 2048 tokens, 8 drafts: 17 us.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
