@@ -37,8 +37,8 @@
 //    exactly.
 //  * Every wait is bounded; a block whose wait expires drains what it started and leaves.
 //
-// Measured on GB300 (time in a graph): 16 sequences of 16384 tokens, 32/8 heads of 128, bf16, 8 drafts: 169 us,
-// 6.37 TB/s; 64 drafts: 291 us, 940 TFLOP/s; 8 of 65536, f16, 64 drafts: 555 us, 990 TFLOP/s; 48 of up to 16001, 64/8
+// Measured on GB300 (time in a graph): 16 sequences of 16384 tokens, 32/8 heads of 128, bf16, 8 drafts: 167 us,
+// 6.4 TB/s; 64 drafts: 293 us, 935 TFLOP/s; 8 of 65536, f16, 64 drafts: 555 us, 990 TFLOP/s; 48 of up to 16001, 64/8
 // heads, E4M3, up to 16 drafts: 237 us, 3.4 TB/s; one of 2048 tokens, 8 drafts: 17 us.
 #pragma once
 #include <cuda.h>
@@ -78,9 +78,10 @@ struct Shape {
   // it has done with a tile), and the queries (two elements a column).
   static constexpr int kBufs = D == 64 ? 3 : 2;
   static constexpr uint32_t kO = 0, kS = D, kQ = D + kBufs * kTile;
-  // What starting and ending a unit costs, in tiles.  (48 sequences of up to 16001 E4M3 tokens with up to 16
-  // drafts: 265 us with 2, 254 with 6; 33 of 6007 in bf16 under a window 120.8, 119.1 with 4.)
-  static constexpr int kUnitWork = kFp8 ? 6 : 4;
+  // What starting and ending a unit costs, in tiles.  (E4M3: 40 sequences of up to 3000 tokens with up to 30 drafts
+  // 67.2 us with 3, 63.3 with 6, 20 of up to 8000 58.3 with 6, 62.3 with 10.  bf16: 200 of up to 600 100.8 us
+  // with 2, 98.0 with 4, 96.7 with 5, 96.9 with 8; 20 of up to 8000 67.7, 65.0, 64.4, 66.7.)
+  static constexpr int kUnitWork = kFp8 ? 6 : 5;
 };
 
 struct Bars {
