@@ -801,8 +801,8 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         const float sub = m == -INFINITY ? 0.f : m - kShift;
         float2 sum = make_float2(0.f, 0.f);
         const float2 ss = make_float2(kCap ? 1.f : scale, kCap ? 1.f : scale), nn = make_float2(-sub, -sub);
-        // (A loop that is not unrolled: with 64 or 128 tokens in one piece of code the instructions no
-        // longer come fast enough, 608 and 748 us for 565 of the same case.)
+        // (A loop that is not unrolled: with 64 or 128 tokens in one piece of code, or loads ahead of the part
+        // in work, registers are spilled, 608, 748 and 679 us for 565 of the same case.)
 #pragma unroll 1
         for (int c = 0; c < kParts; ++c) {
           uint32_t w[32];
