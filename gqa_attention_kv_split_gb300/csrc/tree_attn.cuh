@@ -23,6 +23,7 @@
 //    P overwrites the S it came from (32 tokens' weights: 16 columns of their first terms, 16
 //    of their second ones).
 //  * Weights enter the product with V as two terms of 16 bits (22 bits in f16, 16 in bf16).
+//  * O leaves TMEM every 16384 tokens for sums that round to nearest (fold_out).
 //  * The maximum is raised (and O rescaled in TMEM) only when a row's passes the one in use by
 //    more than 2^8: weights then stay within f16, whose terms keep 2^-31 of the largest.
 //
@@ -82,6 +83,8 @@ struct Shape {
   // 67.2 us with 3, 63.3 with 6, 20 of up to 8000 58.3 with 6, 62.3 with 10.  bf16: 200 of up to 600 100.8 us
   // with 2, 98.0 with 4, 96.7 with 5, 96.9 with 8; 20 of up to 8000 67.7, 65.0, 64.4, 66.7.)
   static constexpr int kUnitWork = kFp8 ? 6 : 5;
+  // Tiles whose products O takes before it goes to a sum outside TMEM (an even number).
+  static constexpr int kFold = 16384 / kTile;
 };
 
 struct Bars {
@@ -97,6 +100,7 @@ struct Smem {
   alignas(16) float stage[2][kRows][20];  // 16 columns of the copies' sums, for each half of the columns
   float m_used[kRows];                 // the maximum that the last tile's weights are relative to
   float m[2][kRows], l[2][kRows];      // of the groups' copies, at a unit's end (and their queries' largest elements)
+  float m_fold[kRows];                 // the maximum that the sums outside TMEM are relative to
   int64_t scan_work[kThreads / 32], scan_turns[kThreads / 32];
   int most[kThreads / 32];
   int64_t total, end, rem;
@@ -281,6 +285,61 @@ struct Sight {
 };
 
 namespace {
+
+// The tensor cores cut off what does not fit their f32 sums, two of them for 16 tokens, so that a long sum drifts towards
+// 0 (1.2e-3 of sum w |V| over 2^20 tokens).  So O goes to sums outside TMEM (in the workspace, where nothing lies yet that is read
+// later), whose f32 additions round to nearest, every 16384 tokens.  (8 x 65536 f16 tokens with 64 drafts: 2.1e-4 off the
+// 64-bit form, as f32 rounded to f16 is, 2.3e-4 without; 605 -> 613 us.  Every 8192 tokens 2.08e-4, 625 us, and pieces of
+// fewer than 16384 tokens pay too, 163 -> 167 us; every 4096 the same error, 665 us.)
+//
+// Adds a lane's columns of O, times alpha, to its sums (times f; there are none yet at the first time).
+template <int D>
+__device__ __forceinline__ void fold_out(uint32_t t_o, float4* sums, float alpha, float f, bool first) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t o[16];
+    tc::ld16(t_o + c, o);
+    tc::ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      float4 y = make_float4(__uint_as_float(o[e]) * alpha, __uint_as_float(o[e + 1]) * alpha, __uint_as_float(o[e + 2]) * alpha,
+                             __uint_as_float(o[e + 3]) * alpha);
+      float4* const at = sums + (c + e) / 4 * kRows;
+      if (!first) {
+        const float4 x = *at;
+        y = make_float4(fmaf(x.x, f, y.x), fmaf(x.y, f, y.y), fmaf(x.z, f, y.z), fmaf(x.w, f, y.w));
+      }
+      *at = y;
+    }
+  }
+}
+
+// And back: the sums, times g, join kCols of a lane's columns of O.
+template <int kCols>
+__device__ __forceinline__ void unfold_out(uint32_t t_o, const float4* sums, float g) {
+  constexpr int kBatch = 32;  // columns whose loads are in flight together (with 64 registers are spilled)
+#pragma unroll 1
+  for (int c0 = 0; c0 < kCols; c0 += kBatch) {
+    float4 x[kBatch / 4];
+#pragma unroll
+    for (int e = 0; e < kBatch / 4; ++e) x[e] = sums[(c0 / 4 + e) * kRows];
+#pragma unroll
+    for (int c = 0; c < kBatch; c += 16) {
+      uint32_t o[16];
+      tc::ld16(t_o + c0 + c, o);
+      tc::ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 y = x[(c + e) / 4];
+        o[e] = __float_as_uint(fmaf(y.x, g, __uint_as_float(o[e])));
+        o[e + 1] = __float_as_uint(fmaf(y.y, g, __uint_as_float(o[e + 1])));
+        o[e + 2] = __float_as_uint(fmaf(y.z, g, __uint_as_float(o[e + 2])));
+        o[e + 3] = __float_as_uint(fmaf(y.w, g, __uint_as_float(o[e + 3])));
+      }
+      tc::st16(t_o + c0 + c, o);
+    }
+  }
+}
 
 template <int kCache, int D, bool kCap>
 __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
@@ -611,7 +670,7 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
 #pragma unroll
             for (int k = h * (kTile / 32); k < (h + 1) * (kTile / 32); ++k) {
               const uint32_t a = tp + 32 * (k / 2) + 8 * (k % 2);
-              tc::mma_f16_tmem_a(tm + S::kO, a, dv + 128 * k, id_o, (i > 0 || k > 0) ? 1u : 0u);
+              tc::mma_f16_tmem_a(tm + S::kO, a, dv + 128 * k, id_o, (i % S::kFold > 0 || k > 0) ? 1u : 0u);
               tc::mma_f16_tmem_a(tm + S::kO, a + 16, dv + 128 * k, id_o, 1u);
             }
             if (h == 1) {
@@ -729,6 +788,10 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
         see.hi = 0x7fffffff;
       }
 
+      // The piece's place in the workspace; until it is written there the sums outside TMEM, four columns of
+      // each lane after the other.
+      auto piece = [&] { return ((int)blockIdx.x * 2 + (seg == 1 ? 0 : 1)) * kRows; };
+      auto folded = [&](int c) { return reinterpret_cast<float4*>(p.part_o + (int64_t)piece() * D) + c / 4 * kRows + L; };
       float m = -INFINITY, l = 0.f;
       auto advance = [&] {
         ++j;
@@ -782,7 +845,15 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
           sm.m_used[L] = m;
           named_bar_arrive(2 + 2 * quad + ((j + 1) & 1), 64);
         }
-        if (i > 0 && !failed && __any_sync(0xffffffffu, raise)) {
+        if (i > 0 && i % S::kFold == 0) {
+          // O goes to the sums outside TMEM and begins anew.  (kFold is even: one group does this for a whole piece.)
+          if (!failed && !wait_all(&sm.bar.p_free[last_buf()], last_ph())) failed = true;
+          tc::fence_after_thread_sync();
+          const bool first = i == S::kFold;
+          const float f = first || m == -INFINITY ? 0.f : fast_exp2(sm.m_fold[L] - m);
+          if (!failed) fold_out<D>(t_lane + S::kO, folded(0), alpha, f, first);
+          sm.m_fold[L] = m;
+        } else if (i > 0 && !failed && __any_sync(0xffffffffu, raise)) {
           // O holds the products of the tiles before this one
           if (!wait_all(&sm.bar.p_free[last_buf()], last_ph())) failed = true;
           tc::fence_after_thread_sync();
@@ -856,13 +927,17 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
       float f = own == -INFINITY ? 0.f : fast_exp2(own - mm);  // what this copy's sums are multiplied by
       m = mm;
       l = ll;
-      named_bar_sync(1, 256);  // (they are written again at the next unit's end)
+      if (n > S::kFold && !failed) {
+        const float g = sm.m_fold[L] == -INFINITY ? 0.f : fast_exp2(sm.m_fold[L] - own);
+        unfold_out<D / 2>(t_lane + S::kO + group * (D / 2), folded(group * (D / 2)), g);
+        tc::st_wait();
+      }
+      named_bar_sync(1, 256);  // (they are written again at the next unit's end, and the piece takes the folded sums' place)
       const bool summed = n > 0 && !failed;  // there is something in O
       if (!summed) f = 0.f;
       const bool whole = walk.whole(), writes = live && rep == 0 && !failed;
       if (whole) f = l == 0.f ? 0.f : f * (p.v_scale / l);
       const int64_t out_row = (s.row0 + token) * p.hq + head;
-      const int64_t piece = ((int64_t)blockIdx.x * 2 + (seg == 1 ? 0 : 1)) * kRows;
 #pragma unroll 1
       for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 16) {
         uint32_t o[16];
@@ -897,7 +972,7 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
               *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (((s.row0 + t) * p.hq + h) * D + d) * 2) =
                   make_uint2(pack<kQBf16>(u.x, u.y), pack<kQBf16>(u.z, u.w));
             } else {
-              *reinterpret_cast<float4*>(p.part_o + (piece + y) * D + d) = u;
+              *reinterpret_cast<float4*>(p.part_o + (int64_t)(piece() + y) * D + d) = u;
             }
           }
           named_bar_sync(10 + group, 128);
@@ -913,14 +988,14 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
           dst[0] = u[0];
           dst[1] = u[1];
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (piece + row) * D + c);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (int64_t)(piece() + row) * D + c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
       }
       if (writes && group == 0) {
         if (!whole)
-          p.part_ml[piece + row] = make_float2(m - kShift, l);
+          p.part_ml[piece() + row] = make_float2(m - kShift, l);
         else if (p.lse)
           p.lse[out_row] = l == 0.f ? -INFINITY : (m - kShift) * 0.6931471805599453f + logf(l);
       }

@@ -588,7 +588,10 @@ gqa_status gqa_tree_mask_t(const gqa_tensor* parents, const gqa_tensor* qo_indpt
  * Scores, maxima, sums and accumulators are f32.  A softmax weight meets V as two
  * 16-bit terms of the pages' type (f16 for E4M3 ones), 22 bits in f16 and 16 in bf16;
  * f16 terms are exact to 2^-31 of the largest weight at best.  A bf16 query over E4M3
- * pages is exact to 2^-40 of its row's largest element.
+ * pages is exact to 2^-40 of its row's largest element.  The accumulators of the product
+ * with V cut sums off; they take 16384 tokens at most (about 2e-5 of sum w |V| by
+ * then) before they are added up with rounding, so that the error does not grow with the
+ * length.
  *
  * A row that sees nothing (a sequence of length 0, an empty mask) becomes zeros, with
  * lse = -infinity; rows behind qo_indptr[batch] are left as they are.  Slots that no
