@@ -370,7 +370,7 @@ def gqa_paged_keep(pages, block_table, qo_indptr, kv_lens, kept, num_kept, *, ne
     page_size,w] of any type (K and V, or the codes and scales of NVFP4
     pages); kept [B,max_kept] int32, the accepted tokens' numbers within the
     draft, rising; num_kept [B] int32.  Returns the sequences' new lengths [B]
-    int32 (or writes `new_lens`, which may not be kv_lens)."""
+    int32 (or writes `new_lens`, which may share no memory with the others)."""
     if new_lens is None:
         new_lens = torch.empty_like(kv_lens, memory_format=torch.contiguous_format)
     st = _binding().keep(tuple(pages), block_table, qo_indptr, kv_lens, kept, num_kept, new_lens)

@@ -56,6 +56,17 @@ gqa_status check_strided(const gqa_tensor* t, const char* name, std::initializer
 // Stride of a dimension; 0 where its extent is 1 (nothing is ever added for it).
 int64_t stride_of(const gqa_tensor* t, int d) { return t->shape[d] > 1 ? t->strides[d] : 0; }
 
+// Do two dense tensors share a byte?
+bool overlap(const gqa_tensor* a, const gqa_tensor* b) {
+  auto bytes = [](const gqa_tensor* t) {
+    uint64_t n = (uint64_t)dtype_bytes(t->dtype);
+    for (int d = 0; d < t->ndim; ++d) n *= (uint64_t)t->shape[d];
+    return n;
+  };
+  const uint64_t x = reinterpret_cast<uintptr_t>(a->data), y = reinterpret_cast<uintptr_t>(b->data), m = bytes(a), n = bytes(b);
+  return m > 0 && n > 0 && (x < y ? y - x < m : x - y < n);
+}
+
 gqa_status check_scale(float s, const char* name) {
   if (!std::isfinite(s) || !(s > 0.f) || !std::isfinite(1.f / s))
     return fail(GQA_ERR_INVALID_ARG, "%s must be finite and > 0", name);
@@ -533,6 +544,10 @@ gqa_status gqa_paged_keep_t(const gqa_tensor* const* pages, int num_tensors, con
     GQA_TRY(check_desc(num_kept, "num_kept", {GQA_I32}, {ls[0]}));
     GQA_TRY(check_desc(new_lens, "new_lens", {GQA_I32}, {ls[0]}));
     if (new_lens->data == kv_lens->data) return fail(GQA_ERR_INVALID_ARG, "new_lens may not be kv_lens: both are in use at once");
+    // (blocks that have yet to begin read what the first ones of a sequence would have written over)
+    for (const Named& t : {Named{kv_lens, "kv_lens"}, Named{num_kept, "num_kept"}, Named{kept, "kept"}, Named{qo_indptr, "qo_indptr"},
+                           Named{block_table, "block_table"}})
+      if (overlap(new_lens, t.first)) return fail(GQA_ERR_INVALID_ARG, "new_lens overlaps %s: both are in use at once", t.second);
     if (bs[1] < 1) return fail(GQA_ERR_INVALID_ARG, "block_table has no column");
     if (ks[1] < 1) return fail(GQA_ERR_INVALID_ARG, "kept has no column");
     std::vector<Named> ts = {{block_table, "block_table"}, {qo_indptr, "qo_indptr"}, {kv_lens, "kv_lens"},

@@ -634,7 +634,8 @@ int64_t gqa_paged_tree_attn_workspace(int64_t q_heads, int64_t kv_heads, int64_t
  *   kept         [batch, max_kept]  int32, rising; entries from num_kept[b] on are
  *                not read
  *   num_kept     [batch]  int32
- *   new_lens     [batch]  int32, written; another tensor than kv_lens
+ *   new_lens     [batch]  int32, written; overlaps none of the other small tensors
+ *                (checked), nor pages
  *   batch        1 .. 65535
  *
  * A sequence whose kept tokens do not rise, or do not lie in its draft, or which is
