@@ -507,6 +507,11 @@ gqa_status gqa_tree_mask_t(const gqa_tensor* parents, const gqa_tensor* qo_indpt
       return fail(GQA_ERR_UNSUPPORTED_SHAPE, "%lld words of bits: 1 to %d are taken", (long long)ms[1], gqa::kMaxTreeTokens / 32);
     if (window < 0) return fail(GQA_ERR_INVALID_ARG, "window %d is negative", window);
     if (sinks < 0) return fail(GQA_ERR_INVALID_ARG, "sinks %d is negative", sinks);
+    // (trees' blocks run at the same time; one reads all its parents before it writes)
+    for (const Named& out : {Named{&ma, "mask"}, Named{&po, "positions"}})
+      for (const Named& in : {Named{&pa, "parents"}, Named{qo_indptr, "qo_indptr"}, Named{kv_lens, "kv_lens"}, Named{&po, "positions"}})
+        if (out.first != in.first && overlap(out.first, in.first) && !(out.first == &po && in.first == &pa && po.data == pa.data))
+          return fail(GQA_ERR_INVALID_ARG, "%s overlaps %s: both are in use at once", out.second, in.second);
     if (ps[0] == 0) return GQA_OK;
     Where where;
     GQA_TRY(locate_tensors({{parents, "parents"}, {qo_indptr, "qo_indptr"}, {kv_lens, "kv_lens"}, {mask, "mask"}, {positions, "positions"}},

@@ -544,6 +544,8 @@ gqa_status gqa_paged_window_attn_t(const gqa_tensor* q, const gqa_tensor* k_page
  *   qo_indptr  [batch + 1], kv_lens [batch]  int32; the drafted tokens included
  *   mask       [total, words]  int32, bit j % 32 of word j / 32; written
  *   positions  [total]  int32, written
+ *   (mask and positions overlap nothing else, which is checked; positions may be
+ *   parents itself)
  *   words      1 .. 32: trees of up to 32 * words tokens; batch 1 .. 2^20
  *   window, sinks  >= 0, those of the attention
  *

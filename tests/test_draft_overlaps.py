@@ -5,7 +5,7 @@ import torch
 
 import gqa_attention_kv_split_gb300 as gqa
 from gqa_attention_kv_split_gb300 import build_lib
-from test_draft_refusals import keep_args
+from test_draft_refusals import keep_args, mask_args
 from test_paged_cache import fake
 
 I32 = torch.int32
@@ -33,3 +33,24 @@ def test_new_lengths_beside_other_inputs():
     for new_lens in (memory[0:2], memory[4:6]):
         with pytest.raises(gqa.GqaError, match="device tensors only"):
             gqa.gqa_paged_keep(**a, new_lens=new_lens)
+
+
+@pytest.mark.parametrize("written", ["mask", "positions"])
+@pytest.mark.parametrize("name", ["parents", "qo_indptr", "kv_lens", "mask"])
+def test_masks_and_positions_over_other_arguments(name, written):
+    """A tree's block writes its rows while the blocks of other trees read their parents, offsets and lengths."""
+    if name == written:
+        return
+    a, memory = mask_args(), fake((16,), I32)
+    other = memory.as_strided(a[name].shape, a[name].stride(), 6)
+    for start in (2, 5 + other.numel()):  # its first number is in it, its last one
+        out = memory.as_strided(a[written].shape, a[written].stride(), start)
+        with pytest.raises(gqa.GqaError, match="mask overlaps positions" if name == "mask" else f"{written} overlaps {name}"):
+            gqa.gqa_tree_mask(**{**a, name: other, written: out})
+
+
+def test_positions_in_place_of_parents():
+    """A tree's parents have been read when its positions are written: they may be the same tensor."""
+    a = mask_args()
+    with pytest.raises(gqa.GqaError, match="device tensors only"):
+        gqa.gqa_tree_mask(**{**a, "positions": a["parents"]})
