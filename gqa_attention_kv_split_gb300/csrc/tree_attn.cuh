@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
   int n_gangs, b0 = 0;         // gangs with a share: none is empty; the share's first sequence
   int64_t total, beg, end, rem = 0;
   auto shares = [&](int most, int64_t total_w, int64_t total_t) {
-    by_unit = most <= kWholeTiles && total_t <= gangs;
+    // (without a record nothing would be joined: the host has seen that no unit needs to be split, but where offsets fall
+    // the sequences between may have more rows than it counted)
+    by_unit = !p.record || (most <= kWholeTiles && total_t <= gangs);
     total = by_unit ? total_t : total_w;
     n_gangs = total < gangs ? (int)total : gangs;
     beg = gang < n_gangs ? share_begin(gang, total, n_gangs) : 0;
