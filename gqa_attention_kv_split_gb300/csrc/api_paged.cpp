@@ -654,8 +654,8 @@ gqa_status gqa_paged_tree_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages,
     GQA_TRY(check_numbers(q_scale, k_scale, v_scale, window, sinks, softcap));
     const int64_t group = z.hq / z.hkv, tiles = z.max_pages * z.page_size / 64 + 16;
     if (z.rows * group > 2147483647LL) return fail(GQA_ERR_UNSUPPORTED, "%lld tokens of %lld heads are too many", (long long)z.rows, (long long)group);
-    // (a block of the kernel counts the work of its share, in tiles of 64 tokens at least, in 31 bits)
-    if (z.hkv * (ls[0] + z.rows * group / 128) > (int64_t(1) << 38) / tiles)
+    // (tiles of 64 tokens at least; the kernel looks again, for offsets that fall)
+    if (z.hkv * (ls[0] + z.rows * group / 128) > gqa::kTreeMostWork / tiles)
       return fail(GQA_ERR_UNSUPPORTED, "%lld sequences, %lld tokens x %lld KV heads x %lld tokens of capacity are too many",
                   (long long)ls[0], (long long)z.rows, (long long)z.hkv, (long long)(z.max_pages * z.page_size));
     const float scale = (float)((double)q_scale * k_scale / std::sqrt((double)z.d));

@@ -112,6 +112,9 @@ cudaError_t paged_attn_read_errors(uint32_t* word);
 
 // ---- attention of several new tokens per sequence over a paged cache ---------
 
+// The most work of a call, in tiles of K and V and what the units' ends count as: a block counts its share in 31 bits.
+constexpr int64_t kTreeMostWork = int64_t(1) << 38;
+
 struct TreeAttnArgs {
   const void* q;               // [total, hq, d] f16 or bf16
   void* out;                   // [total, hq, d], q's type, dense

@@ -409,6 +409,12 @@ __global__ void __launch_bounds__(Shape<kCache, D>::kThreads, 1)
     // the sequences between may have more rows than it counted)
     by_unit = !p.record || (most <= kWholeTiles && total_t <= gangs);
     total = by_unit ? total_t : total_w;
+    // (offsets that fall again and again can make sequences in order of any number of rows, where the host has counted
+    // each row once: no share may pass the 31 bits that it is counted in)
+    if (total > (kTreeMostWork >> p.gang_shift)) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, kErrBadIndptr);
+      total = 0;
+    }
     n_gangs = total < gangs ? (int)total : gangs;
     beg = gang < n_gangs ? share_begin(gang, total, n_gangs) : 0;
     end = gang < n_gangs ? share_begin(gang + 1, total, n_gangs) : 0;

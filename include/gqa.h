@@ -603,8 +603,10 @@ gqa_status gqa_tree_mask_t(const gqa_tensor* parents, const gqa_tensor* qo_indpt
  * whether they see it or not.  A page outside [0, num_pages) is not read: page 0 is
  * used instead and bit 1 of the error word is set.  A sequence whose offsets do not lie
  * in order within [0, total] is left out (its rows are not written) and sets bit 2, as
- * does qo_indptr[0] != 0.  out and lse overlap no other argument.  The split is chosen
- * on the device from the lengths.  One kernel, or two; host tensors are refused.
+ * does qo_indptr[0] != 0; where offsets fall so often that the sequences between pass
+ * the limit on the product, all are left out (but rows without a token become zeros).
+ * out and lse overlap no other argument.  The split is chosen on the device from the
+ * lengths.  One kernel, or two; host tensors are refused.
  */
 gqa_status gqa_paged_tree_attn_t(const gqa_tensor* q, const gqa_tensor* k_pages, const gqa_tensor* v_pages,
                                  const gqa_tensor* block_table, const gqa_tensor* qo_indptr, const gqa_tensor* kv_lens,

@@ -35,3 +35,21 @@ def test_sequences_over_the_same_rows(short):
     gqa.gqa_paged_tree_attn(q, k, v, table.repeat(3, 1), i32([0, short, 0, n]), i32([before + short, 7, before + n]), out=out, lse=got_lse)
     assert gqa.gqa_check_device_errors(0) == 4
     assert torch.equal(out, want) and torch.equal(got_lse, lse)
+
+
+def test_more_work_than_shares_can_count():
+    """2048 times the same 16384 tokens of 64 heads over 3.2 million cached ones: a block's share would pass 31 bits.
+    (The producers are starved, so that a kernel that began with it would give up.)"""
+    n, batch, cols = 16384, 4096, 12500
+    q = torch.zeros(n, 64, 64, dtype=torch.float16, device=DEV)
+    k = torch.zeros(1, 1, 256, 64, dtype=torch.float16, device=DEV)
+    table = torch.zeros(batch, cols, dtype=torch.int32, device=DEV)
+    assert batch // 2 * (n * 64 // 128) * (cols * 256 // 128 + 5) // 152 > 2 ** 31
+    out = torch.full_like(q, 5.0)
+    gqa.gqa_debug_starve_producers(True)
+    try:
+        gqa.gqa_paged_tree_attn(q, k, k, table, i32([0, n] * (batch // 2) + [0]), i32([cols * 256] * batch), out=out)
+        assert gqa.gqa_check_device_errors(0) == 4
+    finally:
+        gqa.gqa_debug_starve_producers(False)
+    assert (out == 5.0).all()
