@@ -339,16 +339,31 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     unpack8(cur.lo, x, T());
     unpack8(cur.hi, y, T());
     if (norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
       // (a row's lanes are neighbours and take the same way; other rows of the warp may not be here)
       const unsigned lanes = (kLanes == 32 ? ~0u : (1u << kLanes) - 1) << (lane & ~(kLanes - 1));
+      auto squares = [&] {
+        float ss = 0.f;
 #pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(lanes, ss, o);
-      const float inv = rsqrtf(fmaf(ss, 1.f / D, a.norm_eps));
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(lanes, ss, o);
+        return ss;
+      };
+      float mean = fmaf(squares(), 1.f / D, a.norm_eps);
+      if (mean < 0x1p-100f || mean > 3.402823466e38f) {
+        // Squares near the lower end of f32's range, or past the upper one: once more for a head brought to its middle by
+        // a power of two (bf16's smallest element, 2^-133, to 2^-33, its largest ones to 2^58), eps with it.
+        const float by = mean < 1.f ? 0x1p100f : 0x1p-70f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] *= by;
+          y[e] *= by;
+        }
+        mean = fmaxf(fmaf(squares(), 1.f / D, a.norm_eps * by * by), 1.17549435e-38f);  // (zeros stay zeros, with an eps of 0 too)
+      }
+      const float inv = rsqrtf(mean);
       const float* w = weight + (is_q ? 0 : D);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

@@ -441,8 +441,8 @@ gqa_status nvfp4_paged_append_t(const gqa_tensor* q, const gqa_tensor* k, const 
  *                They choose the angles alone; page and slot are as above.  A
  *                token whose position lies outside the rope table is skipped and
  *                bit 1 of the error word is set.  Needs rope
- *   norm_eps     finite, >= 0 (read where there is a norm); squares are summed in
- *                f32, so that a head whose squares pass its range becomes zeros
+ *   norm_eps     finite, >= 0 (read where there is a norm); a head of zeros stays
+ *                zeros, with a norm_eps of 0 too
  * Everything else as gqa_paged_append_t and nvfp4_paged_append_t.  q_norm and
  * k_norm overlap nothing that is written.
  */
