@@ -99,6 +99,11 @@ struct Shape {
   // blocks went in gangs; with them 35.9, 40.6 and, one term a weight as before, 124 us, and the
   // same with 64 or 144 KB.)
   static constexpr int kUnitWork = NT * 96 * 1024 / (2 * kHalf);
+  // Tiles in which a warp sums up 8192 tokens.  The tensor cores cut off what does not fit their f32 sums, so that longer
+  // ones drift towards 0 (a sequence of 2^20 tokens in one block: 5.9e-4 of sum w |V|, 1.2e-3 at head dim 256; 6e-5 so):
+  // they go to shared memory then, where sums round to nearest.  (Units of fewer tiles give the same bits as without, in the
+  // same time but for the shortest: 190 x 64 tokens 23.8 -> 24.4 us.)
+  static constexpr int kFold = 8192 * kWarps / kTile;
   static constexpr int kRoom = 128 * 1024;  // the warps' join takes up to 68 KB
   // A whole number of groups' turns, so that a stage always belongs to one group (a
   // wait on its barrier can then never be a phase behind).
@@ -647,213 +652,245 @@ __global__ void __launch_bounds__(Shape<kCache, D, NT>::kThreads, 1)
     }
 
     int tile = walk.t_beg + skip;
-    for (; tile < walk.t_end; tile += S::kGroups) {
-      if (dead) continue;
-      const int key0 = walk.span.place(walk.span.tile0 + tile) * kTile + row0;  // this warp's first key
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), ph, err))) {
-        dead = true;
-        continue;
-      }
-      const uint32_t kb = ring_u + st * 2 * S::kHalf, vb = kb + S::kHalf;
-      if (walk.span.any(key0, kKeys)) {
-        const bool edge = walk.span.edge(key0, kKeys);
-        // ---- S^T = K Q^T
-        float s[kBlocks][NT][4];
+    for (int end = walk.t_beg;;) {  // kFold tiles at a time
+      const bool first = end == walk.t_beg;
+      end = walk.t_end - end > S::kFold ? end + S::kFold : walk.t_end;
+      for (; tile < end; tile += S::kGroups) {
+        if (dead) continue;
+        const int key0 = walk.span.place(walk.span.tile0 + tile) * kTile + row0;  // this warp's first key
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), ph, err))) {
+          dead = true;
+          continue;
+        }
+        const uint32_t kb = ring_u + st * 2 * S::kHalf, vb = kb + S::kHalf;
+        if (walk.span.any(key0, kKeys)) {
+          const bool edge = walk.span.edge(key0, kKeys);
+          // ---- S^T = K Q^T
+          float s[kBlocks][NT][4];
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j)
+          for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[j][t][e] = 0.f;
+          if (!kFp8) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+              for (int j = 0; j < kBlocks; ++j) {
+                uint32_t a[4];
+                ldsm4(a, kb + blk[j] + col(k_row, 2 * k + k_sel));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma<kBf16>(s[j][t], a, qf[t][k][0], qf[t][k][1]);
+              }
+          } else {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+              for (int j = 0; j < kBlocks; ++j) {
+                uint32_t w[4];
+                ldsm4(w, kb + blk[j] + col(k_row, 2 * k + k_sel));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t a[4] = {e4m3_to_f16x2(w[2 * i] & 0xffffu), e4m3_to_f16x2(w[2 * i + 1] & 0xffffu),
+                                         e4m3_to_f16x2(w[2 * i] >> 16), e4m3_to_f16x2(w[2 * i + 1] >> 16)};
+#pragma unroll
+                  for (int t = 0; t < NT; ++t) mma<false>(s[j][t], a, qf[t][2 * k + i][0], qf[t][2 * k + i][1]);
+                }
+              }
+          }
+          if (edge) {
+            // V rows outside the sequence may hold anything; 0 * NaN is NaN, so they are zeroed.
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j)
+              for (int i = lane; i < 16 * (S::kRow / 16); i += 32) {
+                const int r = i % 16, c16 = i / 16, key = key0 + 16 * j + r;
+                if (walk.span.hidden(key))
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + blk[j] + col(r, c16)), "r"(0) : "memory");
+              }
+            __syncwarp();
+          }
+          // ---- softmax weights: rows (keys) g, g + 8 of each block; columns (heads) c2, c2 + 1
+          bool grow = false;  // has a score passed its head's maximum?
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][t][e] = 0.f;
-        if (!kFp8) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-#pragma unroll
             for (int j = 0; j < kBlocks; ++j) {
-              uint32_t a[4];
-              ldsm4(a, kb + blk[j] + col(k_row, 2 * k + k_sel));
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma<kBf16>(s[j][t], a, qf[t][k][0], qf[t][k][1]);
+              for (int e = 0; e < 4; ++e) {
+                float& v = s[j][t][e];
+                v *= sc[t][e & 1];
+                if (p.cap_out != 0.f) v = capped(v, p.cap_out, p.cap_inv);
+              }
+              if (edge) {
+                const int ka = key0 + 16 * j + g, kc = ka + 8;
+                if (walk.span.hidden(ka)) s[j][t][0] = s[j][t][1] = -INFINITY;
+                if (walk.span.hidden(kc)) s[j][t][2] = s[j][t][3] = -INFINITY;
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) grow |= s[j][t][e] > m[t][e & 1];
             }
-        } else {
+          if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-            for (int j = 0; j < kBlocks; ++j) {
-              uint32_t w[4];
-              ldsm4(w, kb + blk[j] + col(k_row, 2 * k + k_sel));
+            for (int t = 0; t < NT; ++t) {
+              float alpha[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t a[4] = {e4m3_to_f16x2(w[2 * i] & 0xffffu), e4m3_to_f16x2(w[2 * i + 1] & 0xffffu),
-                                       e4m3_to_f16x2(w[2 * i] >> 16), e4m3_to_f16x2(w[2 * i + 1] >> 16)};
+                float x = m[t][i];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma<false>(s[j][t], a, qf[t][2 * k + i][0], qf[t][2 * k + i][1]);
+                for (int j = 0; j < kBlocks; ++j) x = fmaxf(x, fmaxf(s[j][t][i], s[j][t][i + 2]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                alpha[i] = x == -INFINITY ? 0.f : fast_exp2(m[t][i] - x);
+                m[t][i] = x;
+                l[t][i] *= alpha[i];
               }
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][i][e] *= alpha[e & 1];
             }
-        }
-        if (edge) {
-          // V rows outside the sequence may hold anything; 0 * NaN is NaN, so they are zeroed.
-#pragma unroll
-          for (int j = 0; j < kBlocks; ++j)
-            for (int i = lane; i < 16 * (S::kRow / 16); i += 32) {
-              const int r = i % 16, c16 = i / 16, key = key0 + 16 * j + r;
-              if (walk.span.hidden(key))
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + blk[j] + col(r, c16)), "r"(0) : "memory");
-            }
-          __syncwarp();
-        }
-        // ---- softmax weights: rows (keys) g, g + 8 of each block; columns (heads) c2, c2 + 1
-        bool grow = false;  // has a score passed its head's maximum?
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int j = 0; j < kBlocks; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float& v = s[j][t][e];
-              v *= sc[t][e & 1];
-              if (p.cap_out != 0.f) v = capped(v, p.cap_out, p.cap_inv);
-            }
-            if (edge) {
-              const int ka = key0 + 16 * j + g, kc = ka + 8;
-              if (walk.span.hidden(ka)) s[j][t][0] = s[j][t][1] = -INFINITY;
-              if (walk.span.hidden(kc)) s[j][t][2] = s[j][t][3] = -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) grow |= s[j][t][e] > m[t][e & 1];
           }
-        if (__any_sync(0xffffffffu, grow)) {
+          uint32_t pb[kBlocks][NT][2], pl[kBlocks][NT][2];  // the weights' two terms
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float alpha[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float x = m[t][i];
+              const float sub = m[t][i] == -INFINITY ? 0.f : m[t][i];
 #pragma unroll
-              for (int j = 0; j < kBlocks; ++j) x = fmaxf(x, fmaxf(s[j][t][i], s[j][t][i + 2]));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              alpha[i] = x == -INFINITY ? 0.f : fast_exp2(m[t][i] - x);
-              m[t][i] = x;
-              l[t][i] *= alpha[i];
+              for (int j = 0; j < kBlocks; ++j) {
+                s[j][t][i] = fast_exp2(s[j][t][i] - sub + kShift);
+                s[j][t][i + 2] = fast_exp2(s[j][t][i + 2] - sub + kShift);
+                l[t][i] += s[j][t][i] + s[j][t][i + 2];
+              }
             }
+            // P^T as the B operand of O^T = V^T P^T: rows = keys, columns = heads
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j) {
+              const float* v = s[j][t];
+              if (kBf16) {
+                const uint32_t x0 = pack_bf16(v[0], v[1]), x1 = pack_bf16(v[2], v[3]);
+                pb[j][t][0] = movm_t(x0);
+                pb[j][t][1] = movm_t(x1);
+                pl[j][t][0] = movm_t(pack_bf16(v[0] - bf16_lo(x0), v[1] - bf16_hi(x0)));
+                pl[j][t][1] = movm_t(pack_bf16(v[2] - bf16_lo(x1), v[3] - bf16_hi(x1)));
+              } else {
+                const uint32_t x0 = pack_f16(v[0], v[1]), x1 = pack_f16(v[2], v[3]);
+                pb[j][t][0] = movm_t(x0);
+                pb[j][t][1] = movm_t(x1);
+                pl[j][t][0] = movm_t(pack_f16(v[0] - f16_lo(x0), v[1] - f16_hi(x0)));
+                pl[j][t][1] = movm_t(pack_f16(v[2] - f16_lo(x1), v[3] - f16_hi(x1)));
+              }
+            }
+          }
+          // ---- O^T += V^T P^T
+          if (!kFp8) {
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t a[4];
+                ldsm4_t(a, vb + blk[j] + col(v_row, 2 * i + v_sel));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  mma<kBf16>(o[t][i], a, pb[j][t][0], pb[j][t][1]);
+                  mma<kBf16>(o[t][i], a, pl[j][t][0], pl[j][t][1]);
+                }
+              }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t w[4];
+                ldsm4_t(w, vb + blk[j] + col(v_row, 2 * k + v_sel));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  // two keys of two neighbouring elements -> the two keys of each element
+                  const uint32_t lo = __byte_perm(w[2 * i], 0u, 0x3120), hi = __byte_perm(w[2 * i + 1], 0u, 0x3120);
+                  const uint32_t a[4] = {e4m3_to_f16x2(lo & 0xffffu), e4m3_to_f16x2(lo >> 16), e4m3_to_f16x2(hi & 0xffffu),
+                                         e4m3_to_f16x2(hi >> 16)};
+#pragma unroll
+                  for (int t = 0; t < NT; ++t) {
+                    mma<false>(o[t][2 * k + i], a, pb[j][t][0], pb[j][t][1]);
+                    mma<false>(o[t][2 * k + i], a, pl[j][t][0], pl[j][t][1]);
+                  }
+                }
+              }
+          }
+          if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
+        st += S::kGroups;
+        if (st >= S::kStages) {
+          st = grp;
+          ph ^= 1;
+        }
+      }
+      // ---- join the warps: (m, l) and o as they are, put together by the reading threads ----
+      float sum[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sum[t][i] = l[t][i];
+          sum[t][i] += __shfl_xor_sync(0xffffffffu, sum[t][i], 4);
+          sum[t][i] += __shfl_xor_sync(0xffffffffu, sum[t][i], 8);
+          sum[t][i] += __shfl_xor_sync(0xffffffffu, sum[t][i], 16);
+        }
+      if (first && seg > 1) named_bar_sync(1, kWarps * 32);  // the last unit has been read
+      if (!first) {
+        // What this warp has put there before joins o.
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (8 * t + c2 >= heads) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float was = sm.m[warp][8 * t + c2 + h], f = was == -INFINITY ? 0.f : fast_exp2(was - m[t][h]);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[t][i][e] *= alpha[e & 1];
-          }
-        }
-        uint32_t pb[kBlocks][NT][2], pl[kBlocks][NT][2];  // the weights' two terms
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float sub = m[t][i] == -INFINITY ? 0.f : m[t][i];
-#pragma unroll
-            for (int j = 0; j < kBlocks; ++j) {
-              s[j][t][i] = fast_exp2(s[j][t][i] - sub + kShift);
-              s[j][t][i + 2] = fast_exp2(s[j][t][i + 2] - sub + kShift);
-              l[t][i] += s[j][t][i] + s[j][t][i + 2];
-            }
-          }
-          // P^T as the B operand of O^T = V^T P^T: rows = keys, columns = heads
-#pragma unroll
-          for (int j = 0; j < kBlocks; ++j) {
-            const float* v = s[j][t];
-            if (kBf16) {
-              const uint32_t x0 = pack_bf16(v[0], v[1]), x1 = pack_bf16(v[2], v[3]);
-              pb[j][t][0] = movm_t(x0);
-              pb[j][t][1] = movm_t(x1);
-              pl[j][t][0] = movm_t(pack_bf16(v[0] - bf16_lo(x0), v[1] - bf16_hi(x0)));
-              pl[j][t][1] = movm_t(pack_bf16(v[2] - bf16_lo(x1), v[3] - bf16_hi(x1)));
-            } else {
-              const uint32_t x0 = pack_f16(v[0], v[1]), x1 = pack_f16(v[2], v[3]);
-              pb[j][t][0] = movm_t(x0);
-              pb[j][t][1] = movm_t(x1);
-              pl[j][t][0] = movm_t(pack_f16(v[0] - f16_lo(x0), v[1] - f16_hi(x0)));
-              pl[j][t][1] = movm_t(pack_f16(v[2] - f16_lo(x1), v[3] - f16_hi(x1)));
-            }
-          }
-        }
-        // ---- O^T += V^T P^T
-        if (!kFp8) {
-#pragma unroll
-          for (int j = 0; j < kBlocks; ++j)
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              uint32_t a[4];
-              ldsm4_t(a, vb + blk[j] + col(v_row, 2 * i + v_sel));
-#pragma unroll
-              for (int t = 0; t < NT; ++t) {
-                mma<kBf16>(o[t][i], a, pb[j][t][0], pb[j][t][1]);
-                mma<kBf16>(o[t][i], a, pl[j][t][0], pl[j][t][1]);
+              for (int e = h; e < 4; e += 2) {
+                const int d = kFp8 ? 16 * i + 2 * g + (e >> 1) : 16 * i + g + 8 * (e >> 1);
+                o[t][i][e] = fmaf(sm.o[warp][8 * t + c2 + h][d], f, o[t][i][e]);
               }
-            }
-        } else {
-#pragma unroll
-          for (int j = 0; j < kBlocks; ++j)
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              uint32_t w[4];
-              ldsm4_t(w, vb + blk[j] + col(v_row, 2 * k + v_sel));
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                // two keys of two neighbouring elements -> the two keys of each element
-                const uint32_t lo = __byte_perm(w[2 * i], 0u, 0x3120), hi = __byte_perm(w[2 * i + 1], 0u, 0x3120);
-                const uint32_t a[4] = {e4m3_to_f16x2(lo & 0xffffu), e4m3_to_f16x2(lo >> 16), e4m3_to_f16x2(hi & 0xffffu),
-                                       e4m3_to_f16x2(hi >> 16)};
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                  mma<false>(o[t][2 * k + i], a, pb[j][t][0], pb[j][t][1]);
-                  mma<false>(o[t][2 * k + i], a, pl[j][t][0], pl[j][t][1]);
-                }
-              }
-            }
+          }
         }
-        if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
       }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (8 * t + c2 >= heads) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (g == 0) {
+            sm.m[warp][8 * t + c2 + i] = m[t][i];
+            sm.l[warp][8 * t + c2 + i] = sum[t][i];
+          }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // element of the head dim in row g (+ 8) of this 16-row block
+            const int d = kFp8 ? 16 * i + 2 * g + (e >> 1) : 16 * i + g + 8 * (e >> 1);
+            sm.o[warp][8 * t + c2 + (e & 1)][d] = o[t][i][e];
+          }
+      }
+      if (end == walk.t_end) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
-      st += S::kGroups;
-      if (st >= S::kStages) {
-        st = grp;
-        ph ^= 1;
-      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
     }
     skip = tile - walk.t_end;
-
-    // ---- join the warps: (m, l) and o as they are, put together by the reading threads ----
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
-        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
-        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
-      }
     const bool whole = walk.whole();
     const int slot = seg == 1 ? 0 : 1;
     const int64_t piece = ((int64_t)blockIdx.x * 2 + slot) * kRows;
-    if (seg > 1) named_bar_sync(1, kWarps * 32);  // the last unit has been read
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (8 * t + c2 >= heads) continue;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (g == 0) {
-          sm.m[warp][8 * t + c2 + i] = m[t][i];
-          sm.l[warp][8 * t + c2 + i] = l[t][i];
-        }
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // element of the head dim in row g (+ 8) of this 16-row block
-          const int d = kFp8 ? 16 * i + 2 * g + (e >> 1) : 16 * i + g + 8 * (e >> 1);
-          sm.o[warp][8 * t + c2 + (e & 1)][d] = o[t][i][e];
-        }
-    }
     named_bar_sync(1, kWarps * 32);
     for (int i = threadIdx.x; i < heads * (D / 2); i += kWarps * 32) {
       const int r = i / (D / 2), d = (i % (D / 2)) * 2;

@@ -495,6 +495,9 @@ gqa_status nvfp4_paged_norm_append_t(const gqa_tensor* q, const gqa_tensor* k, c
  * meets V as two 16-bit terms of the pages' type (f16 for E4M3 ones), 22 bits in
  * f16 and 16 in bf16; f16 terms are exact to 2^-39 of the largest weight at best.
  * A bf16 query over E4M3 pages is exact to 2^-40 of its row's largest element.
+ * The accumulators of the product with V cut sums off; they take 65536 tokens at
+ * most (32768 at d = 256; about 5e-5 of sum w |V| by then) before they are added up
+ * with rounding, so that the error does not grow with the length.
  *
  * A sequence of length 0 produces a zero row and lse = -infinity.  Slots outside
  * the visible tokens may hold anything, NaN too; an infinity among the visible
