@@ -33,7 +33,7 @@ extern "C" {
 
 const char* gqa_last_error(void) { return t_last_error.c_str(); }
 
-int gqa_version(void) { return 500; }  // 0.5.0: drafted tokens over paged caches, head norms, sinks
+int gqa_version(void) { return 501; }  // 0.5.1: long sums of the paged attentions, norms over f32's whole range
 
 namespace {
 gqa_status decode_impl(const void* q, const void* kv, const int32_t* seq_lens, void* out, int64_t batch,

@@ -13,8 +13,8 @@
 // NVFP4: sf = E4M3(amax / 6) of a 16-element block, codes = E2M1(x / sf), what f32
 // divisions give, so a plain f32 evaluation gives the same bits.
 // With a norm (kNorm), a head x becomes x * rsqrt(sum x^2 / D + eps) * w in f32 before
-// its rotation, not rounded in between (8192 tokens of 32 + 8 + 8 heads of 128 in bf16: 41.1 us,
-// 5.0 TB/s; 39.9 with the norm's arithmetic left out of that instance).
+// its rotation, not rounded in between (8192 tokens of 32 + 8 + 8 heads of 128, time in a graph of 21 calls: to bf16 pages
+// 38.7 us, 5.3 TB/s, 36.3 without a norm; to E4M3 ones 37.9 and 34.3; to NVFP4 ones 39.5 and 30.9; one token 3.6-4.0 and 3.2).
 //
 // What bounds it: HBM for prompts (each input read once, each output written
 // once, 3 flops per rotated element), latency for single tokens -- a chain of

@@ -46,8 +46,8 @@
 //
 // Measured on GB300 (time in a graph): 64 sequences of up to 8192 tokens, 32/8 heads,
 // bf16: 155 us, 6.94 TB/s; 20 of 8192: 99 us, 6.75 TB/s; 48 of up to 16001, 64/8 heads,
-// E4M3: 126 us, 6.27 TB/s; 8 of 131072, f16: 585 us, 7.34 TB/s; the 48 under a window of
-// 4096 with 4 sinks: 68 us.
+// E4M3: 126 us, 6.27 TB/s; 8 of 131072, f16: 583 us, 7.37 TB/s; the 48 under a window of
+// 4096 with 4 sinks: 64 us.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

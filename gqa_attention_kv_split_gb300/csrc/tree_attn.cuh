@@ -16,10 +16,11 @@
 // weights as TMEM operand.  With 128 rows or fewer a tile of 128 tokens (64 KB in bf16, head
 // dim 128: 1.5 us of an SM's share of HBM) keeps the tensor pipe busy for 0.8 us, however few
 // rows there are, and the softmax for less:
-//  * Copies.  With 64 (32) rows or fewer each row stands in the M dimension twice (four times), if there are tiles enough,
+//  * Copies.  With 64 (32) rows or fewer each row stands in the M dimension twice (four times; twice too at head dim 256,
+//    whose tiles have two parts), if there is more than one tile,
 //    and each copy weighs a half (a quarter) of a tile's tokens, with zeros in P for the
 //    others: the warps share the softmax evenly, as independent (m, l, o) that join at the end.
-//  * S in two TMEM buffers: S of the next tile is computed while the softmax works on this one;
+//  * S in two TMEM buffers (three at head dim 64): S of the next tile is computed while the softmax works on this one;
 //    P overwrites the S it came from (32 tokens' weights: 16 columns of their first terms, 16
 //    of their second ones).
 //  * Weights enter the product with V as two terms of 16 bits (22 bits in f16, 16 in bf16).
@@ -38,9 +39,10 @@
 //    exactly.
 //  * Every wait is bounded; a block whose wait expires drains what it started and leaves.
 //
-// Measured on GB300 (time in a graph): 16 sequences of 16384 tokens, 32/8 heads of 128, bf16, 8 drafts: 167 us,
-// 6.4 TB/s; 64 drafts: 293 us, 935 TFLOP/s; 8 of 65536, f16, 64 drafts: 555 us, 990 TFLOP/s; 48 of up to 16001, 64/8
-// heads, E4M3, up to 16 drafts: 237 us, 3.4 TB/s; one of 2048 tokens, 8 drafts: 17 us.
+// Measured on GB300 (time in a graph of 21 calls): 16 sequences of 16384 tokens, 32/8 heads of 128, bf16, 8 drafts: 164 us,
+// 6.55 TB/s; 64 drafts: 294 us, 935 TFLOP/s; 8 of 65536, f16, 64 drafts: 617-630 us at the power limit, 570 before it, 965
+// TFLOP/s; 48 of up to 16001, 64/8 heads, E4M3, up to 16 drafts: 233 us, 3.4 TB/s; 200 of up to 600, bf16, up to 8 drafts: 93 us;
+// one of 2048 tokens, 8 drafts: 13.6 us.  (Times beside single steps below are of graphs of one call, which take 3 us more.)
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -1115,8 +1117,8 @@ __device__ __forceinline__ void load_l2(const float* p, float (&v)[kN]) {
 // Joins the pieces of the units that lie in several blocks' shares, in the order of their
 // tiles: a warp per row.  Up to 32 pieces' maxima and sums come at once, a lane each, and their
 // outputs kBatch at a time, none of which waits for another.  Two at a time where units have few pieces (16
-// sequences of 16384 tokens, 32 drafts, head dim 64: 133.5 us; 135 with 8, 141 with 16), eight for long
-// lists (one of 2048 tokens, 20 pieces a unit: 16.6 us; 18.7 with 2).
+// sequences of 16384 tokens, 32 drafts, head dim 64, graphs of 21 calls: 132.2 us; 134.2 with 8), eight for long
+// lists (one of 2048 tokens, up to 14 pieces a unit: 13.7 us, 15.1 with 2; of 8192: 18.8, 20.2).
 template <int D, bool kQBf16, int kBatch>
 __global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ Params p) {
   constexpr int kN = D / 32;
